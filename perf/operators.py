@@ -302,7 +302,7 @@ def run_own(s, op):
 def outputs(s, op):
     pool = (s["k"], s["v"], s["k_scale"], s["v_scale"])
     meta = (s["page_table"], s["seq_lens"], s["refcount"])
-    return {"append": pool, "copy": pool, "fork": pool + meta, "turnover": meta, "compact": pool + meta}[op]
+    return {"append": (s["k"], s["k_scale"], s["v"], s["v_scale"]), "copy": pool, "fork": pool + meta, "turnover": meta, "compact": pool + meta}[op]
 
 
 def token_rows(s):
