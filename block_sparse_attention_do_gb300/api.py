@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "libnsa.so")
 
 NSA_OK = 0
 STATUS = {0: "NSA_OK", 1: "NSA_ERR_INVALID_ARG", 2: "NSA_ERR_UNSUPPORTED", 3: "NSA_ERR_BAD_INDEX",
-          4: "NSA_ERR_DEVICE_TIMEOUT", 5: "NSA_ERR_CUDA", 6: "NSA_ERR_WORKSPACE"}
+          4: "NSA_ERR_DEVICE_TIMEOUT", 5: "NSA_ERR_CUDA", 6: "NSA_ERR_WORKSPACE", 7: "NSA_ERR_CACHE_FULL"}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 LAYOUT_BHTD, LAYOUT_THD = 0, 1
 
@@ -34,6 +34,8 @@ SYMBOLS = (
     "nsa_causal_fwd_workspace_size", "nsa_causal_bwd_workspace_size", "nsa_causal_fwd", "nsa_causal_bwd",
     "nsa_select_workspace_size", "nsa_compress_keys_mean", "nsa_block_scores", "nsa_select_topk",
     "nsa_sel_fwd_workspace_size", "nsa_sel_bwd_workspace_size",
+    "nsa_cache_workspace_size", "nsa_cache_reserve", "nsa_cache_free", "nsa_cache_fork", "nsa_cache_copy",
+    "nsa_cache_compact", "nsa_cache_append", "nsa_cache_fwd_workspace_size", "nsa_cache_fwd",
 )
 
 
@@ -46,6 +48,14 @@ class Problem(C.Structure):
                 ("dq_stride", C.c_int64 * 3), ("dkv_stride", C.c_int64 * 3),
                 ("Tk", C.c_int32), ("total_keys", C.c_int32), ("bottom_right", C.c_int32),
                 ("reserved2", C.c_int32)]
+
+
+class CacheStruct(C.Structure):
+    """nsa_cache."""
+    _fields_ = [("num_pages", C.c_int32), ("Hkv", C.c_int32), ("D", C.c_int32), ("block_size", C.c_int32),
+                ("rows", C.c_int32), ("max_pages", C.c_int32), ("stride", C.c_int64 * 3),
+                ("k", C.c_void_p), ("v", C.c_void_p), ("k_scale", C.c_void_p), ("v_scale", C.c_void_p),
+                ("page_table", C.c_void_p), ("seq_lens", C.c_void_p), ("refcount", C.c_void_p)]
 
 
 def _bht_strides(t, thd):
@@ -141,6 +151,18 @@ def lib() -> C.CDLL:
         L.nsa_compress_keys_mean.argtypes = [pp] + [_P] * 3 + [_P]
         L.nsa_block_scores.argtypes = [pp] + [_P] * 4 + [_P, C.c_size_t, _P]
         L.nsa_select_topk.argtypes = [pp] + [_P] * 3 + [_P]
+        pc = C.POINTER(CacheStruct)
+        L.nsa_cache_workspace_size.restype = C.c_size_t
+        L.nsa_cache_workspace_size.argtypes = [pc]
+        L.nsa_cache_reserve.argtypes = [pc, _P] + [_P, C.c_size_t, _P]
+        L.nsa_cache_free.argtypes = [pc, _P, C.c_int32] + [_P, C.c_size_t, _P]
+        L.nsa_cache_fork.argtypes = [pc, _P, _P, C.c_int32] + [_P, C.c_size_t, _P]
+        L.nsa_cache_copy.argtypes = [pc, _P, _P, C.c_int32] + [_P, C.c_size_t, _P]
+        L.nsa_cache_compact.argtypes = [pc] + [_P, C.c_size_t, _P]
+        L.nsa_cache_append.argtypes = [pp, pc] + [_P] * 3 + [_P, C.c_size_t, _P]
+        L.nsa_cache_fwd_workspace_size.restype = C.c_size_t
+        L.nsa_cache_fwd_workspace_size.argtypes = [pp, pc, C.c_int32]
+        L.nsa_cache_fwd.argtypes = [pp, pc, C.c_int32] + [_P] * 6 + [_P, C.c_size_t, _P]
         for name in SYMBOLS:
             fn = getattr(L, name)
             if fn.restype is C.c_int:  # default restype: status enums
@@ -543,3 +565,227 @@ def select_topk(scores, block_size, S, cu_seqlens=None, max_seqlen=None, stream=
     _check(lib().nsa_select_topk(C.byref(p), _ptr(cu_seqlens), _ptr(scores), _ptr(idx), _stream(stream)),
            "nsa_select_topk")
     return idx
+
+
+# ---------------------------------------------------------------- paged 8-bit cache
+# Serving (include/nsa.h states the layout and every rule): a cache of pages
+# in e4m3, one scale per page and kv head.  A step of a served batch is
+# cache_reserve (pages for the new tokens), cache_append (their keys and
+# values) and cache_fwd (their attention).
+
+
+def _need(ok, what):
+    if not ok:
+        raise NsaError(1, what)
+
+
+def _int32(t, what, device, shape=None):
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.device == device and
+          (shape is None or tuple(t.shape) == tuple(shape)), f"{what}: a dense int32 tensor on the cache's device is wanted")
+    return t
+
+
+class KVCache:
+    """The tensors of one paged 8-bit cache (nsa_cache), all on one device:
+    k, v float8_e4m3fn [num_pages, Hkv, block_size, D] (strided, D
+    contiguous), k_scale, v_scale float32 [num_pages, Hkv], page_table int32
+    [rows, max_pages], seq_lens int32 [rows], refcount int32 [num_pages]
+    (None: the caller manages pages itself; no reserve, free, fork or
+    compact).  `ws` is the workspace of the calls that change the cache;
+    get_error(cache.ws) reads what the last of them found."""
+
+    def __init__(self, k, v, k_scale, v_scale, page_table, seq_lens, refcount=None):
+        _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.float8_e4m3fn,
+              "KVCache: k and v are float8_e4m3fn [num_pages, Hkv, block_size, D]")
+        _need(k.stride(3) == 1 and k.stride() == v.stride(), "KVCache: k and v have the same strides, D contiguous")
+        dev = k.device
+        for s in (k_scale, v_scale):
+            _need(s.dtype == torch.float32 and s.is_contiguous() and tuple(s.shape) == tuple(k.shape[:2]) and s.device == dev,
+                  "KVCache: scales are dense float32 [num_pages, Hkv]")
+        _need(v.device == dev and page_table.dim() == 2, "KVCache: one device, page_table [rows, max_pages]")
+        _int32(page_table, "KVCache: page_table", dev)
+        _int32(seq_lens, "KVCache: seq_lens", dev, (page_table.shape[0],))
+        if refcount is not None:
+            _int32(refcount, "KVCache: refcount", dev, (k.shape[0],))
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.page_table, self.seq_lens, self.refcount = page_table, seq_lens, refcount
+        self.device = dev
+        s = CacheStruct(k.shape[0], k.shape[1], k.shape[3], k.shape[2], page_table.shape[0], page_table.shape[1])
+        if not k.is_contiguous():
+            s.stride[:] = k.stride()[:3]
+        s.k, s.v, s.k_scale, s.v_scale = k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()
+        s.page_table, s.seq_lens = page_table.data_ptr(), seq_lens.data_ptr()
+        s.refcount = refcount.data_ptr() if refcount is not None else None
+        self.struct, self.ref = s, C.byref(s)
+        n = int(lib().nsa_cache_workspace_size(self.ref))
+        if n == 0:
+            raise NsaError(1, "nsa_cache_workspace_size")
+        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        self._problems = {}
+
+    def problem(self, x, S, scale, cu_seqlens, max_seqlen, selection, query):
+        """The nsa_problem of a call on x (queries, or new keys), and the
+        attention's workspace size; remembered by shape."""
+        key = (x.shape, x.stride(), x.dtype, S, scale, max_seqlen, cu_seqlens is None, selection, query)
+        got = self._problems.get(key)
+        if got is None:
+            s = self.struct
+            _need(x.dtype in DTYPE and x.shape[-1] == s.D, "cache: float32 or bfloat16 rows of the cache's head dimension")
+            Hq = x.shape[1]
+            if cu_seqlens is None:
+                p = problem(x.shape[0], Hq, s.Hkv, x.shape[2], s.D, s.block_size, S, x.dtype, scale=scale)
+            else:
+                p = problem(s.rows, Hq, s.Hkv, max(1, max_seqlen), s.D, s.block_size, S, x.dtype, layout=LAYOUT_THD,
+                            total_tokens=x.shape[0], scale=scale)
+            n = 0
+            if query:
+                declare_strides(p, cu_seqlens is not None, q=x)
+                n = int(lib().nsa_cache_fwd_workspace_size(C.byref(p), self.ref, int(selection)))
+                if n == 0:
+                    raise NsaError(1, "nsa_cache_fwd_workspace_size")
+            else:
+                declare_strides(p, cu_seqlens is not None, k=x)
+            if len(self._problems) >= 256:
+                self._problems.clear()
+            got = self._problems[key] = (p, C.byref(p), n)
+        return got
+
+
+def make_cache(num_pages, Hkv, D, block_size, rows, max_pages, device="cuda"):
+    """An empty KVCache."""
+    dev = torch.device(device)
+    shape = (num_pages, Hkv, block_size, D)
+    i32 = dict(dtype=torch.int32, device=dev)
+    return KVCache(torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+                   torch.zeros(shape, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
+                   torch.ones(num_pages, Hkv, device=dev), torch.ones(num_pages, Hkv, device=dev),
+                   torch.full((rows, max_pages), -1, **i32), torch.zeros(rows, **i32), torch.zeros(num_pages, **i32))
+
+
+def _elsewhere(cache, stream):
+    """Whether a call has to leave the current device or stream for the
+    cache's device and the caller's stream."""
+    return stream is not None or cache.device.index != torch.cuda.current_device()
+
+
+def _there(cache, stream):
+    """The caller's stream (else the device's current one) as the context of
+    a call, so that what it allocates belongs to that stream."""
+    return torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream)
+
+
+def _cu(cache, x, cu_seqlens, max_seqlen):
+    """The longest of the new tokens' runs, the packed offsets checked."""
+    if cu_seqlens is None:
+        _need(x.dim() == 4 and x.shape[0] == cache.struct.rows, "cache: x is [rows, heads, T, D], or packed with cu_seqlens")
+        return None
+    _need(x.dim() == 3, "cache: packed x is [total, heads, D]")
+    _int32(cu_seqlens, "cache: cu_seqlens", cache.device, (cache.struct.rows + 1,))
+    return int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if max_seqlen is None else int(max_seqlen)
+
+
+def cache_reserve(cache, n_new, stream=None):
+    """Row b of the cache grows by n_new[b] tokens (int32 [rows]): pages from
+    the pool, lowest ids first, and seq_lens.  All rows or, with too few free
+    pages (NSA_ERR_CACHE_FULL in cache.ws), none."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_reserve(cache, n_new)
+    _int32(n_new, "cache_reserve: n_new", cache.device, (cache.struct.rows,))
+    _check(lib().nsa_cache_reserve(cache.ref, n_new.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _stream()),
+           "nsa_cache_reserve")
+
+
+def cache_free(cache, rows, stream=None):
+    """The listed rows (int32) give back their pages and become empty."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_free(cache, rows)
+    _int32(rows, "cache_free: rows", cache.device)
+    _check(lib().nsa_cache_free(cache.ref, rows.data_ptr(), rows.numel(), cache.ws.data_ptr(), cache.ws.numel(),
+                                _stream()), "nsa_cache_free")
+
+
+def cache_fork(cache, src, dst, stream=None):
+    """Row dst[i] (int32) gives back its pages and continues row src[i]: full
+    blocks shared, the last, partly filled one copied."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_fork(cache, src, dst)
+    _int32(src, "cache_fork: src", cache.device)
+    _int32(dst, "cache_fork: dst", cache.device, src.shape)
+    _check(lib().nsa_cache_fork(cache.ref, src.data_ptr(), dst.data_ptr(), src.numel(), cache.ws.data_ptr(),
+                                cache.ws.numel(), _stream()), "nsa_cache_fork")
+
+
+def cache_copy(cache, src, dst, stream=None):
+    """Pages src[i] (int32) are copied to pages dst[i], codes and scales."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_copy(cache, src, dst)
+    _int32(src, "cache_copy: src", cache.device)
+    _int32(dst, "cache_copy: dst", cache.device, src.shape)
+    _check(lib().nsa_cache_copy(cache.ref, src.data_ptr(), dst.data_ptr(), src.numel(), cache.ws.data_ptr(),
+                                cache.ws.numel(), _stream()), "nsa_cache_copy")
+
+
+def cache_compact(cache, stream=None):
+    """Pages in use move to the front of the pool; table and counts follow."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_compact(cache)
+    _check(lib().nsa_cache_compact(cache.ref, cache.ws.data_ptr(), cache.ws.numel(), _stream()), "nsa_cache_compact")
+
+
+def cache_append(cache, k, v, cu_seqlens=None, max_seqlen=None, stream=None):
+    """The new tokens' keys and values ([rows, Hkv, T, D], or packed
+    [total, Hkv, D] with cu_seqlens) go, rounded to e4m3, to the last
+    positions of their rows; seq_lens counts them already (cache_reserve)."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_append(cache, k, v, cu_seqlens, max_seqlen)
+    longest = _cu(cache, k, cu_seqlens, max_seqlen)
+    _need(k.shape == v.shape and k.dtype == v.dtype and k.shape[1] == cache.struct.Hkv and
+          k.device == v.device == cache.device, "cache_append: k and v alike, on the cache's device, with its heads")
+    _same_strides(k, v, "k and v")
+    if k.numel() == 0:
+        return
+    _, p, _ = cache.problem(k, 1, None, cu_seqlens, longest, False, False)
+    _check(lib().nsa_cache_append(p, cache.ref, cu_seqlens.data_ptr() if cu_seqlens is not None else None, k.data_ptr(),
+                                  v.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _stream()), "nsa_cache_append")
+
+
+def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=None, window=None, sinks=None, ws=None,
+              stream=None):
+    """Attention of the rows' last tokens ([rows, Hq, T, D], or packed
+    [total, Hq, D] with cu_seqlens) over the cache: all of it, with `window`
+    each token's latest keys, with `block_idx` the selected blocks; `sinks` as
+    for sel_fwd.  Returns (o, lse).  A ws of the caller's
+    (nsa_cache_fwd_workspace_size) holds the error word that get_error reads;
+    without one each call has its own."""
+    if _elsewhere(cache, stream):
+        with _there(cache, stream):
+            return cache_fwd(q, cache, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)
+    longest = _cu(cache, q, cu_seqlens, max_seqlen)
+    _need(q.device == cache.device, "cache_fwd: q is on the cache's device")
+    S = 1
+    if block_idx is not None:
+        _need(window is None and sinks is None, "cache_fwd: a window or sinks go with the whole cache only")
+        S = block_idx.shape[-1]
+        head = (q.shape[0], cache.struct.Hkv) + ((q.shape[2],) if cu_seqlens is None else ())
+        _int32(block_idx, "cache_fwd: block_idx", cache.device, head + (S,))
+    if sinks is not None:
+        _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and tuple(sinks.shape) == (q.shape[1],) and
+              sinks.device == cache.device, "cache_fwd: sinks are float32 [Hq]")
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    if q.numel() == 0:
+        return o, lse
+    _, p, n = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
+    if ws is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
+                               block_idx.data_ptr() if block_idx is not None else None,
+                               sinks.data_ptr() if sinks is not None else None, q.data_ptr(), o.data_ptr(),
+                               lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream()), "nsa_cache_fwd")
+    return o, lse

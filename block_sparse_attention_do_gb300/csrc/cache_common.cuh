@@ -1,0 +1,63 @@
+// cache_common.cuh -- the paged 8-bit key/value cache on the device: its
+// geometry, and the e4m3 conversions that its kernels share.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "nsa_common.cuh"
+
+namespace nsa {
+
+// Device-side view of an nsa_cache.  A page is one block of bs tokens; the
+// codes of (page p, head h, token i of the page) start at p*sp + h*sh + i*st
+// bytes (one byte per code), the D codes of a token are contiguous.
+struct Cache {
+    int pages, Hkv, D, bs, rows, cols;
+    int64_t sp, sh, st;
+    uint8_t *k, *v;
+    float *ks, *vs;  // [pages, Hkv]
+    int *table;      // [rows, cols], -1: no page
+    int *lens;       // [rows]
+    int *ref;        // [pages] (nullptr: the caller keeps no counts)
+};
+
+// Workspace of the page operations: header, then three arrays of one int per
+// page and two of one int per row.
+struct CacheWs {
+    int *err;     // nsa_status recorded by the device
+    int *npairs;  // pages to copy
+    int *p0, *p1, *p2;
+    int *r0, *r1;
+};
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
+
+// The least power of two s with amax <= 448 s, at least 2^-100 (amax finite,
+// >= 0): 448 = 1.75 * 2^8, so with amax = m * 2^e, 1 <= m < 2, s is 2^(e-8)
+// for m <= 1.75 and 2^(e-7) above.  A power of two makes x / s exact, so a
+// code is x rounded once, and makes a later rescaling exact but for codes
+// that fall below e4m3's normal range.
+__device__ __forceinline__ float e4m3_scale(float amax)
+{
+    const uint32_t u = __float_as_uint(fmaxf(amax, kE4m3Max * kScaleFloor));
+    const int e = (int)(u >> 23) - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return __uint_as_float((uint32_t)e << 23);
+}
+
+// two floats to two codes (lo in the low byte): nearest, ties to even,
+// beyond +-448 (infinities too) to +-448; NaN stays NaN
+__device__ __forceinline__ uint32_t e4m3_pack2(float lo, float hi)
+{
+    return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+// two codes (low 16 bits) to a pair of halves: exact (e4m3 is a subset)
+__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+
+}  // namespace nsa

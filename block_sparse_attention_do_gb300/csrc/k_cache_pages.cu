@@ -1,0 +1,528 @@
+// k_cache_pages.cu -- the pages of the cache: reserving them for rows that
+// grow, freeing, sharing between forked rows, copying and compacting.
+//
+// The pool's whole state is one reference count per page (0: free), the
+// page table and the rows' lengths.  "The lowest free pages first" makes the
+// choice of pages a function of that state alone, whatever order the threads
+// run in.  The metadata of a call is one cluster of 8 CTAs: the counts are
+// read by all 4096 threads at once, the clusters' barriers stand between the
+// steps, and the calls need no host round trip.  What bounds it is the chain
+// of those steps (a few dependent reads each), not the bytes: 0.26 MB of
+// counts for 65,536 pages.  The pages' contents move in a second, wide launch
+// that is bound by memory bandwidth.
+#include <cooperative_groups.h>
+
+#include "cache_common.cuh"
+#include "launch.h"
+
+namespace cg = cooperative_groups;
+
+namespace nsa {
+
+namespace {
+
+constexpr int kCluster = 8;      // CTAs of a metadata call (the portable cluster size)
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kAllWarps = kCluster * kWarps;
+
+struct Where {
+    int rank, warp, lane;  // CTA of the cluster, warp of the cluster, lane
+};
+__device__ __forceinline__ Where where(const cg::cluster_group &cl)
+{
+    return Where{(int)cl.block_rank(), (int)cl.block_rank() * kWarps + (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31)};
+}
+
+// blocks of `bs` that hold len tokens
+__device__ __forceinline__ int blocks_of(int len, int bs) { return (int)(((int64_t)len + bs - 1) / bs); }
+
+// Each warp of the cluster owns one run of pages: count() counts those that
+// pred() names, scan() turns the cluster's counts into the number before the
+// calling warp's run and the total.
+struct Runs {
+    int begin, end;
+    __device__ __forceinline__ Runs(const Cache &c, int warp)
+    {
+        const int per = ((c.pages + kAllWarps - 1) / kAllWarps + 31) & ~31;
+        begin = min(c.pages, warp * per);
+        end = min(c.pages, begin + per);
+    }
+    template <typename P> __device__ __forceinline__ int count(int lane, P pred) const
+    {
+        int n = 0;
+#pragma unroll 8
+        for (int p = begin + lane; p < end; p += 32)
+            n += pred(p) ? 1 : 0;
+        return __reduce_add_sync(0xffffffffu, n);
+    }
+};
+
+// every warp's count into every CTA's table (the cluster synchronises after)
+__device__ __forceinline__ void share_count(const cg::cluster_group &cl, int *counts, const Where &w, int n)
+{
+    if (w.lane < kCluster)
+        cl.map_shared_rank(counts, w.lane)[w.warp] = n;
+}
+__device__ __forceinline__ void scan_counts(const int *counts, const Where &w, int &before, int &total)
+{
+    int b = 0, t = 0;
+    for (int i = w.lane; i < kAllWarps; i += 32) {
+        t += counts[i];
+        b += i < w.warp ? counts[i] : 0;
+    }
+    before = __reduce_add_sync(0xffffffffu, b);
+    total = __reduce_add_sync(0xffffffffu, t);
+}
+
+// Exclusive prefix over i < n of need(i), by one CTA: out[i], the sum
+// returned to every thread.
+template <typename F> __device__ int64_t cta_prefix(int n, int *out, F need)
+{
+    __shared__ int64_t part[kWarps];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t base = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const int64_t x = i < n ? need(i) : 0;
+        int64_t incl = x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            incl += lane >= o ? y : 0;
+        }
+        if (lane == 31)
+            part[warp] = incl;
+        __syncthreads();
+        int64_t before = base, all = base;
+        for (int k = 0; k < kWarps; ++k) {
+            before += k < warp ? part[k] : 0;
+            all += part[k];
+        }
+        if (i < n)
+            out[i] = (int)min(before + incl - x, (int64_t)INT32_MAX);
+        base = all;
+        __syncthreads();
+    }
+    return base;
+}
+
+// Takes the `total` lowest free pages: order[i] = the i-th, its count 1.
+__device__ __forceinline__ void take_free(const Cache &c, const Runs &r, int lane, int before, int total, int *order)
+{
+    for (int p0 = r.begin; p0 < r.end && before < total; p0 += 32) {
+        const int p = p0 + lane;
+        const bool free = p < r.end && __ldcg(c.ref + p) <= 0;
+        const unsigned m = __ballot_sync(0xffffffffu, free);
+        const int nth = before + __popc(m & ((1u << lane) - 1u));
+        if (free && nth < total) {
+            order[nth] = p;
+            c.ref[p] = 1;
+        }
+        before += __popc(m);
+    }
+}
+
+// Gives back the pages of row r (lanes over its columns): true if an entry
+// names no page or a page that nobody holds.
+__device__ __forceinline__ bool release_row(const Cache &c, int r, int lane, bool clear)
+{
+    bool bad = false;
+    for (int col = lane; col < c.cols; col += 32) {
+        int *e = c.table + (int64_t)r * c.cols + col;
+        const int p = *e;
+        if (p >= 0 && p < c.pages) {
+            if (atomicSub(c.ref + p, 1) <= 0) {
+                atomicAdd(c.ref + p, 1);
+                bad = true;
+            }
+        } else if (p != -1)
+            bad = true;
+        if (clear)
+            *e = -1;
+    }
+    return bad;
+}
+
+// ---- reserve: row b grows by n_new[b] tokens; all rows or none ------------
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cache_reserve_kernel(const Cache c, const int *n_new, const CacheWs ws)
+{
+    cg::cluster_group cl = cg::this_cluster();
+    __shared__ int counts[kAllWarps];
+    __shared__ int bad;
+    __shared__ int64_t need_all;
+    const Where w = where(cl);
+    if (threadIdx.x == 0)
+        bad = 0;
+    cl.sync();  // every CTA of the cluster runs from here on: its shared memory may be written
+    auto ok = [&](int b) {
+        const int len = c.lens[b], n = n_new[b];
+        return n >= 0 && len >= 0 && (int64_t)len + n <= (int64_t)c.cols * c.bs;
+    };
+    auto need = [&](int b) {
+        const int len = c.lens[b], n = n_new[b];
+        return ok(b) ? blocks_of(len + n, c.bs) - blocks_of(len, c.bs) : 0;
+    };
+    // every CTA checks every row and knows the sum; CTA 0 writes the offsets
+    for (int b = threadIdx.x; b < c.rows; b += kThreads)
+        if (!ok(b))
+            bad = 1;
+    const Runs run(c, w.warp);
+    share_count(cl, counts, w, run.count(w.lane, [&](int p) { return c.ref[p] <= 0; }));
+    int64_t total;
+    if (w.rank == 0) {
+        total = cta_prefix(c.rows, ws.r1, need);
+        if (threadIdx.x < kCluster)
+            *cl.map_shared_rank(&need_all, threadIdx.x) = total;
+    }
+    cl.sync();
+    total = need_all;
+    int before, free;
+    scan_counts(counts, w, before, free);
+    const bool full = total > free;
+    if (w.rank == 0 && threadIdx.x == 0)
+        *ws.err = bad ? NSA_ERR_BAD_INDEX : full ? NSA_ERR_CACHE_FULL : NSA_OK;
+    if (bad || full)
+        return;  // the same in every CTA: nothing has changed
+    take_free(c, run, w.lane, before, (int)total, ws.p2);
+    cl.sync();
+    for (int b = w.warp; b < c.rows; b += kAllWarps) {
+        const int len = c.lens[b], n = n_new[b];
+        const int have = blocks_of(len, c.bs), want = blocks_of(len + n, c.bs), off = __ldcg(ws.r1 + b);
+        for (int col = have + w.lane; col < want; col += 32)
+            c.table[(int64_t)b * c.cols + col] = __ldcg(ws.p2 + off + col - have);
+        __syncwarp();
+        if (w.lane == 0)
+            c.lens[b] = len + n;
+    }
+}
+
+// Claims: mark[x] = the first list position that names x.  The caller
+// synchronises between the two steps and before it reads.
+__device__ __forceinline__ void claim_clear(const int *list, int n, int limit, int *mark, const Where &w)
+{
+    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads)
+        if (list[i] >= 0 && list[i] < limit)
+            mark[list[i]] = INT32_MAX;
+}
+__device__ __forceinline__ void claim(const int *list, int n, int limit, int *mark, const Where &w, bool by_source)
+{
+    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads)
+        if (list[i] >= 0 && list[i] < limit)
+            atomicMin(mark + list[i], by_source ? -1 : i);
+}
+
+// ---- free: the listed rows give back their pages ---------------------------
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cache_free_kernel(const Cache c, const int *rows, int n, const CacheWs ws)
+{
+    cg::cluster_group cl = cg::this_cluster();
+    const Where w = where(cl);
+    if (w.rank == 0 && threadIdx.x == 0)
+        *ws.err = NSA_OK;
+    claim_clear(rows, n, c.rows, ws.r0, w);
+    cl.sync();
+    claim(rows, n, c.rows, ws.r0, w, false);
+    cl.sync();
+    bool bad = false;
+    for (int i = w.warp; i < n; i += kAllWarps) {
+        const int r = rows[i];
+        if (r < 0 || r >= c.rows || __ldcg(ws.r0 + r) != i) {  // no row, or listed before
+            bad = true;
+            continue;
+        }
+        bad |= release_row(c, r, w.lane, true);
+        if (w.lane == 0)
+            c.lens[r] = 0;
+    }
+    if (bad)
+        set_error(ws.err, NSA_ERR_BAD_INDEX);
+}
+
+// ---- fork: row dst[i] becomes a continuation of row src[i] -----------------
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cache_fork_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
+{
+    cg::cluster_group cl = cg::this_cluster();
+    __shared__ int counts[kAllWarps];
+    __shared__ int64_t tails_all;
+    const Where w = where(cl);
+    if (w.rank == 0 && threadIdx.x == 0) {
+        *ws.err = NSA_OK;
+        *ws.npairs = 0;
+    }
+    claim_clear(src, n, c.rows, ws.r0, w);
+    claim_clear(dst, n, c.rows, ws.r0, w);
+    cl.sync();
+    claim(dst, n, c.rows, ws.r0, w, false);
+    claim(src, n, c.rows, ws.r0, w, true);
+    cl.sync();
+    bool bad = false;
+    for (int i = w.warp; i < n; i += kAllWarps) {
+        const int s = src[i], d = dst[i];
+        if (s < 0 || s >= c.rows || d < 0 || d >= c.rows || __ldcg(ws.r0 + d) != i) {
+            bad = true;
+            continue;
+        }
+        const int len = c.lens[s];
+        if (len < 0 || (int64_t)len > (int64_t)c.cols * c.bs) {
+            bad = true;
+            continue;
+        }
+        for (int col = w.lane; col < blocks_of(len, c.bs); col += 32) {
+            const int p = c.table[(int64_t)s * c.cols + col];
+            bad |= p < 0 || p >= c.pages || c.ref[p] < 1;
+        }
+        for (int col = w.lane; col < c.cols; col += 32) {
+            const int p = c.table[(int64_t)d * c.cols + col];
+            bad |= p < -1 || p >= c.pages || (p >= 0 && c.ref[p] < 1);
+        }
+    }
+    if (bad)
+        set_error(ws.err, NSA_ERR_BAD_INDEX);
+    cl.sync();
+    if (__ldcg(ws.err) != NSA_OK)
+        return;  // the same in every CTA: nothing has changed
+    // the destinations' own pages come back first: a tail may reuse them (an
+    // error here: more table entries name a page than its count says)
+    for (int i = w.warp; i < n; i += kAllWarps)
+        bad |= release_row(c, dst[i], w.lane, false);
+    cl.sync();  // every thread has read ws.err: it may be written again
+    if (bad)
+        set_error(ws.err, NSA_ERR_BAD_INDEX);
+    const Runs run(c, w.warp);
+    share_count(cl, counts, w, run.count(w.lane, [&](int p) { return __ldcg(c.ref + p) <= 0; }));
+    if (w.rank == 0) {
+        const int64_t t = cta_prefix(n, ws.r1, [&](int i) { return c.lens[src[i]] % c.bs != 0 ? 1 : 0; });
+        if (threadIdx.x < kCluster)
+            *cl.map_shared_rank(&tails_all, threadIdx.x) = t;
+    }
+    cl.sync();
+    const int64_t tails = tails_all;
+    int before, free;
+    scan_counts(counts, w, before, free);
+    if (tails > free) {  // undo: nothing has changed
+        for (int i = w.warp; i < n; i += kAllWarps)
+            for (int col = w.lane; col < c.cols; col += 32) {
+                const int p = c.table[(int64_t)dst[i] * c.cols + col];
+                if (p >= 0)
+                    atomicAdd(c.ref + p, 1);
+            }
+        if (w.rank == 0 && threadIdx.x == 0)
+            *ws.err = NSA_ERR_CACHE_FULL;
+        return;
+    }
+    take_free(c, run, w.lane, before, (int)tails, ws.p2);
+    cl.sync();
+    for (int i = w.warp; i < n; i += kAllWarps) {
+        const int s = src[i], d = dst[i], len = c.lens[s];
+        const int full = len / c.bs;
+        const bool tail = len % c.bs != 0;
+        const int nth = __ldcg(ws.r1 + i);
+        for (int col = w.lane; col < c.cols; col += 32) {
+            const int theirs = col < full + (tail ? 1 : 0) ? c.table[(int64_t)s * c.cols + col] : -1;
+            int mine = -1;
+            if (col < full) {
+                mine = theirs;
+                atomicAdd(c.ref + mine, 1);
+            } else if (col == full && tail) {
+                mine = __ldcg(ws.p2 + nth);
+                ws.p0[nth] = theirs;
+                ws.p1[nth] = mine;
+            }
+            c.table[(int64_t)d * c.cols + col] = mine;
+        }
+        if (w.lane == 0)
+            c.lens[d] = len;
+    }
+    if (w.rank == 0 && threadIdx.x == 0)
+        *ws.npairs = (int)tails;
+}
+
+// ---- copy: the pairs that may be copied -------------------------------------
+// A pair with a page outside the pool, a destination that an earlier pair
+// has, or a destination that is any pair's source is left out (-1).
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    cache_copy_check_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
+{
+    cg::cluster_group cl = cg::this_cluster();
+    const Where w = where(cl);
+    if (w.rank == 0 && threadIdx.x == 0) {
+        *ws.err = NSA_OK;
+        *ws.npairs = n;
+    }
+    claim_clear(src, n, c.pages, ws.p2, w);
+    claim_clear(dst, n, c.pages, ws.p2, w);
+    cl.sync();
+    claim(dst, n, c.pages, ws.p2, w, false);
+    claim(src, n, c.pages, ws.p2, w, true);
+    cl.sync();
+    bool bad = false;
+    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads) {
+        const int s = src[i], d = dst[i];
+        const bool ok = s >= 0 && s < c.pages && d >= 0 && d < c.pages && __ldcg(ws.p2 + d) == i;
+        ws.p0[i] = ok ? s : -1;
+        ws.p1[i] = ok ? d : -1;
+        bad |= !ok;
+    }
+    if (bad)
+        set_error(ws.err, NSA_ERR_BAD_INDEX);
+}
+
+// ---- compact: live pages to the front of the pool ---------------------------
+// With n live pages, the live pages at n and above move, in order, to the
+// free pages below n, in order.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cache_compact_kernel(const Cache c, const CacheWs ws)
+{
+    cg::cluster_group cl = cg::this_cluster();
+    __shared__ int counts[kAllWarps];
+    __shared__ int low;  // live pages below n
+    const Where w = where(cl);
+    if (w.rank == 0 && threadIdx.x == 0)
+        *ws.err = NSA_OK;
+    cl.sync();  // every CTA of the cluster runs from here on: its shared memory may be written
+    const Runs run(c, w.warp);
+    share_count(cl, counts, w, run.count(w.lane, [&](int p) { return c.ref[p] > 0; }));
+    cl.sync();
+    int before, n;
+    scan_counts(counts, w, before, n);
+    // the warp whose run holds page n (or, with every page live, the last)
+    // knows how many live pages lie below it
+    if (n == c.pages) {
+        if (threadIdx.x == 0)
+            low = n;
+    } else if (n >= run.begin && n < run.end) {
+        int k = before;
+        for (int p0 = run.begin; p0 < n; p0 += 32) {
+            const int p = p0 + w.lane;
+            k += __popc(__ballot_sync(0xffffffffu, p < n && c.ref[p] > 0));
+        }
+        if (w.lane < kCluster)
+            *cl.map_shared_rank(&low, w.lane) = k;
+    }
+    cl.sync();
+    const int moved = n - low;
+    int rank = before;
+    for (int p0 = run.begin; p0 < run.end; p0 += 32) {
+        const int p = p0 + w.lane;
+        const bool live = p < run.end && c.ref[p] > 0;
+        const unsigned m = __ballot_sync(0xffffffffu, live);
+        const int r = rank + __popc(m & ((1u << w.lane) - 1u));  // live pages below p
+        if (live && p >= n) {
+            ws.p0[r - low] = p;
+            ws.p2[p] = r - low;
+        } else if (!live && p < n)
+            ws.p1[p - r] = p;
+        rank += __popc(m);
+    }
+    cl.sync();
+    bool bad = false;
+    const int64_t entries = (int64_t)c.rows * c.cols;
+    for (int64_t i = w.rank * kThreads + threadIdx.x; i < entries; i += kCluster * kThreads) {
+        const int p = c.table[i];
+        if (p >= n && p < c.pages) {
+            // p's place among the moved pages, if it is one of them (a free
+            // page's entry of p2 was not written and may hold anything)
+            const int k = __ldcg(ws.p2 + p);
+            if (k >= 0 && k < moved && __ldcg(ws.p0 + k) == p)
+                c.table[i] = __ldcg(ws.p1 + k);
+            else
+                bad = true;
+        } else if (p < -1 || p >= c.pages)
+            bad = true;
+    }
+    for (int k = w.rank * kThreads + threadIdx.x; k < moved; k += kCluster * kThreads) {
+        const int s = __ldcg(ws.p0 + k), d = __ldcg(ws.p1 + k);
+        c.ref[d] = c.ref[s];
+        c.ref[s] = 0;
+    }
+    if (w.rank == 0 && threadIdx.x == 0)
+        *ws.npairs = moved;
+    if (bad)
+        set_error(ws.err, NSA_ERR_BAD_INDEX);
+}
+
+// ---- the pages' contents ------------------------------------------------------
+constexpr int kCopyThreads = 256;
+constexpr int kCopyVecs = 4;                          // 16-byte vectors per thread in flight
+constexpr int kChunk = kCopyThreads * kCopyVecs;      // vectors per step of a block
+
+// Pairs p0 -> p1, each in chunks of 16 KB of its keys, then of its values.
+__global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const Cache c, const CacheWs ws)
+{
+    const int n = *ws.npairs;
+    const int vtok = c.D / 16, sh_tok = 31 - __clz(vtok), sh_head = sh_tok + 31 - __clz(c.bs);
+    const int nvec = c.Hkv << sh_head;  // vectors of one page's keys
+    const int chunks = (nvec + kChunk - 1) / kChunk;
+    for (int64_t u = blockIdx.x; u < (int64_t)n * 2 * chunks; u += gridDim.x) {
+        const int chunk = (int)(u % chunks);
+        const int which = (int)(u / chunks & 1);
+        const int64_t pair = u / chunks / 2;
+        const int s = ws.p0[pair], d = ws.p1[pair];
+        if (s < 0)
+            continue;
+        uint8_t *base = which ? c.v : c.k;
+        uint4 x[kCopyVecs];
+        int64_t off[kCopyVecs];
+#pragma unroll
+        for (int i = 0; i < kCopyVecs; ++i) {
+            const int v = chunk * kChunk + i * kCopyThreads + threadIdx.x;
+            off[i] = (int64_t)(v >> sh_head) * c.sh + (int64_t)((v >> sh_tok) & (c.bs - 1)) * c.st + (v & (vtok - 1)) * 16;
+            if (v < nvec)
+                x[i] = *(const uint4 *)(base + (int64_t)s * c.sp + off[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopyVecs; ++i)
+            if (chunk * kChunk + i * kCopyThreads + threadIdx.x < nvec)
+                *(uint4 *)(base + (int64_t)d * c.sp + off[i]) = x[i];
+        if (chunk == 0)
+            for (int h = threadIdx.x; h < c.Hkv; h += kCopyThreads) {
+                float *f = which ? c.vs : c.ks;
+                f[(int64_t)d * c.Hkv + h] = f[(int64_t)s * c.Hkv + h];
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_reserve(const Cache &c, const int *n_new, const CacheWs &ws, cudaStream_t st)
+{
+    cache_reserve_kernel<<<kCluster, kThreads, 0, st>>>(c, n_new, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_free(const Cache &c, const int *rows, int n, const CacheWs &ws, cudaStream_t st)
+{
+    cache_free_kernel<<<kCluster, kThreads, 0, st>>>(c, rows, n, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_fork(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws, cudaStream_t st)
+{
+    cache_fork_kernel<<<kCluster, kThreads, 0, st>>>(c, src, dst, n, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_copy_check(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws,
+                                    cudaStream_t st)
+{
+    cache_copy_check_kernel<<<kCluster, kThreads, 0, st>>>(c, src, dst, n, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_compact(const Cache &c, const CacheWs &ws, cudaStream_t st)
+{
+    cache_compact_kernel<<<kCluster, kThreads, 0, st>>>(c, ws);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, cudaStream_t st)
+{
+    const int nvec = c.Hkv * c.bs * (c.D / 16);
+    const int64_t units = (int64_t)max_pairs * 2 * ((nvec + kChunk - 1) / kChunk);
+    const int64_t most = (int64_t)num_sms() * 8;
+    cache_move_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, st>>>(c, ws);
+    return cudaGetLastError();
+}
+
+}  // namespace nsa

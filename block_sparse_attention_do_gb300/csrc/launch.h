@@ -130,4 +130,22 @@ cudaError_t launch_dkdv_tc(const Geo &g, const void *q, const void *k, const voi
                            const WsHeader *hdr, int max_units, float *partials, void *dk, void *dv,
                            int *err, cudaStream_t st);
 
+// ---- the paged 8-bit cache (k_cache_*.cu) -----------------------------------
+struct Cache;
+struct CacheWs;
+int num_sms();  // of the current device (k_tc.cu)
+cudaError_t launch_cache_reserve(const Cache &c, const int *n_new, const CacheWs &ws, cudaStream_t st);
+cudaError_t launch_cache_free(const Cache &c, const int *rows, int n, const CacheWs &ws, cudaStream_t st);
+// the pairs of pages to copy go to ws; launch_cache_move copies them
+cudaError_t launch_cache_fork(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws, cudaStream_t st);
+cudaError_t launch_cache_copy_check(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws,
+                                    cudaStream_t st);
+cudaError_t launch_cache_compact(const Cache &c, const CacheWs &ws, cudaStream_t st);
+cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, cudaStream_t st);
+cudaError_t launch_cache_append(const Geo &g, const Cache &c, const void *k, const void *v, int dtype, int *err,
+                                cudaStream_t st);
+size_t cache_attn_ws_bytes(const Geo &g, bool sel);
+cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const int *idx, const float *sinks, void *o,
+                              float *lse, int dtype, char *ws, cudaStream_t st);
+
 }  // namespace nsa

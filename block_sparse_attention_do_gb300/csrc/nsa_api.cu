@@ -9,6 +9,7 @@
 
 #include <mutex>
 
+#include "cache_common.cuh"
 #include "launch.h"
 
 using namespace nsa;
@@ -973,6 +974,7 @@ const char *nsa_status_string(int32_t s)
     case NSA_ERR_DEVICE_TIMEOUT: return "NSA_ERR_DEVICE_TIMEOUT";
     case NSA_ERR_CUDA: return "NSA_ERR_CUDA";
     case NSA_ERR_WORKSPACE: return "NSA_ERR_WORKSPACE";
+    case NSA_ERR_CACHE_FULL: return "NSA_ERR_CACHE_FULL";
     default: return "NSA_ERR_UNKNOWN";
     }
 }
@@ -1093,6 +1095,251 @@ nsa_status nsa_count_pairs(const nsa_problem *p, const int32_t *cu_seqlens,
     if (!block_idx || !out_pairs)
         return NSA_ERR_INVALID_ARG;
     return cuda_status(launch_count_pairs(g, block_idx, (long long *)out_pairs, (cudaStream_t)stream));
+}
+
+// ---- the paged 8-bit cache --------------------------------------------------
+
+}  // extern "C"
+
+namespace {
+
+// Checks the cache and fills its device view.  `counts`: the call needs the
+// reference counts; `meta` / `data`: it needs the table and lengths / the pools.
+nsa_status make_cache(const nsa_cache *p, bool meta, bool counts, bool data, Cache &c)
+{
+    if (!p || p->num_pages < 1 || p->Hkv < 1 || p->rows < 1 || p->max_pages < 1)
+        return NSA_ERR_INVALID_ARG;
+    if ((p->D != 32 && p->D != 64 && p->D != 128) || (p->block_size != 16 && p->block_size != 32 && p->block_size != 64))
+        return NSA_ERR_UNSUPPORTED;
+    // positions, table entries and scales are counted in int
+    if ((int64_t)p->max_pages * p->block_size >= INT32_MAX || (int64_t)p->rows * p->max_pages >= INT32_MAX ||
+        (int64_t)p->num_pages * p->Hkv >= INT32_MAX || (int64_t)p->Hkv * p->block_size * p->D >= INT32_MAX)
+        return NSA_ERR_UNSUPPORTED;
+    const int64_t *s = p->stride;
+    if (s[0] == 0 && s[1] == 0 && s[2] == 0) {
+        c.st = p->D;
+        c.sh = c.st * p->block_size;
+        c.sp = c.sh * p->Hkv;
+    } else {
+        for (int i = 0; i < 3; ++i)
+            if (s[i] <= 0 || s[i] % 16 != 0 || s[i] >= ((int64_t)1 << 40))
+                return NSA_ERR_INVALID_ARG;
+        c.sp = s[0];
+        c.sh = s[1];
+        c.st = s[2];
+    }
+    auto bad4 = [](const void *x) { return !x || ((uintptr_t)x & 3u); };
+    if (meta && (bad4(p->page_table) || bad4(p->seq_lens)))
+        return NSA_ERR_INVALID_ARG;
+    if ((counts && bad4(p->refcount)) || (p->refcount && bad4(p->refcount)))
+        return NSA_ERR_INVALID_ARG;
+    if (data && (!p->k || !p->v || !aligned16(p->k) || !aligned16(p->v) || bad4(p->k_scale) || bad4(p->v_scale)))
+        return NSA_ERR_INVALID_ARG;
+    c.pages = p->num_pages;
+    c.Hkv = p->Hkv;
+    c.D = p->D;
+    c.bs = p->block_size;
+    c.rows = p->rows;
+    c.cols = p->max_pages;
+    c.k = (uint8_t *)p->k;
+    c.v = (uint8_t *)p->v;
+    c.ks = p->k_scale;
+    c.vs = p->v_scale;
+    c.table = p->page_table;
+    c.lens = p->seq_lens;
+    c.ref = p->refcount;
+    return NSA_OK;
+}
+
+size_t cache_ws(const Cache &c, char *ws, CacheWs &w)
+{
+    size_t off = kAlign;
+    auto take = [&](int n) {
+        int *p = (int *)(ws + off);
+        off = align_up(off + sizeof(int) * (size_t)n);
+        return p;
+    };
+    w.err = (int *)ws;
+    w.npairs = w.err + 1;
+    w.p0 = take(c.pages);
+    w.p1 = take(c.pages);
+    w.p2 = take(c.pages);
+    w.r0 = take(c.rows);
+    w.r1 = take(c.rows);
+    return off;
+}
+
+// the problem and the cache of one call: the problem's rows are the table's
+nsa_status cache_geo(const nsa_problem *p, const nsa_cache *pc, const int32_t *cu, bool sel, int window, Geo &g, Cache &c)
+{
+    nsa_status s = make_cache(pc, true, false, true, c);
+    if (s != NSA_OK)
+        return s;
+    if (!p)
+        return NSA_ERR_INVALID_ARG;
+    if ((s = make_geo(p, p->layout == NSA_LAYOUT_THD, sel ? SPARSE : DENSE, cu, g, window)) != NSA_OK)
+        return s;
+    if (!g.thd && cu)
+        return NSA_ERR_INVALID_ARG;
+    if (p->B != pc->rows || p->Hkv != pc->Hkv || p->D != pc->D || p->block_size != pc->block_size)
+        return NSA_ERR_INVALID_ARG;
+    return NSA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t nsa_cache_workspace_size(const nsa_cache *pc)
+{
+    Cache c;
+    CacheWs w;
+    return make_cache(pc, false, false, false, c) == NSA_OK ? cache_ws(c, nullptr, w) : 0;
+}
+
+nsa_status nsa_cache_reserve(const nsa_cache *pc, const int32_t *n_new, void *ws, size_t ws_bytes, void *stream)
+{
+    Cache c;
+    CacheWs w;
+    nsa_status s = make_cache(pc, true, true, false, c);
+    if (s != NSA_OK)
+        return s;
+    if (!n_new || ((uintptr_t)n_new & 3u))
+        return NSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, cache_ws(c, (char *)ws, w))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_reserve", launch_cache_reserve(c, n_new, w, st));
+    return NSA_OK;
+}
+
+nsa_status nsa_cache_free(const nsa_cache *pc, const int32_t *rows, int32_t n, void *ws, size_t ws_bytes, void *stream)
+{
+    Cache c;
+    CacheWs w;
+    nsa_status s = make_cache(pc, true, true, false, c);
+    if (s != NSA_OK)
+        return s;
+    if (n < 0 || n > c.rows || (n > 0 && (!rows || ((uintptr_t)rows & 3u))))
+        return NSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, cache_ws(c, (char *)ws, w))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_free", launch_cache_free(c, rows, n, w, st));
+    return NSA_OK;
+}
+
+nsa_status nsa_cache_fork(const nsa_cache *pc, const int32_t *src, const int32_t *dst, int32_t n, void *ws,
+                          size_t ws_bytes, void *stream)
+{
+    Cache c;
+    CacheWs w;
+    nsa_status s = make_cache(pc, true, true, true, c);
+    if (s != NSA_OK)
+        return s;
+    if (n < 0 || n > c.rows || (n > 0 && (!src || !dst || ((uintptr_t)src & 3u) || ((uintptr_t)dst & 3u))))
+        return NSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, cache_ws(c, (char *)ws, w))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_fork", launch_cache_fork(c, src, dst, n, w, st));
+    if (n > 0)
+        NSA_LAUNCH("cache_move", launch_cache_move(c, w, n, st));
+    return NSA_OK;
+}
+
+nsa_status nsa_cache_copy(const nsa_cache *pc, const int32_t *src_pages, const int32_t *dst_pages, int32_t n, void *ws,
+                          size_t ws_bytes, void *stream)
+{
+    Cache c;
+    CacheWs w;
+    nsa_status s = make_cache(pc, false, false, true, c);
+    if (s != NSA_OK)
+        return s;
+    if (n < 0 || n > c.pages ||
+        (n > 0 && (!src_pages || !dst_pages || ((uintptr_t)src_pages & 3u) || ((uintptr_t)dst_pages & 3u))))
+        return NSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, cache_ws(c, (char *)ws, w))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_copy_check", launch_cache_copy_check(c, src_pages, dst_pages, n, w, st));
+    if (n > 0)
+        NSA_LAUNCH("cache_move", launch_cache_move(c, w, n, st));
+    return NSA_OK;
+}
+
+nsa_status nsa_cache_compact(const nsa_cache *pc, void *ws, size_t ws_bytes, void *stream)
+{
+    Cache c;
+    CacheWs w;
+    nsa_status s = make_cache(pc, true, true, true, c);
+    if (s != NSA_OK)
+        return s;
+    if ((s = check_ws(ws, ws_bytes, cache_ws(c, (char *)ws, w))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_compact", launch_cache_compact(c, w, st));
+    NSA_LAUNCH("cache_move", launch_cache_move(c, w, (c.pages + 1) / 2, st));
+    return NSA_OK;
+}
+
+nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *pc, const int32_t *cu_seqlens, const void *k,
+                            const void *v, void *ws, size_t ws_bytes, void *stream)
+{
+    Geo g;
+    Cache c;
+    nsa_status s = cache_geo(p, pc, cu_seqlens, false, 0, g, c);
+    if (s != NSA_OK)
+        return s;
+    if (!k || !v || !aligned16(k) || !aligned16(v))
+        return NSA_ERR_INVALID_ARG;
+    if ((s = check_ws(ws, ws_bytes, kAlign)) != NSA_OK)
+        return s;
+    const int64_t units = (int64_t)c.rows * ((g.T + c.bs - 2) / c.bs + 1) * 2 * c.Hkv;
+    if (units + 1 >= INT32_MAX)
+        return NSA_ERR_UNSUPPORTED;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_append", launch_cache_append(g, c, k, v, p->dtype, (int *)ws, st));
+    return NSA_OK;
+}
+
+size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *pc, int32_t selection)
+{
+    Geo g;
+    Cache c;
+    if (!p || !pc)
+        return 0;
+    nsa_cache shape = *pc;  // pointers do not matter here
+    shape.k = shape.v = (void *)(uintptr_t)kAlign;
+    shape.k_scale = shape.v_scale = (float *)(uintptr_t)kAlign;
+    shape.page_table = shape.seq_lens = (int32_t *)(uintptr_t)kAlign;
+    shape.refcount = nullptr;
+    const bool thd = p->layout == NSA_LAYOUT_THD;
+    if (cache_geo(p, &shape, thd ? kFakeCuQ : nullptr, selection != 0, 0, g, c) != NSA_OK)
+        return 0;
+    return cache_attn_ws_bytes(g, selection != 0);
+}
+
+nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t window, const int32_t *cu_seqlens,
+                         const int32_t *block_idx, const float *sinks, const void *q, void *o, float *lse, void *ws,
+                         size_t ws_bytes, void *stream)
+{
+    Geo g;
+    Cache c;
+    nsa_status s = cache_geo(p, pc, cu_seqlens, block_idx != nullptr, window, g, c);
+    if (s != NSA_OK)
+        return s;
+    if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || ((uintptr_t)lse & 3u) || ((uintptr_t)block_idx & 3u) ||
+        ((uintptr_t)sinks & 3u) || (block_idx && sinks))
+        return NSA_ERR_INVALID_ARG;
+    // the list of pages is counted in int, and its prefix over the sequences sits in shared memory
+    if (!block_idx && ((int64_t)g.B * c.cols * (((int64_t)g.T * g.G + 7) / 8) >= INT32_MAX || g.B > 8192))
+        return NSA_ERR_UNSUPPORTED;
+    if ((s = check_ws(ws, ws_bytes, cache_attn_ws_bytes(g, block_idx != nullptr))) != NSA_OK)
+        return s;
+    cudaStream_t st = (cudaStream_t)stream;
+    NSA_LAUNCH("cache_attn", launch_cache_attn(g, c, q, block_idx, sinks, o, lse, p->dtype, (char *)ws, st));
+    return NSA_OK;
 }
 
 }  // extern "C"

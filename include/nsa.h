@@ -66,7 +66,8 @@ typedef enum nsa_status {
     NSA_ERR_BAD_INDEX = 3,      /* (device) index entry < -1, in the future, or repeated in a row */
     NSA_ERR_DEVICE_TIMEOUT = 4, /* (device) a bounded wait inside a kernel gave up */
     NSA_ERR_CUDA = 5,           /* a CUDA runtime call failed (launch, tensor map) */
-    NSA_ERR_WORKSPACE = 6       /* ws is NULL, too small or misaligned */
+    NSA_ERR_WORKSPACE = 6,      /* ws is NULL, too small or misaligned */
+    NSA_ERR_CACHE_FULL = 7      /* (device) the cache has too few free pages; nothing was changed */
 } nsa_status;
 
 enum { NSA_DTYPE_F32 = 0, NSA_DTYPE_BF16 = 1 };
@@ -413,6 +414,119 @@ nsa_status nsa_block_scores(const nsa_problem *p, const int32_t *cu_seqlens, con
                             float *scores, void *ws, size_t ws_bytes, void *stream);
 nsa_status nsa_select_topk(const nsa_problem *p, const int32_t *cu_seqlens, const float *scores, int32_t *idx,
                            void *stream);
+
+/*
+ * A paged key/value cache held in 8 bits, for serving: keys and values of
+ * earlier tokens in e4m3 with one fp32 scale per page and kv head, the pages
+ * themselves, and the attention of new tokens over them.  (The pages this
+ * library follows are about training and describe no cache; the operators
+ * below are the decoding side of the same attention: same heads, same index
+ * rows, same masks.)
+ *
+ *   page       one block of block_size tokens.  Page p, head h, token i of the
+ *              page: D codes at k + p*stride[0] + h*stride[1] + i*stride[2]
+ *              (v alike); its key is k_scale[p*Hkv + h] * code
+ *   page_table [rows, max_pages] int32: row b's blocks in order, -1 behind
+ *              them.  A row is one sequence (a batch entry of the calls below)
+ *   seq_lens   [rows] int32: tokens of each row, NEW TOKENS INCLUDED: reserve
+ *              first, then append, then attend
+ *   refcount   [num_pages] int32: table entries that name each page; 0: free
+ *
+ * All of it is the caller's device memory; the calls change it on `stream`,
+ * without a host round trip, so they can be captured in CUDA graphs.  Calls
+ * that change a cache must not run at the same time as any other call on it;
+ * nsa_cache_fwd calls only read it and may run at the same time (each with a
+ * ws of its own).  Table entries and lengths are checked on the device: an
+ * entry outside the pool, a length beyond max_pages * block_size or below 0
+ * is reported (NSA_ERR_BAD_INDEX through nsa_get_error(ws, ...), of the last
+ * call that used ws) and left out; nothing is read or written outside the
+ * pool.
+ */
+typedef struct nsa_cache {
+    int32_t num_pages;
+    int32_t Hkv;
+    int32_t D;            /* 32, 64 or 128 */
+    int32_t block_size;   /* tokens per page: 16, 32 or 64 */
+    int32_t rows;
+    int32_t max_pages;    /* columns of the page table */
+    int64_t stride[3];    /* (page, head, token) strides of k and v in bytes; all 0: dense
+                             [num_pages, Hkv, block_size, D].  Multiples of 16, below 2^40 */
+    void *k, *v;          /* e4m3 codes, 16-byte aligned */
+    float *k_scale, *v_scale; /* [num_pages, Hkv], positive */
+    int32_t *page_table, *seq_lens;
+    int32_t *refcount;    /* may be NULL for nsa_cache_append, _copy and _fwd */
+} nsa_cache;
+
+/*
+ * The pages.  All five take a workspace of nsa_cache_workspace_size bytes
+ * (256-byte aligned, any contents; 0: invalid cache), and choose the lowest
+ * free page ids first, so that their results depend on the cache's state alone.
+ *  - reserve: row b grows by n_new[b] >= 0 tokens (device int32 [rows]): pages
+ *    for them, in the order of rows and columns, and seq_lens.  All rows or
+ *    none: NSA_ERR_CACHE_FULL (too few free pages) or NSA_ERR_BAD_INDEX (a
+ *    negative count, a row beyond max_pages) changes nothing.
+ *  - free: the n listed rows (device int32) give up their pages and have
+ *    length 0.  A row outside the table or listed twice is reported, and
+ *    freed once.
+ *  - fork: row dst[i] gives up its pages and becomes a continuation of row
+ *    src[i]: it shares src's full blocks and gets a copy of its last, partly
+ *    filled one.  The dst are distinct and none is a src (else
+ *    NSA_ERR_BAD_INDEX); that, or NSA_ERR_CACHE_FULL, changes nothing.
+ *  - copy: page src_pages[i] to dst_pages[i], codes and scales (table and
+ *    counts stay).  A dst that is listed before, or is any src, is reported
+ *    and left out.
+ *  - compact: with n pages in use, those at n and above move, in order, to the
+ *    free ones below n; table and counts follow.  Every page in use must be
+ *    named by the table.
+ */
+size_t nsa_cache_workspace_size(const nsa_cache *c);
+nsa_status nsa_cache_reserve(const nsa_cache *c, const int32_t *n_new, void *ws, size_t ws_bytes, void *stream);
+nsa_status nsa_cache_free(const nsa_cache *c, const int32_t *rows, int32_t n, void *ws, size_t ws_bytes,
+                          void *stream);
+nsa_status nsa_cache_fork(const nsa_cache *c, const int32_t *src, const int32_t *dst, int32_t n, void *ws,
+                          size_t ws_bytes, void *stream);
+nsa_status nsa_cache_copy(const nsa_cache *c, const int32_t *src_pages, const int32_t *dst_pages, int32_t n, void *ws,
+                          size_t ws_bytes, void *stream);
+nsa_status nsa_cache_compact(const nsa_cache *c, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Append: the new tokens' keys and values (p's dtype, layout and kv_stride;
+ * BHTD k, v [rows,Hkv,T,D], every row T new tokens; THD [total_tokens,Hkv,D]
+ * with cu_seqlens, 0 .. T each) go, rounded to e4m3, to the last n_b positions
+ * of their rows.  p->B = rows, and p->Hkv, D and block_size are the cache's.
+ *   scale s of a page and head that gets tokens: the least power of two with
+ *     max|x| <= 448 s over their finite x, at least 2^-100; if the page holds
+ *     earlier tokens of the row, at least its old scale, and where that grew
+ *     their codes are rounded again: code' = e4m3(code * (old / s))
+ *   code = e4m3(x / s): nearest, ties to even, clamped to +-448; NaN stays NaN
+ * Other slots of the pages are left as they were.  Pages that get tokens must
+ * be the row's alone: with refcount given, a page whose count is not 1 is
+ * reported (NSA_ERR_BAD_INDEX) and not written.  ws: 256 bytes.
+ */
+nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *c, const int32_t *cu_seqlens, const void *k,
+                            const void *v, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of the rows' last tokens over the cache: query token t of the n_b
+ * of row b (BHTD n_b = T; THD n_b from cu_seqlens, at most T) sits at key
+ * position c_t = seq_lens[b] - n_b + t and attends key k iff k <= c_t and
+ *   block_idx NULL:  with window >= 1, also c_t - k < window
+ *   block_idx given: k / block_size is in its index row ([B,Hkv,T,S], THD
+ *                    [total,Hkv,S]; entries as for nsa_sel_fwd: -1 pads, an
+ *                    entry in the future or repeated is reported and left
+ *                    out); window 0, sinks NULL
+ * sinks (Hq floats or NULL): as for nsa_sink_fwd.  q, o: p's dtype, layout and
+ * strides; lse as for the other forwards.  A row that attends nothing gets
+ * O = 0 and LSE = -inf (with sinks: the sink).  Masked places may hold
+ * anything, NaN included.  Rows of THD tensors that belong to no sequence are
+ * left as they were.  p->B = rows, p->Hkv, D and block_size the cache's,
+ * p->kv_stride unused.  `selection`: whether block_idx will be given.
+ * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).
+ */
+size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *c, int32_t selection);
+nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *c, int32_t window, const int32_t *cu_seqlens,
+                         const int32_t *block_idx, const float *sinks, const void *q, void *o, float *lse, void *ws,
+                         size_t ws_bytes, void *stream);
 
 /*
  * Reads the device error word of a workspace used by the calls above,
