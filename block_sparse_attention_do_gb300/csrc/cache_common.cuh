@@ -52,12 +52,12 @@ __device__ __forceinline__ uint32_t e4m3_pack2(float lo, float hi)
     return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-// two codes (low 16 bits) to a pair of halves: exact (e4m3 is a subset)
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two)
+// four codes to two pairs of halves (lo: bytes 0, 1): exact, e4m3 is a subset
+__device__ __forceinline__ void e4m3x4_to_half(uint32_t four, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-    return r;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
 }  // namespace nsa

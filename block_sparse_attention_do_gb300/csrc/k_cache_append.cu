@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
             uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const uint32_t a = e4m3_to_half2(u[i] & 0xffffu), d = e4m3_to_half2(u[i] >> 16);
+                uint32_t a, d;
+                e4m3x4_to_half(u[i], a, d);
                 const float2 fa = __half22float2(*(const __half2 *)&a), fd = __half22float2(*(const __half2 *)&d);
                 u[i] = e4m3_pack2(fa.x * ratio, fa.y * ratio) | e4m3_pack2(fd.x * ratio, fd.y * ratio) << 16;
             }

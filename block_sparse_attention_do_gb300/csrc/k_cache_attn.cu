@@ -40,10 +40,14 @@ namespace nsa {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kList = 256;       // pages of a run listed in shared memory at a time
+// Warps of a CTA and CTAs of an SM, by the tiles of 8 query rows: a thread
+// holds O in 4 D / 16 registers a tile, and the codes in flight in 32.  One
+// tile: 16 warps an SM of 128 registers; two: 12 of 168 (128 spill); four: 8
+// of 255.
+__host__ __device__ constexpr int attn_warps(int nt) { return nt == 2 ? 6 : 8; }
+__host__ __device__ constexpr int attn_ctas(int nt) { return nt >= 4 ? 1 : 2; }
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
+constexpr int kNoKey = 0x7f000000; // position of the keys of an entry that is left out
 constexpr float kLazy = 10.f;    // w may reach 2^10 before its row's maximum is raised (half holds 2^15)
 
 struct AttnArgs {
@@ -80,6 +84,11 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// programmatic dependents: the next kernel may be set up from here on; wait
+// for the kernel before this one to complete
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t y;
@@ -108,15 +117,21 @@ __device__ __forceinline__ int query_tokens(const Geo &g, int b)
     return g.thd && (n < 0 || n > g.T || g.cu[b] < 0 || g.cu[b + 1] > g.ntok) ? -1 : n;
 }
 
+// tokens of sequence b in the cache (a length that the table cannot hold is reported by the join)
+__device__ __forceinline__ int held_tokens(const AttnArgs &a, int b)
+{
+    return min(max(a.c.lens[b], 0), a.c.cols * a.c.bs);
+}
+
 // The pages of sequence b that any of its query rows attends: [lo, lo + n).
 __device__ __forceinline__ int attended_pages(const AttnArgs &a, int b, int &lo)
 {
-    const int nq = query_tokens(a.g, b), len = (int)min((int64_t)a.c.lens[b], (int64_t)a.c.cols * a.c.bs);
+    const int nq = query_tokens(a.g, b), len = held_tokens(a, b);
     lo = 0;
     if (nq <= 0 || len <= 0)
         return 0;
     if (a.g.window > 0) {
-        const int64_t first = (int64_t)a.c.lens[b] - nq - a.g.window + 1;  // the first row's left edge
+        const int64_t first = (int64_t)len - nq - a.g.window + 1;  // the first row's left edge
         lo = first > 0 ? (int)(first / a.c.bs) : 0;
     }
     return max(0, (len - 1) / a.c.bs + 1 - lo);
@@ -132,26 +147,48 @@ template <int R> __device__ __forceinline__ int row_tiles_of(const Geo &g, int b
 // belongs to it.
 struct UnitRows {
     int b, kvh, row0, nrows;  // rows row0 .. of sequence b (row = token * G + head), nrows of them valid
-    int64_t begin, count;     // its entries in the list
+    int begin, count;         // its entries in the list
     int page_lo;              // dense: first page
+};
+
+// The list cut into equal runs, one per CTA, at multiples of the quantum.
+struct Runs {
+    int total, quantum, ncta, per, rem;
+    __device__ __forceinline__ Runs(int total_, const AttnArgs &a) : total(total_), quantum(a.quantum), ncta(a.ncta)
+    {
+        const int nq = (total + quantum - 1) / quantum;
+        per = nq / ncta;
+        rem = nq % ncta;
+    }
+    __device__ __forceinline__ int begin(int cta) const
+    {
+        return (int)min((int64_t)total, (int64_t)(cta * per + min(cta, rem)) * quantum);
+    }
+    __device__ __forceinline__ int cta_of(int entry) const
+    {
+        const int q = entry / quantum, longer = rem * (per + 1);
+        return q < longer ? q / (per + 1) : rem + (q - longer) / max(per, 1);
+    }
 };
 
 // NT: tiles of 8 query rows; SPLIT: fp32 queries (two halves)
 template <int D, int NT, bool SPLIT> struct Smem {
+    static constexpr int kWarps = attn_warps(NT);
+    static constexpr int kList = kWarps * 32;  // pages of a run listed at a time, one per thread
     static constexpr int R = NT * 8;
     static constexpr int KS = D / 16;  // k-steps of S
     uint2 qf[SPLIT ? 2 : 1][KS][NT][32];
     float qmul[R];  // scale * log2(e) * 2^-e of each row
     int pos[R];     // key position of each row's token (-1: no such row)
-    int page[kList], key0[kList];
-    float ks[kList], lv[kList], iv[kList];
-    int sidx[256];
-    float m[kWarps][R], l[kWarps][R];
-    float o[kWarps / 2][R][D + 4];
+    int64_t off[kList];  // of the listed entries: byte offset of the page and head
+    int key0[kList];     // first key (kNoKey: left out)
+    float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
+    float2 ml[kWarps][R];       // each warp's maximum and sum
+    float o[kWarps][R][D + 4];  // and its part of O
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn_kernel(const AttnArgs a)
 {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int R = NT * 8, KS = D / 16, MT = D / 16;
@@ -159,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
     constexpr int KL = D / 4 / KB;             // K loads per token and thread
     constexpr int VB = D / 8;                  // bytes of a V load: one per token and thread
     constexpr int VW = VB / 4;                 // words
+    constexpr int kWarps = attn_warps(NT), kThreads = kWarps * 32, kList = kThreads;
     using SM = Smem<D, NT, SPLIT>;
     extern __shared__ __align__(16) char smem_raw[];
     SM &sm = *(SM *)smem_raw;
@@ -167,17 +205,18 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gq = lane >> 2, tq = lane & 3;  // the fragment's row group and column pair
     const int cta = blockIdx.x;
+    dependents_may_start();
     const bool sel = a.idx != nullptr;
     bool bad = false;
 
     // ---- the call's list of pages and this CTA's run of it
     __shared__ int part_s[kWarps];
     int *prefix = (int *)(smem_raw + sizeof(SM));  // dense: as a.prefix
-    int64_t total;
+    int total;
     if (sel)
-        total = (int64_t)g.ntok * g.Hkv * a.row_tiles * g.S;
+        total = g.ntok * g.Hkv * a.row_tiles * g.S;
     else {
-        int64_t base = 0;
+        int base = 0;
         for (int b0 = 0; b0 < g.B; b0 += kThreads) {
             const int b = b0 + tid;
             int lo, n = b < g.B ? attended_pages(a, b, lo) : 0;
@@ -196,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 all += part_s[k];
             }
             if (b < g.B) {
-                prefix[b] = (int)base + before + incl - n;
+                prefix[b] = base + before + incl - n;
                 if (cta == 0)
                     a.prefix[b] = prefix[b];
             }
@@ -204,35 +243,34 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
             __syncthreads();
         }
         if (tid == 0) {
-            prefix[g.B] = (int)base;
+            prefix[g.B] = base;
             if (cta == 0)
-                a.prefix[g.B] = (int)base;
+                a.prefix[g.B] = base;
         }
         __syncthreads();
         total = base * g.Hkv;
     }
-    const int64_t nq = (total + a.quantum - 1) / a.quantum;
-    const int64_t run0 = nq * cta / a.ncta * a.quantum;
-    const int64_t run1 = min(total, nq * (cta + 1) / a.ncta * a.quantum);
+    const int st = (int)c.st, per_sh = 31 - __clz(c.bs) - 4, per_mask = (1 << per_sh) - 1;  // steps per page
+    const Runs runs(total, a);
+    const int run0 = runs.begin(cta), run1 = runs.begin(cta + 1);
 
-    for (int64_t at = run0; at < run1;) {
+    for (int at = run0; at < run1;) {
         // ---- the unit that holds list entry `at`
         UnitRows u;
         if (sel) {
-            const int64_t unit = at / g.S;
+            const int unit = at / g.S;
             u.begin = unit * g.S;
             u.count = g.S;
-            const int rt = (int)(unit % a.row_tiles);
-            const int64_t row = unit / a.row_tiles;  // index row
+            const int rt = unit % a.row_tiles, row = unit / a.row_tiles;  // row: of the index
             int t;
             if (g.thd) {
-                const int tok = (int)(row / g.Hkv);
-                u.kvh = (int)(row % g.Hkv);
+                const int tok = row / g.Hkv;
+                u.kvh = row % g.Hkv;
                 u.b = seq_of_token(g, tok);
                 t = tok - g.cu[u.b];
             } else {
-                t = (int)(row % g.T);
-                const int bg = (int)(row / g.T);
+                t = row % g.T;
+                const int bg = row / g.T;
                 u.b = bg / g.Hkv;
                 u.kvh = bg % g.Hkv;
             }
@@ -240,33 +278,62 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
             u.nrows = t < query_tokens(g, u.b) ? min(R, g.G - rt * R) : 0;  // 0: a token of no sequence
             u.page_lo = 0;
         } else {
-            const int64_t per = g.Hkv;
-            int lo = 0, hi = g.B - 1;  // the sequence: prefix[b] * per <= at < prefix[b + 1] * per
+            int lo = 0, hi = g.B - 1;  // the sequence: prefix[b] * Hkv <= at < prefix[b + 1] * Hkv
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if ((int64_t)prefix[mid] * per <= at)
+                if (prefix[mid] * g.Hkv <= at)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
             u.b = lo;
             const int n = attended_pages(a, lo, u.page_lo), tiles = row_tiles_of<R>(g, lo);
-            const int64_t in = (at - (int64_t)prefix[lo] * per) / n;  // (kv head, row tile)
-            u.begin = (int64_t)prefix[lo] * per + in * n;
+            const int in = (at - prefix[lo] * g.Hkv) / n;  // (kv head, row tile)
+            u.begin = prefix[lo] * g.Hkv + in * n;
             u.count = n;
-            u.kvh = (int)(in / tiles);
-            u.row0 = (int)(in % tiles) * R;
+            u.kvh = in / tiles;
+            u.row0 = in % tiles * R;
             u.nrows = min(R, query_tokens(g, lo) * g.G - u.row0);
         }
-        const int64_t seg1 = min(run1, u.begin + u.count);
+        const int seg1 = min(run1, u.begin + u.count);
         if (u.nrows <= 0) {
             at = seg1;
             continue;
         }
-        const int len = min((int64_t)max(c.lens[u.b], 0), (int64_t)c.cols * c.bs);
-        const int pos0 = c.lens[u.b] - seq_len(g, u.b);  // position of the sequence's first query token
-        if (c.lens[u.b] < 0 || c.lens[u.b] > len)
-            bad = true;
+        const int len = held_tokens(a, u.b);
+        const int pos0 = len - query_tokens(g, u.b);  // position of the sequence's first query token
+        const int t_first = u.row0 / g.G, t_last = (u.row0 + u.nrows - 1) / g.G;
+        const int pmin = pos0 + t_first, pmax = pos0 + t_last;  // of the tile's rows
+        const int key_lo = g.window > 0 ? pmin - g.window - 14 : INT32_MIN;  // steps before it lie left of every window
+
+        // One list entry per thread: its block (-1: left out) and page.  Only
+        // the ids stand before the first loads of codes; what else an entry
+        // needs is fetched behind those.
+        const int64_t irow = sel ? index_row(g, u.b, u.kvh, t_first) * g.S : 0;
+        auto list_block = [&](int entry) {
+            int j = sel ? a.idx[irow + entry - u.begin] : u.page_lo + entry - u.begin;
+            if (sel && j != -1 && (j < 0 || j >= c.cols || j * c.bs > pmax || j * c.bs >= len)) {  // no block, or in the future
+                bad = true;
+                j = -1;
+            }
+            return j;
+        };
+        auto list_page = [&](int j) {
+            int page = -1;
+            if (j >= 0) {
+                page = c.table[(int64_t)u.b * c.cols + j];
+                if (page < 0 || page >= c.pages) {
+                    bad = true;
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        int my_block = -1, my_page = -1;
+        if (at + tid < min(seg1, at + kList)) {
+            my_block = list_block(at + tid);
+            my_page = list_page(my_block);
+        }
 
         // ---- queries into fragments: element (k, n) of B is row n's element
         // k, in the order of the head dimension that the K loads give
@@ -282,9 +349,7 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 x[e] = have ? to_f<T>(((const T *)a.q)[q_off(g, u.b, h, t) + e * 32 + lane]) : 0.f;
                 amax = fmaxf(amax, fabsf(x[e]));
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // of values >= 0
             // the row's largest element to [2^14, 2^15)
             const int be = (int)(__float_as_uint(amax) >> 23);  // biased exponent (0: none, 255: infinity)
             const int e2 = be == 0 || be == 255 ? 0 : min(max(14 - (be - 127), -120), 120);
@@ -310,25 +375,16 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 sm.pos[r] = have ? pos0 + t : -1;
             }
         }
-        __syncthreads();
 
         float o[NT][MT][4];
-        float m[NT][2], l[NT][2], qm[NT][2];
-        int pos[NT][2];
-        int pmin = INT32_MAX, pmax = -1;  // of the tile's rows
+        float m[NT][2], l[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = kNoMax;
                 l[n][i] = 0.f;
-                qm[n][i] = sm.qmul[n * 8 + tq * 2 + i];
-                pos[n][i] = sm.pos[n * 8 + tq * 2 + i];
             }
-        for (int r = 0; r < u.nrows; ++r) {
-            pmin = min(pmin, sm.pos[r]);
-            pmax = max(pmax, sm.pos[r]);
-        }
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -337,142 +393,146 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 for (int i = 0; i < 4; ++i)
                     o[n][j][i] = 0.f;
 
-        for (int64_t e0 = at; e0 < seg1; e0 += kList) {
-            const int ne = (int)min((int64_t)kList, seg1 - e0);
-            // ---- the run's next pages
-            __syncthreads();
-            if (sel) {
-                const int64_t irow = index_row(g, u.b, u.kvh, u.row0 / g.G);
-                for (int s = tid; s < g.S; s += kThreads)
-                    sm.sidx[s] = a.idx[irow * g.S + s];
-                __syncthreads();
+        for (int e0 = at; e0 < seg1; e0 += kList) {
+            const int ne = min(kList, seg1 - e0);
+            if (e0 > at) {
+                my_block = my_page = -1;
+                if (tid < ne) {
+                    my_block = list_block(e0 + tid);
+                    my_page = list_page(my_block);
+                }
+                __syncthreads();  // the list before is used up
             }
-            for (int i = tid; i < ne; i += kThreads) {
-                const int s = (int)(e0 + i - u.begin);
-                int j = sel ? sm.sidx[s] : u.page_lo + s, page = -1;
-                if (sel && j >= 0) {
-                    bool twice = false;
-                    for (int k = 0; k < s; ++k)
-                        twice |= sm.sidx[k] == j;
-                    if (twice || (int64_t)j * c.bs > pmax || (int64_t)j * c.bs >= len) {  // repeated or in the future
-                        bad = true;
-                        j = -1;
-                    }
-                } else if (sel && j != -1) {
-                    bad = true;
-                    j = -1;
-                }
-                float ks = 0.f, vs = 1.f;
-                if (j >= 0) {
-                    page = c.table[(int64_t)u.b * c.cols + j];
-                    if (page < 0 || page >= c.pages) {
-                        bad = true;
-                        page = -1;
-                    } else {
-                        ks = c.ks[(int64_t)page * c.Hkv + u.kvh];
-                        vs = fmaxf(c.vs[(int64_t)page * c.Hkv + u.kvh], kScaleFloor);
-                    }
-                }
-                sm.page[i] = page;
-                sm.key0[i] = j * c.bs;
-                sm.ks[i] = ks;
-                sm.lv[i] = log2f(vs);
-                sm.iv[i] = 1.f / vs;
+            if (tid < ne) {
+                sm.off[tid] = my_page >= 0 ? (int64_t)my_page * c.sp + (int64_t)u.kvh * c.sh : 0;
+                sm.key0[tid] = my_page >= 0 ? my_block * c.bs : kNoKey;
             }
             __syncthreads();
 
             // ---- 16-token steps of the listed pages, the warps in turn
-            const int per = c.bs / 16, steps = ne * per;
-            const int64_t head_off = (int64_t)u.kvh * c.sh;
+            const int steps = ne << per_sh;
             uint32_t kw[2][KL * KB / 4], vw[4][VW];
-            auto step_page = [&](int s, int &page, int &key) {
-                const int e = s / per;
-                page = sm.page[e];
-                key = sm.key0[e] + s % per * 16;
-                // a step that no row attends is not read
-                return page >= 0 && key < len && key <= pmax && !(g.window > 0 && key + 15 <= pmin - g.window);
-            };
-            auto next_step = [&](int s, int &page, int &key) {
-                while (s < steps && !step_page(s, page, key))
-                    s += kWarps;
-                return s;
-            };
-            auto load_k = [&](int page, int key) {
-                const uint8_t *p = c.k + (int64_t)page * c.sp + head_off + (int64_t)(key % c.bs) * c.st;
+            // the step's first key; a step that no row attends is not read
+            auto step_key = [&](int s) { return s < steps ? sm.key0[s >> per_sh] + (s & per_mask) * 16 : kNoKey; };
+            auto attended = [&](int key) { return key <= pmax && key >= key_lo; };
+            auto load_k = [&](int s) {
+                const uint8_t *p = c.k + sm.off[s >> per_sh] + ((s & per_mask) * 16 + gq) * st + tq * KB;
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int i = 0; i < KL; ++i)
-                        load_bytes<KB>(p + (gq + r * 8) * c.st + i * 4 * KB + tq * KB, &kw[r][i * (KB / 4)]);
+                for (int i = 0; i < KL; ++i) {
+                    load_bytes<KB>(p + i * 4 * KB, &kw[0][i * (KB / 4)]);
+                    load_bytes<KB>(p + 8 * st + i * 4 * KB, &kw[1][i * (KB / 4)]);
+                }
             };
-            auto load_v = [&](int page, int key) {
-                const uint8_t *p = c.v + (int64_t)page * c.sp + head_off + (int64_t)(key % c.bs) * c.st;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    load_bytes<VB>(p + (tq * 2 + (i & 1) + (i >> 1) * 8) * c.st + gq * VB, vw[i]);
+            auto load_v = [&](int s) {
+                const uint8_t *p = c.v + sm.off[s >> per_sh] + ((s & per_mask) * 16 + tq * 2) * st + gq * VB;
+                load_bytes<VB>(p, vw[0]);
+                load_bytes<VB>(p + st, vw[1]);
+                load_bytes<VB>(p + 8 * st, vw[2]);
+                load_bytes<VB>(p + 9 * st, vw[3]);
             };
-            int page, key;
-            int s = next_step(warp, page, key);
-            if (s < steps) {
-                load_k(page, key);
-                load_v(page, key);
+            int s = warp, key = step_key(s);
+            bool have = attended(key);
+            if (have) {
+                load_k(s);
+                load_v(s);
             }
-            while (s < steps) {
-                const int e = s / per;
-                const float ks = sm.ks[e], lv = sm.lv[e], iv = sm.iv[e];
-                const int key_now = key;
-                const int s_next = next_step(s + kWarps, page, key);
+            if (tid < ne) {
+                float ks = 0.f, vs = 1.f;
+                if (my_page >= 0) {
+                    ks = c.ks[(int64_t)my_page * c.Hkv + u.kvh];
+                    vs = fmaxf(c.vs[(int64_t)my_page * c.Hkv + u.kvh], kScaleFloor);
+                }
+                sm.sc[tid] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+                if (sel && my_page >= 0) {  // an entry that its row has before is left out: no row attends its keys
+                    bool twice = false;
+                    for (int k = 0; k < e0 + tid - u.begin; ++k)
+                        twice |= a.idx[irow + k] == my_block;
+                    if (twice) {
+                        bad = true;
+                        sm.key0[tid] = kNoKey;
+                    }
+                }
+            }
+            __syncthreads();
+            if (sel)
+                key = step_key(s);
+            for (; s < steps; s += kWarps) {
+                const int key_now = key, s_now = s;
+                key = step_key(s + kWarps);
+                const bool next = attended(key);
+                if (!have) {
+                    have = next;
+                    if (next) {
+                        load_k(s + kWarps);
+                        load_v(s + kWarps);
+                    }
+                    continue;
+                }
+                have = next;
                 // ---- S^T = K q^T
-                float sc[NT][4];
+                float x[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        sc[n][i] = 0.f;
+                        x[n][i] = 0.f;
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    const uint32_t af[4] = {e4m3_to_half2(kw[0][k] & 0xffffu), e4m3_to_half2(kw[1][k] & 0xffffu),
-                                            e4m3_to_half2(kw[0][k] >> 16), e4m3_to_half2(kw[1][k] >> 16)};
+                    uint32_t af[4];
+                    e4m3x4_to_half(kw[0][k], af[0], af[2]);
+                    e4m3x4_to_half(kw[1][k], af[1], af[3]);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint2 bf = sm.qf[0][k][n][lane];
-                        mma_f16(sc[n], af, bf.x, bf.y);
+                        mma_f16(x[n], af, bf.x, bf.y);
                         if constexpr (SPLIT) {
                             const uint2 bl = sm.qf[SPLIT ? 1 : 0][k][n][lane];
-                            mma_f16(sc[n], af, bl.x, bl.y);
+                            mma_f16(x[n], af, bl.x, bl.y);
                         }
                     }
                 }
-                if (s_next < steps)
-                    load_k(page, key);  // in flight over the softmax and the second product
+                if (next)
+                    load_k(s + kWarps);  // in flight over the softmax and the second product
                 // ---- w = 2^(x + log2 vs - M)
-                const bool part = key_now + 15 > pmin || key_now + 16 > len || (g.window > 0 && key_now <= pmax - g.window);
+                const float4 sc = sm.sc[s_now >> per_sh];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float f = sc.x * sm.qmul[n * 8 + tq * 2 + i];
+                        x[n][i] = fmaf(x[n][i], f, sc.y);
+                        x[n][i + 2] = fmaf(x[n][i + 2], f, sc.y);
+                    }
+                // keys past a row's own, left of its window, or of an entry that is left out
+                const bool part = key_now + 15 > pmin || (g.window > 0 && key_now <= pmax - g.window);
+                if (part) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int kk = key_now + gq + (i >> 1) * 8, p = sm.pos[n * 8 + tq * 2 + (i & 1)];
+                            if (kk > p || (g.window > 0 && kk <= p - g.window))
+                                x[n][i] = -INFINITY;
+                        }
+                }
                 bool raise = false;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x = sc[n][i] * (ks * qm[n][i & 1]) + lv;
-                        if (part) {
-                            const int kk = key_now + gq + (i >> 1) * 8, p = pos[n][i & 1];
-                            if (kk > p || kk >= len || (g.window > 0 && kk <= p - g.window))
-                                x = -INFINITY;
-                        }
-                        sc[n][i] = x;
-                        raise |= x > m[n][i & 1] + kLazy;
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        raise |= fmaxf(x[n][i], x[n][i + 2]) > m[n][i] + kLazy;
                 if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            float x = fmaxf(sc[n][i], sc[n][i + 2]);
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-                            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                            const float mn = fmaxf(m[n][i], x);
-                            const float f = exp2f(m[n][i] - mn);
-                            m[n][i] = mn;
+                            float y = fmaxf(x[n][i], x[n][i + 2]);
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+                            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+                            y = fmaxf(y, m[n][i]);
+                            const float f = exp2f(m[n][i] - y);
+                            m[n][i] = y;
                             l[n][i] *= f;
 #pragma unroll
                             for (int j = 0; j < MT; ++j) {
@@ -486,16 +546,16 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        sc[n][i] = tc::ex2(sc[n][i] - m[n][i & 1]);
-                        l[n][i & 1] += sc[n][i] * iv;
+                        x[n][i] = tc::ex2(x[n][i] - m[n][i & 1]);
+                        l[n][i & 1] = fmaf(x[n][i], sc.z, l[n][i & 1]);
                     }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint32_t hi = pack_half(sc[n][2 * i], sc[n][2 * i + 1]);
+                        const uint32_t hi = pack_half(x[n][2 * i], x[n][2 * i + 1]);
                         pb[0][n][i] = transpose8x8(hi);
                         if constexpr (SPLIT) {
                             const float2 f = __half22float2(*(const __half2 *)&hi);
-                            pb[SPLIT ? 1 : 0][n][i] = transpose8x8(pack_half(sc[n][2 * i] - f.x, sc[n][2 * i + 1] - f.y));
+                            pb[SPLIT ? 1 : 0][n][i] = transpose8x8(pack_half(x[n][2 * i] - f.x, x[n][2 * i + 1] - f.y));
                         }
                     }
                 }
@@ -505,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int kk = key_now + tq * 2 + (i & 1) + (i >> 1) * 8;
-                        const bool out = kk > pmax || kk >= len || (g.window > 0 && kk <= pmin - g.window);
+                        const bool out = kk > pmax || (g.window > 0 && kk <= pmin - g.window);
 #pragma unroll
                         for (int w = 0; w < VW; ++w) {
                             if (out)
@@ -536,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                                         for (int n = 0; n < NT; ++n)
 #pragma unroll
                                             for (int h = 0; h < 2; ++h)
-                                                if (kk <= pos[n][h] && !(g.window > 0 && kk <= pos[n][h] - g.window))
+                                                if (const int p = sm.pos[n * 8 + tq * 2 + h]; kk <= p && !(g.window > 0 && kk <= p - g.window))
                                                     o[n][(4 * w + y) / 2][(y % 2) * 2 + h] = __int_as_float(0x7fffffff);
                                     }
                             }
@@ -554,10 +614,9 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 for (int w = 0; w < VW; ++w)
 #pragma unroll
                     for (int hf = 0; hf < 2; ++hf) {
-                        const uint32_t lo2 = __byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140);
-                        const uint32_t hi2 = __byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140);
-                        const uint32_t af[4] = {e4m3_to_half2(lo2 & 0xffffu), e4m3_to_half2(lo2 >> 16),
-                                                e4m3_to_half2(hi2 & 0xffffu), e4m3_to_half2(hi2 >> 16)};
+                        uint32_t af[4];
+                        e4m3x4_to_half(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), af[0], af[1]);
+                        e4m3x4_to_half(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), af[2], af[3]);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             mma_f16(o[n][w * 2 + hf], af, pb[0][n][0], pb[0][n][1]);
@@ -565,14 +624,12 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                                 mma_f16(o[n][w * 2 + hf], af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
                         }
                     }
-                if (s_next < steps)
-                    load_v(page, key);
-                s = s_next;
+                if (next)
+                    load_v(s_now + kWarps);
             }
         }
 
-        // ---- the warps' sums joined: statistics, then O in two rounds of
-        // half the warps (shared memory for 4)
+        // ---- the warps' sums joined in shared memory
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -581,80 +638,47 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
                 x += __shfl_xor_sync(0xffffffffu, x, 4);
                 x += __shfl_xor_sync(0xffffffffu, x, 8);
                 x += __shfl_xor_sync(0xffffffffu, x, 16);
-                if (gq == 0) {
-                    sm.m[warp][n * 8 + tq * 2 + i] = m[n][i];
-                    sm.l[warp][n * 8 + tq * 2 + i] = x;
+                const int r = n * 8 + tq * 2 + i;
+                if (gq == 0)
+                    sm.ml[warp][r] = make_float2(m[n][i], x);
+                if (r < u.nrows) {
+#pragma unroll
+                    for (int j = 0; j < MT; j += 2)  // dimensions gq * VB + 2 j ..
+                        *(float4 *)&sm.o[warp][r][gq * VB + 2 * j] = make_float4(o[n][j][i], o[n][j][i + 2], o[n][j + 1][i], o[n][j + 1][i + 2]);
                 }
             }
         __syncthreads();
-        constexpr int PER = R * D / kThreads > 0 ? R * D / kThreads : 1;  // outputs per thread
-        float acc[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            acc[i] = 0.f;
-#pragma unroll
-        for (int round = 0; round < 2; ++round) {
-            if (warp / (kWarps / 2) == round) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = n * 8 + tq * 2 + i;
-                        float top = kNoMax;
-#pragma unroll
-                        for (int w = 0; w < kWarps; ++w)
-                            top = fmaxf(top, sm.m[w][r]);
-                        const float f = exp2f(m[n][i] - top);
-#pragma unroll
-                        for (int j = 0; j < MT; ++j) {
-                            sm.o[warp % (kWarps / 2)][r][gq * VB + 2 * j] = o[n][j][i] * f;
-                            sm.o[warp % (kWarps / 2)][r][gq * VB + 2 * j + 1] = o[n][j][i + 2] * f;
-                        }
-                    }
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int x = i * kThreads + tid;
-                if (x < R * D)
-#pragma unroll
-                    for (int w = 0; w < kWarps / 2; ++w)
-                        acc[i] += sm.o[w][x / D][x % D];
-            }
-            __syncthreads();
-        }
         const bool whole = at == u.begin && seg1 == u.begin + u.count;
         // a part: the first of the run in slot 0, its last in slot 1 (a run
         // within one unit has one part)
-        const int64_t slot = (int64_t)cta * 2 + (at == run0 ? 0 : 1);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int x = i * kThreads + tid, r = x / D, d = x % D;
-            if (x >= R * D || r >= u.nrows)
-                continue;
-            float top = kNoMax, sum = 0.f;
+        const int slot = cta * 2 + (at == run0 ? 0 : 1);
+        for (int x = tid; x < u.nrows * D; x += kThreads) {
+            const int r = x / D, d = x % D;
+            float top = kNoMax, sum = 0.f, acc = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                top = fmaxf(top, sm.m[w][r]);
+                top = fmaxf(top, sm.ml[w][r].x);
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                sum += sm.l[w][r] * exp2f(sm.m[w][r] - top);
+            for (int w = 0; w < kWarps; ++w) {
+                const float2 ml = sm.ml[w][r];
+                const float f = exp2f(ml.x - top);
+                sum += ml.y * f;
+                acc += sm.o[w][r][d] * f;
+            }
             if (!whole) {
-                a.part_o[(slot * R + r) * D + d] = acc[i];
+                a.part_o[((int64_t)slot * R + r) * D + d] = acc;
                 if (d == 0)
                     a.part_ml[slot * R + r] = make_float2(top, sum);
                 continue;
             }
             const int row = u.row0 + r, t = row / g.G, h = u.kvh * g.G + row % g.G;
-            float f = 1.f;
             if (a.sinks) {
-                const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk);
-                f = exp2f(top - mn);
+                const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk), f = exp2f(top - mn);
+                acc *= f;
                 sum = sum * f + exp2f(sk - mn);
                 top = mn;
             }
-            const float y = sum > 0.f || sum != sum ? acc[i] * f / sum : 0.f;
-            ((T *)a.o)[o_off(g, u.b, h, t) + d] = from_f<T>(y);
+            ((T *)a.o)[o_off(g, u.b, h, t) + d] = from_f<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
             if (d == 0)
                 a.lse[stat_off(g, u.b, h, t)] = lse_of(top, sum);
         }
@@ -666,30 +690,36 @@ __global__ void __launch_bounds__(kThreads, NT >= 4 ? 1 : 2) cache_attn_kernel(c
 }
 
 // Joins the parts of the rows that several CTAs worked on, and writes the
-// rows that no CTA saw (no attended page).  A warp per query row; the parts
-// are taken in the order of the CTAs.
-template <typename T, int D> __global__ void __launch_bounds__(256) cache_join_kernel(const AttnArgs a, int R, int *err)
+// rows that no CTA saw (no attended page).  A block per query row, its warps
+// taking the parts in turn, all of their loads in flight together; the order
+// of the sum is that of the CTAs and warps, whatever order they ran in.  The
+// kernel is a programmatic dependent of the main one: it is set up while that
+// runs and waits before it reads what that wrote.
+constexpr int kJoinWarps = 4;
+template <typename T, int D> __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnArgs a, int R, int *err)
 {
+    constexpr int E = D / 32;
     const Geo &g = a.g;
-    const int lane = threadIdx.x & 31;
-    if (blockIdx.x == gridDim.x - 1) {  // the call's error word
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ float part[kJoinWarps][D + 2];
+    if (blockIdx.x == 0) {  // the call's error word
         int bad = 0;
-        for (int i = threadIdx.x; i < a.ncta; i += 256)
-            bad |= a.status[i] != NSA_OK;
-        for (int b = threadIdx.x; b < g.B; b += 256) {
+        for (int b = tid; b < g.B; b += kJoinWarps * 32) {
             const int len = a.c.lens[b];
-            bad |= len < 0 || (int64_t)len > (int64_t)a.c.cols * a.c.bs || query_tokens(g, b) < 0;
+            bad |= len < 0 || len > a.c.cols * a.c.bs || query_tokens(g, b) < 0;
         }
+        dependency_wait();
+        for (int i = tid; i < a.ncta; i += kJoinWarps * 32)
+            bad |= a.status[i] != NSA_OK;
         bad = __syncthreads_or(bad);
-        if (threadIdx.x == 0)
+        if (tid == 0)
             *err = bad ? NSA_ERR_BAD_INDEX : NSA_OK;
         return;
     }
     const bool sel = a.idx != nullptr;
-    const int64_t nrow = (int64_t)g.ntok * g.Hq;
-    for (int64_t w = blockIdx.x * 8 + threadIdx.x / 32; w < nrow; w += (int64_t)(gridDim.x - 1) * 8) {
-        const int h = (int)(w % g.Hq);
-        const int tok = (int)(w / g.Hq);
+    const int nrow = g.ntok * g.Hq;
+    for (int w = blockIdx.x - 1; w < nrow; w += gridDim.x - 1) {
+        const int h = w % g.Hq, tok = w / g.Hq;
         int b, t;
         if (g.thd) {
             b = seq_of_token(g, tok);
@@ -701,72 +731,81 @@ template <typename T, int D> __global__ void __launch_bounds__(256) cache_join_k
             t = tok % g.T;
         }
         const int kvh = h / g.G, hh = h % g.G;
-        int64_t begin, count, total;
-        int r;
+        int count, r, in = 0;
         if (sel) {
-            const int64_t unit = index_row(g, b, kvh, t) * a.row_tiles + hh / R;
             r = hh % R;
-            begin = unit * g.S;
             count = g.S;
-            total = (int64_t)g.ntok * g.Hkv * a.row_tiles * g.S;
         } else {
-            const int row = t * g.G + hh;
-            r = row % R;
             int lo;
-            const int tiles = (query_tokens(g, b) * g.G + R - 1) / R;
+            const int row = t * g.G + hh, tiles = (query_tokens(g, b) * g.G + R - 1) / R;
+            r = row % R;
             count = attended_pages(a, b, lo);
-            begin = (int64_t)a.prefix[b] * g.Hkv + ((int64_t)kvh * tiles + row / R) * count;
-            total = (int64_t)a.prefix[g.B] * g.Hkv;
+            in = (kvh * tiles + row / R) * count;
         }
-        const int64_t nq = (total + a.quantum - 1) / a.quantum;
-        float top = kNoMax, sum = 0.f, acc[D / 32];
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i)
-            acc[i] = 0.f;
+        dependency_wait();
+        int first = 0, last = -1, begin = 0;  // the CTAs with a part of the row
         if (count > 0) {
-            // the first CTA whose run reaches past `begin`
-            auto run_at = [&](int64_t x) { return nq * x / a.ncta * a.quantum; };
-            int64_t cta = begin / a.quantum * a.ncta / max(nq, (int64_t)1);
-            while (cta > 0 && run_at(cta) > begin)
-                --cta;
-            while (min(run_at(cta + 1), total) <= begin)
-                ++cta;
-            if (run_at(cta) <= begin && run_at(cta + 1) >= begin + count)
+            int total;
+            if (sel) {
+                begin = ((int)index_row(g, b, kvh, t) * a.row_tiles + hh / R) * g.S;
+                total = g.ntok * g.Hkv * a.row_tiles * g.S;
+            } else {
+                begin = a.prefix[b] * g.Hkv + in;
+                total = a.prefix[g.B] * g.Hkv;
+            }
+            const Runs runs(total, a);
+            first = runs.cta_of(begin);
+            last = runs.cta_of(begin + count - 1);
+            if (first == last && runs.begin(first) <= begin && runs.begin(first + 1) >= begin + count)
                 continue;  // one CTA had it all and wrote the result
-            const int64_t first = cta;
-            int64_t last = first;
-            for (; last < a.ncta && run_at(last) < begin + count; ++last)
-                if (run_at(last + 1) > run_at(last)) {
-                    const int64_t slot = last * 2 + (run_at(last) >= begin ? 0 : 1);
-                    top = fmaxf(top, a.part_ml[slot * R + r].x);
-                }
-            for (cta = first; cta < last; ++cta)
-                if (run_at(cta + 1) > run_at(cta)) {
-                    const int64_t slot = cta * 2 + (run_at(cta) >= begin ? 0 : 1);
-                    const float2 ml = a.part_ml[slot * R + r];
-                    const float f = exp2f(ml.x - top);
-                    sum += ml.y * f;
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i)
-                        acc[i] += a.part_o[(slot * R + r) * D + i * 32 + lane] * f;
-                }
+            begin = runs.begin(first) >= begin ? 0 : 1;  // slot of the first part; later runs start within the row's entries
         }
-        if (a.sinks) {
-            const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk);
-            const float f = exp2f(top - mn);
-            sum = sum * f + exp2f(sk - mn);
+        float top = kNoMax, sum = 0.f, acc[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i)
+            acc[i] = 0.f;
+#pragma unroll 4
+        for (int c = first + warp; c <= last; c += kJoinWarps) {
+            const int64_t at = (int64_t)(c * 2 + (c == first ? begin : 0)) * R + r;
+            const float2 ml = a.part_ml[at];
+            float x[E];
+#pragma unroll
+            for (int i = 0; i < E; ++i)
+                x[i] = a.part_o[at * D + i * 32 + lane];
+            const float mn = fmaxf(top, ml.x), f0 = exp2f(top - mn), f1 = exp2f(ml.x - mn);
             top = mn;
+            sum = sum * f0 + ml.y * f1;
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-                acc[i] *= f;
+            for (int i = 0; i < E; ++i)
+                acc[i] = acc[i] * f0 + x[i] * f1;
         }
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const float y = sum > 0.f || sum != sum ? acc[i] / sum : 0.f;
-            ((T *)a.o)[o_off(g, b, h, t) + i * 32 + lane] = from_f<T>(y);
+        for (int i = 0; i < E; ++i)
+            part[warp][i * 32 + lane] = acc[i];
+        if (lane == 0) {
+            part[warp][D] = top;
+            part[warp][D + 1] = sum;
         }
-        if (lane == 0)
+        __syncthreads();
+        const float sk = a.sinks ? a.sinks[h] * 1.4426950408889634f : kNoMax;
+        top = sk;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i)
+            top = fmaxf(top, part[i][D]);
+        sum = a.sinks ? exp2f(sk - top) : 0.f;
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            const float f = exp2f(part[i][D] - top);
+            sum += part[i][D + 1] * f;
+            if (tid < D)
+                y += part[i][tid] * f;
+        }
+        if (tid < D)
+            ((T *)a.o)[o_off(g, b, h, t) + tid] = from_f<T>(sum > 0.f || sum != sum ? y / sum : 0.f);
+        if (tid == 0)
             a.lse[stat_off(g, b, h, t)] = lse_of(top, sum);
+        __syncthreads();
     }
 }
 
@@ -777,7 +816,7 @@ int row_tile(const Geo &g, bool sel)
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
-int ctas_of(const Geo &g, bool sel) { return num_sms() * (row_tile(g, sel) >= 4 ? 1 : 2); }
+int ctas_of(const Geo &g, bool sel) { return num_sms() * attn_ctas(row_tile(g, sel)); }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -788,13 +827,12 @@ template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cu
     cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess)
         return e;
-    cache_attn_kernel<T, D, NT><<<a.ncta, kThreads, smem, st>>>(a);
+    cache_attn_kernel<T, D, NT><<<a.ncta, attn_warps(NT) * 32, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const int64_t rows = (int64_t)a.g.ntok * a.g.Hq;
-    const int64_t blocks = (rows + 7) / 8, most = (int64_t)num_sms() * 8;
-    cache_join_kernel<T, D><<<(unsigned)(blocks < most ? blocks : most) + 1, 256, 0, st>>>(a, NT * 8, err);
-    return cudaGetLastError();
+    const int64_t rows = (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 16;
+    return launch_dependent(cache_join_kernel<T, D>, dim3((unsigned)(rows < most ? rows : most) + 1), dim3(kJoinWarps * 32), 0, st,
+                            a, NT * 8, err);
 }
 
 template <typename T> cudaError_t attn_d(const AttnArgs &a, int nt, int *err, cudaStream_t st)
@@ -830,6 +868,13 @@ AttnLayout attn_layout(const Geo &g, bool sel)
 }
 
 }  // namespace
+
+int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)
+{
+    const int R = row_tile(g, sel) * 8;
+    return sel ? (int64_t)g.ntok * g.Hkv * g.S * ((g.G + R - 1) / R)
+               : (int64_t)g.B * c.cols * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
+}
 
 size_t cache_attn_ws_bytes(const Geo &g, bool sel) { return attn_layout(g, sel).total; }
 

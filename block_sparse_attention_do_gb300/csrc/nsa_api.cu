@@ -1122,7 +1122,7 @@ nsa_status make_cache(const nsa_cache *p, bool meta, bool counts, bool data, Cac
         c.sp = c.sh * p->Hkv;
     } else {
         for (int i = 0; i < 3; ++i)
-            if (s[i] <= 0 || s[i] % 16 != 0 || s[i] >= ((int64_t)1 << 40))
+            if (s[i] <= 0 || s[i] % 16 != 0 || s[i] >= ((int64_t)1 << (i == 2 ? 24 : 40)))
                 return NSA_ERR_INVALID_ARG;
         c.sp = s[0];
         c.sh = s[1];
@@ -1333,7 +1333,7 @@ nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t wind
         ((uintptr_t)sinks & 3u) || (block_idx && sinks))
         return NSA_ERR_INVALID_ARG;
     // the list of pages is counted in int, and its prefix over the sequences sits in shared memory
-    if (!block_idx && ((int64_t)g.B * c.cols * (((int64_t)g.T * g.G + 7) / 8) >= INT32_MAX || g.B > 8192))
+    if (cache_attn_entries(g, c, block_idx != nullptr) >= INT32_MAX || (!block_idx && g.B > 8192))
         return NSA_ERR_UNSUPPORTED;
     if ((s = check_ws(ws, ws_bytes, cache_attn_ws_bytes(g, block_idx != nullptr))) != NSA_OK)
         return s;

@@ -450,7 +450,8 @@ typedef struct nsa_cache {
     int32_t rows;
     int32_t max_pages;    /* columns of the page table */
     int64_t stride[3];    /* (page, head, token) strides of k and v in bytes; all 0: dense
-                             [num_pages, Hkv, block_size, D].  Multiples of 16, below 2^40 */
+                             [num_pages, Hkv, block_size, D].  Multiples of 16, below 2^40
+                             (the token stride below 2^24) */
     void *k, *v;          /* e4m3 codes, 16-byte aligned */
     float *k_scale, *v_scale; /* [num_pages, Hkv], positive */
     int32_t *page_table, *seq_lens;
