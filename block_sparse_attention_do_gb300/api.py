@@ -668,6 +668,12 @@ def _elsewhere(cache, stream):
     return stream is not None or cache.device.index != torch.cuda.current_device()
 
 
+def _raw_stream(cache):
+    """The current stream of the cache's device (a step of a served batch is
+    a few microseconds: the plain handle, without a Stream object)."""
+    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+
+
 def _there(cache, stream):
     """The caller's stream (else the device's current one) as the context of
     a call, so that what it allocates belongs to that stream."""
@@ -692,7 +698,7 @@ def cache_reserve(cache, n_new, stream=None):
         with _there(cache, stream):
             return cache_reserve(cache, n_new)
     _int32(n_new, "cache_reserve: n_new", cache.device, (cache.struct.rows,))
-    _check(lib().nsa_cache_reserve(cache.ref, n_new.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _stream()),
+    _check(lib().nsa_cache_reserve(cache.ref, n_new.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _raw_stream(cache)),
            "nsa_cache_reserve")
 
 
@@ -703,7 +709,7 @@ def cache_free(cache, rows, stream=None):
             return cache_free(cache, rows)
     _int32(rows, "cache_free: rows", cache.device)
     _check(lib().nsa_cache_free(cache.ref, rows.data_ptr(), rows.numel(), cache.ws.data_ptr(), cache.ws.numel(),
-                                _stream()), "nsa_cache_free")
+                                _raw_stream(cache)), "nsa_cache_free")
 
 
 def cache_fork(cache, src, dst, stream=None):
@@ -715,7 +721,7 @@ def cache_fork(cache, src, dst, stream=None):
     _int32(src, "cache_fork: src", cache.device)
     _int32(dst, "cache_fork: dst", cache.device, src.shape)
     _check(lib().nsa_cache_fork(cache.ref, src.data_ptr(), dst.data_ptr(), src.numel(), cache.ws.data_ptr(),
-                                cache.ws.numel(), _stream()), "nsa_cache_fork")
+                                cache.ws.numel(), _raw_stream(cache)), "nsa_cache_fork")
 
 
 def cache_copy(cache, src, dst, stream=None):
@@ -726,7 +732,7 @@ def cache_copy(cache, src, dst, stream=None):
     _int32(src, "cache_copy: src", cache.device)
     _int32(dst, "cache_copy: dst", cache.device, src.shape)
     _check(lib().nsa_cache_copy(cache.ref, src.data_ptr(), dst.data_ptr(), src.numel(), cache.ws.data_ptr(),
-                                cache.ws.numel(), _stream()), "nsa_cache_copy")
+                                cache.ws.numel(), _raw_stream(cache)), "nsa_cache_copy")
 
 
 def cache_compact(cache, stream=None):
@@ -734,7 +740,7 @@ def cache_compact(cache, stream=None):
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_compact(cache)
-    _check(lib().nsa_cache_compact(cache.ref, cache.ws.data_ptr(), cache.ws.numel(), _stream()), "nsa_cache_compact")
+    _check(lib().nsa_cache_compact(cache.ref, cache.ws.data_ptr(), cache.ws.numel(), _raw_stream(cache)), "nsa_cache_compact")
 
 
 def cache_append(cache, k, v, cu_seqlens=None, max_seqlen=None, stream=None):
@@ -752,7 +758,7 @@ def cache_append(cache, k, v, cu_seqlens=None, max_seqlen=None, stream=None):
         return
     _, p, _ = cache.problem(k, 1, None, cu_seqlens, longest, False, False)
     _check(lib().nsa_cache_append(p, cache.ref, cu_seqlens.data_ptr() if cu_seqlens is not None else None, k.data_ptr(),
-                                  v.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _stream()), "nsa_cache_append")
+                                  v.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _raw_stream(cache)), "nsa_cache_append")
 
 
 def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=None, window=None, sinks=None, ws=None,
@@ -787,5 +793,5 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
                                block_idx.data_ptr() if block_idx is not None else None,
                                sinks.data_ptr() if sinks is not None else None, q.data_ptr(), o.data_ptr(),
-                               lse.data_ptr(), ws.data_ptr(), ws.numel(), _stream()), "nsa_cache_fwd")
+                               lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(cache)), "nsa_cache_fwd")
     return o, lse

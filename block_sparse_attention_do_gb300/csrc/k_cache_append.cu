@@ -76,20 +76,20 @@ __device__ __forceinline__ bool writable(const Cache &c, int page)
 }
 
 // Every row and every page that the call writes, checked by one block of the
-// launch, which alone writes the error word: it needs no clearing.
-__device__ void append_check(const Geo &g, const Cache &c, int *err)
+// launch, which alone writes the error word: it needs no clearing.  A thread
+// takes one (row, touched page) at a time, so its few dependent reads are
+// under way for all of them together.
+__device__ void append_check(const Geo &g, const Cache &c, int per_row, int *err)
 {
     int bad = 0;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int b = warp; b < c.rows; b += kCta / 32) {
+#pragma unroll 4
+    for (int64_t i = threadIdx.x; i < (int64_t)c.rows * per_row; i += kCta) {
+        const int b = (int)(i / per_row), j = (int)(i % per_row);
         int n, start;
-        if (!new_tokens(g, c, b, n, start)) {
+        if (!new_tokens(g, c, b, n, start))
             bad = 1;
-            continue;
-        }
-        for (int col = start / c.bs + lane; n > 0 && col <= (start + n - 1) / c.bs; col += 32)
-            if (!writable(c, c.table[(int64_t)b * c.cols + col]))
-                bad = 1;
+        else if (n > 0 && start / c.bs + j <= (start + n - 1) / c.bs)
+            bad |= !writable(c, c.table[(int64_t)b * c.cols + start / c.bs + j]);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0)
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
     constexpr int N = Vec16<T>::N;
     __shared__ float red[kCta / 32];
     if (blockIdx.x == gridDim.x - 1) {
-        append_check(g, c, err);
+        append_check(g, c, per_row, err);
         return;
     }
     const int64_t unit = blockIdx.x * (int64_t)(kCta / GROUP) + threadIdx.x / GROUP;

@@ -32,6 +32,8 @@
 // busy, and tcgen05 would take the codes through shared memory first.
 #include <math.h>
 
+#include <atomic>
+
 #include "cache_common.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
@@ -47,6 +49,7 @@ namespace {
 __host__ __device__ constexpr int attn_warps(int nt) { return nt == 2 ? 6 : 8; }
 __host__ __device__ constexpr int attn_ctas(int nt) { return nt >= 4 ? 1 : 2; }
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
+constexpr int kMaxRows = 8192;   // sequences of a call without an index (their prefix sits in shared memory)
 constexpr int kNoKey = 0x7f000000; // position of the keys of an entry that is left out
 constexpr float kLazy = 10.f;    // w may reach 2^10 before its row's maximum is raised (half holds 2^15)
 
@@ -94,6 +97,36 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// E (1, 2, 4) consecutive elements of a row as floats
+template <int E> __device__ __forceinline__ void load_row(const float *p, float (&x)[E])
+{
+    if constexpr (E == 4) {
+        const float4 v = *(const float4 *)p;
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else if constexpr (E == 2) {
+        const float2 v = *(const float2 *)p;
+        x[0] = v.x, x[1] = v.y;
+    } else
+        x[0] = *p;
+}
+template <int E> __device__ __forceinline__ void load_row(const __nv_bfloat16 *p, float (&x)[E])
+{
+    if constexpr (E >= 2) {
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const float2 v = __bfloat1622float2(*(const __nv_bfloat162 *)(p + i));
+            x[i] = v.x, x[i + 1] = v.y;
+        }
+    } else
+        x[0] = __bfloat162float(*p);
+}
+// four outputs of a row
+__device__ __forceinline__ void store4(float *p, const float4 &x) { *(float4 *)p = x; }
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &x)
+{
+    *(uint2 *)p = make_uint2(tc::pack_bf16(x.x, x.y), tc::pack_bf16(x.z, x.w));
 }
 
 // BYTES (4, 8, 16) consecutive bytes as words
@@ -318,17 +351,28 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
             }
             return j;
         };
-        auto list_page = [&](int j) {
-            int page = -1;
-            if (j >= 0) {
-                page = c.table[(int64_t)u.b * c.cols + j];
-                if (page < 0 || page >= c.pages) {
-                    bad = true;
-                    page = -1;
-                }
+        auto list_page = [&](int j) { return j >= 0 ? c.table[(int64_t)u.b * c.cols + j] : -1; };
+        auto in_pool = [&](int j, int page) {
+            if (j >= 0 && (page < 0 || page >= c.pages)) {
+                bad = true;
+                page = -1;
             }
             return page;
         };
+        // the tile's queries, E elements of a row per lane, then the first
+        // page ids: all under way together
+        constexpr int E = D / 32, QR = (R + kWarps - 1) / kWarps;
+        float qx[QR][E];
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            const int r = warp + i * kWarps, row = u.row0 + r;
+            if (r < u.nrows)
+                load_row<E>((const T *)a.q + q_off(g, u.b, u.kvh * g.G + row % g.G, row / g.G) + lane * E, qx[i]);
+            else
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    qx[i][e] = 0.f;
+        }
         int my_block = -1, my_page = -1;
         if (at + tid < min(seg1, at + kList)) {
             my_block = list_block(at + tid);
@@ -338,17 +382,15 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         // ---- queries into fragments: element (k, n) of B is row n's element
         // k, in the order of the head dimension that the K loads give
         __syncthreads();  // the previous unit is done with shared memory
-        for (int r = warp; r < R; r += kWarps) {
-            const bool have = r < u.nrows;
-            const int row = u.row0 + r, t = row / g.G, h = u.kvh * g.G + row % g.G;
-            constexpr int E = D / 32;
-            float x[E];
+#pragma unroll
+        for (int i = 0; i < QR; ++i) {
+            const int r = warp + i * kWarps;
+            if (r >= R)
+                break;
             float amax = 0.f;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                x[e] = have ? to_f<T>(((const T *)a.q)[q_off(g, u.b, h, t) + e * 32 + lane]) : 0.f;
-                amax = fmaxf(amax, fabsf(x[e]));
-            }
+            for (int e = 0; e < E; ++e)
+                amax = fmaxf(amax, fabsf(qx[i][e]));
             amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // of values >= 0
             // the row's largest element to [2^14, 2^15)
             const int be = (int)(__float_as_uint(amax) >> 23);  // biased exponent (0: none, 255: infinity)
@@ -356,25 +398,24 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
             const float up = __uint_as_float((uint32_t)(127 + e2) << 23);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const int d = e * 32 + lane;
-                // dimension d sits in load i, thread column tqd, byte k of the
-                // load: word k / 4 is a k-step, bytes 0-1 its low and 2-3 its high half
-                const int i = d / (4 * KB), tqd = d / KB % 4, k = d % KB;
-                const int step = i * (KB / 4) + k / 4, slot = k % 4;
-                const float y = x[e] * up;
+                const int d = lane * E + e;
+                // dimension d sits in load d / (4 KB), thread column d / KB % 4,
+                // byte d % KB of the load: word / 4 is a k-step, bytes 0-1 its
+                // low and 2-3 its high half
+                const int tqd = d / KB % 4, k = d % KB;
+                const int step = d / (4 * KB) * (KB / 4) + k / 4, slot = k % 4;
+                const float y = qx[i][e] * up;
                 const __half hi = __float2half_rn(y);
-                __half *f = (__half *)&sm.qf[0][step][r / 8][(r % 8) * 4 + tqd];
-                f[slot] = hi;
-                if constexpr (SPLIT) {
-                    __half *f2 = (__half *)&sm.qf[SPLIT ? 1 : 0][step][r / 8][(r % 8) * 4 + tqd];
-                    f2[slot] = __float2half_rn(y - __half2float(hi));
-                }
+                ((__half *)&sm.qf[0][step][r / 8][(r % 8) * 4 + tqd])[slot] = hi;
+                if constexpr (SPLIT)
+                    ((__half *)&sm.qf[SPLIT ? 1 : 0][step][r / 8][(r % 8) * 4 + tqd])[slot] = __float2half_rn(y - __half2float(hi));
             }
             if (lane == 0) {
                 sm.qmul[r] = g.scale_l2 * __uint_as_float((uint32_t)(127 - e2) << 23);
-                sm.pos[r] = have ? pos0 + t : -1;
+                sm.pos[r] = r < u.nrows ? pos0 + (u.row0 + r) / g.G : -1;
             }
         }
+        my_page = in_pool(my_block, my_page);
 
         float o[NT][MT][4];
         float m[NT][2], l[NT][2];
@@ -399,7 +440,7 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                 my_block = my_page = -1;
                 if (tid < ne) {
                     my_block = list_block(e0 + tid);
-                    my_page = list_page(my_block);
+                    my_page = in_pool(my_block, list_page(my_block));
                 }
                 __syncthreads();  // the list before is used up
             }
@@ -652,35 +693,49 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         // a part: the first of the run in slot 0, its last in slot 1 (a run
         // within one unit has one part)
         const int slot = cta * 2 + (at == run0 ? 0 : 1);
-        for (int x = tid; x < u.nrows * D; x += kThreads) {
-            const int r = x / D, d = x % D;
-            float top = kNoMax, sum = 0.f, acc = 0.f;
+        for (int r = warp; r < u.nrows; r += kWarps) {  // the rows' statistics, lane w holding warp w's
+            const float2 ml = lane < kWarps ? sm.ml[lane][r] : make_float2(kNoMax, 0.f);
+            float top = ml.x;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w)
-                top = fmaxf(top, sm.ml[w][r].x);
+            for (int i = 4; i > 0; i >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+            float f = exp2f(ml.x - top), sum = ml.y * f;
+#pragma unroll
+            for (int i = 4; i > 0; i >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, i);
+            if (!whole) {
+                if (lane == 0)
+                    a.part_ml[slot * R + r] = make_float2(top, sum);
+            } else {
+                const int row = u.row0 + r, t = row / g.G, h = u.kvh * g.G + row % g.G;
+                if (a.sinks) {
+                    const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk), g0 = exp2f(top - mn);
+                    sum = sum * g0 + exp2f(sk - mn);
+                    f *= g0;
+                    top = mn;
+                }
+                f = sum > 0.f || sum != sum ? f / sum : 0.f;
+                if (lane == 0)
+                    a.lse[stat_off(g, u.b, h, t)] = lse_of(top, sum);
+            }
+            if (lane < kWarps)
+                sm.ml[lane][r].x = f;  // from here on the warp's factor
+        }
+        __syncthreads();
+        for (int x = tid; x < u.nrows * (D / 4); x += kThreads) {
+            const int r = x / (D / 4), d = x % (D / 4) * 4;
+            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float2 ml = sm.ml[w][r];
-                const float f = exp2f(ml.x - top);
-                sum += ml.y * f;
-                acc += sm.o[w][r][d] * f;
+                const float4 p = *(const float4 *)&sm.o[w][r][d];
+                const float f = sm.ml[w][r].x;
+                y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
             }
-            if (!whole) {
-                a.part_o[((int64_t)slot * R + r) * D + d] = acc;
-                if (d == 0)
-                    a.part_ml[slot * R + r] = make_float2(top, sum);
-                continue;
-            }
-            const int row = u.row0 + r, t = row / g.G, h = u.kvh * g.G + row % g.G;
-            if (a.sinks) {
-                const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk), f = exp2f(top - mn);
-                acc *= f;
-                sum = sum * f + exp2f(sk - mn);
-                top = mn;
-            }
-            ((T *)a.o)[o_off(g, u.b, h, t) + d] = from_f<T>(sum > 0.f || sum != sum ? acc / sum : 0.f);
-            if (d == 0)
-                a.lse[stat_off(g, u.b, h, t)] = lse_of(top, sum);
+            if (whole) {
+                const int row = u.row0 + r;
+                store4((T *)a.o + o_off(g, u.b, u.kvh * g.G + row % g.G, row / g.G) + d, y);
+            } else
+                *(float4 *)&a.part_o[((int64_t)slot * R + r) * D + d] = y;
         }
         at = seg1;
     }
@@ -690,26 +745,29 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
 }
 
 // Joins the parts of the rows that several CTAs worked on, and writes the
-// rows that no CTA saw (no attended page).  A block per query row, its warps
-// taking the parts in turn, all of their loads in flight together; the order
-// of the sum is that of the CTAs and warps, whatever order they ran in.  The
-// kernel is a programmatic dependent of the main one: it is set up while that
-// runs and waits before it reads what that wrote.
-constexpr int kJoinWarps = 4;
-template <typename T, int D> __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnArgs a, int R, int *err)
+// rows that no CTA saw (no attended page).  A block per query row: first the
+// parts' maxima and sums, a thread each, then their vectors, the warps taking
+// the parts in turn with several loads in flight; the order of the sums is
+// that of CTAs and warps, whatever order they ran in.  The kernel is a
+// programmatic dependent of the main one: it is set up while that runs and
+// waits before it reads what that wrote.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttnArgs a, int R, int *err)
 {
     constexpr int E = D / 32;
     const Geo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    __shared__ float part[kJoinWarps][D + 2];
+    __shared__ float part[kJoinWarps][D];
+    __shared__ float factor[kJoinThreads], red[2][kJoinWarps];
     if (blockIdx.x == 0) {  // the call's error word
         int bad = 0;
-        for (int b = tid; b < g.B; b += kJoinWarps * 32) {
+        for (int b = tid; b < g.B; b += kJoinThreads) {
             const int len = a.c.lens[b];
             bad |= len < 0 || len > a.c.cols * a.c.bs || query_tokens(g, b) < 0;
         }
         dependency_wait();
-        for (int i = tid; i < a.ncta; i += kJoinWarps * 32)
+        for (int i = tid; i < a.ncta; i += kJoinThreads)
             bad |= a.status[i] != NSA_OK;
         bad = __syncthreads_or(bad);
         if (tid == 0)
@@ -760,49 +818,74 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinWarps * 32) 
                 continue;  // one CTA had it all and wrote the result
             begin = runs.begin(first) >= begin ? 0 : 1;  // slot of the first part; later runs start within the row's entries
         }
-        float top = kNoMax, sum = 0.f, acc[E];
+        const float sk = a.sinks ? a.sinks[h] * 1.4426950408889634f : kNoMax;
+        auto part_of = [&](int c) { return (int64_t)(c * 2 + (c == first ? begin : 0)) * R + r; };
+        float top = sk, sum = a.sinks ? 1.f : 0.f, acc[E];
 #pragma unroll
         for (int i = 0; i < E; ++i)
             acc[i] = 0.f;
-#pragma unroll 4
-        for (int c = first + warp; c <= last; c += kJoinWarps) {
-            const int64_t at = (int64_t)(c * 2 + (c == first ? begin : 0)) * R + r;
-            const float2 ml = a.part_ml[at];
-            float x[E];
+        for (int c0 = first; c0 <= last; c0 += kJoinThreads) {  // one round unless a row has over 256 parts
+            const int c = c0 + tid, n = min(kJoinThreads, last - c0 + 1);
+            const float2 ml = c <= last ? a.part_ml[part_of(c)] : make_float2(kNoMax, 0.f);
+            float x[4][E];  // the warp's first vectors, under way with the maxima
 #pragma unroll
-            for (int i = 0; i < E; ++i)
-                x[i] = a.part_o[at * D + i * 32 + lane];
-            const float mn = fmaxf(top, ml.x), f0 = exp2f(top - mn), f1 = exp2f(ml.x - mn);
+            for (int k = 0; k < 4; ++k)
+                if (warp + k * kJoinWarps < n)
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        x[k][i] = a.part_o[part_of(c0 + warp + k * kJoinWarps) * D + i * 32 + lane];
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            if (lane == 0)
+                red[0][warp] = m;
+            __syncthreads();
+            float mn = top;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k)
+                mn = fmaxf(mn, red[0][k]);
+            const float f = exp2f(ml.x - mn), older = exp2f(top - mn);
+            factor[tid] = f;
+            float s = ml.y * f;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (lane == 0)
+                red[1][warp] = s;
+            __syncthreads();
+            sum *= older;
+#pragma unroll
+            for (int k = 0; k < kJoinWarps; ++k)
+                sum += red[1][k];
             top = mn;
-            sum = sum * f0 + ml.y * f1;
 #pragma unroll
             for (int i = 0; i < E; ++i)
-                acc[i] = acc[i] * f0 + x[i] * f1;
+                acc[i] *= older;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (warp + k * kJoinWarps < n)
+#pragma unroll
+                    for (int i = 0; i < E; ++i)
+                        acc[i] += x[k][i] * factor[warp + k * kJoinWarps];
+#pragma unroll 4
+            for (int p = warp + 4 * kJoinWarps; p < n; p += kJoinWarps)
+#pragma unroll
+                for (int i = 0; i < E; ++i)
+                    acc[i] += a.part_o[part_of(c0 + p) * D + i * 32 + lane] * factor[p];
+            __syncthreads();
         }
 #pragma unroll
         for (int i = 0; i < E; ++i)
             part[warp][i * 32 + lane] = acc[i];
-        if (lane == 0) {
-            part[warp][D] = top;
-            part[warp][D + 1] = sum;
-        }
         __syncthreads();
-        const float sk = a.sinks ? a.sinks[h] * 1.4426950408889634f : kNoMax;
-        top = sk;
+        if (tid < D) {
+            float y = 0.f;
 #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i)
-            top = fmaxf(top, part[i][D]);
-        sum = a.sinks ? exp2f(sk - top) : 0.f;
-        float y = 0.f;
-#pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) {
-            const float f = exp2f(part[i][D] - top);
-            sum += part[i][D + 1] * f;
-            if (tid < D)
-                y += part[i][tid] * f;
-        }
-        if (tid < D)
+            for (int k = 0; k < kJoinWarps; ++k)
+                y += part[k][tid];
             ((T *)a.o)[o_off(g, b, h, t) + tid] = from_f<T>(sum > 0.f || sum != sum ? y / sum : 0.f);
+        }
         if (tid == 0)
             a.lse[stat_off(g, b, h, t)] = lse_of(top, sum);
         __syncthreads();
@@ -824,14 +907,26 @@ template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cu
 {
     using SM = Smem<D, NT, sizeof(T) == 4>;
     const size_t smem = sizeof(SM) + (a.idx ? 0 : sizeof(int) * (size_t)(a.g.B + 1));
-    cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the largest size that a call can ask for, set once per device
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
+    if (dev >= 64 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
+        e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(sizeof(SM) + sizeof(int) * (kMaxRows + 1)));
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            set.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+    }
     cache_attn_kernel<T, D, NT><<<a.ncta, attn_warps(NT) * 32, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
-    const int64_t rows = (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 16;
-    return launch_dependent(cache_join_kernel<T, D>, dim3((unsigned)(rows < most ? rows : most) + 1), dim3(kJoinWarps * 32), 0, st,
+    // index rows that are whole (see launch_cache_attn) leave nothing to join: the error word alone
+    const int64_t rows = a.idx && a.quantum == a.g.S ? 0 : (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 8;
+    return launch_dependent(cache_join_kernel<T, D>, dim3((unsigned)(rows < most ? rows : most) + 1), dim3(kJoinThreads), 0, st,
                             a, NT * 8, err);
 }
 
@@ -869,6 +964,8 @@ AttnLayout attn_layout(const Geo &g, bool sel)
 
 }  // namespace
 
+int cache_attn_max_rows() { return kMaxRows; }
+
 int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)
 {
     const int R = row_tile(g, sel) * 8;
@@ -894,10 +991,12 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     const int nt = row_tile(g, sel);
     a.row_tiles = (g.G + nt * 8 - 1) / (nt * 8);
     a.ncta = ctas_of(g, sel);
-    // a run is cut at multiples of 128 tokens, a step of the CTA's 8 warps;
-    // with many index rows at the rows themselves (nothing to join then)
+    // a run is cut at multiples of 128 tokens, a step of the CTA's warps; of
+    // index rows, whole ones where that leaves the fullest CTA at most a
+    // quarter above the average (nothing is to join then)
     a.quantum = 128 / c.bs;
-    if (sel && (int64_t)g.ntok * g.Hkv * a.row_tiles >= 4 * (int64_t)a.ncta)
+    const int64_t units = (int64_t)g.ntok * g.Hkv * a.row_tiles;
+    if (sel && (units + a.ncta - 1) / a.ncta * a.ncta * 4 <= units * 5)
         a.quantum = g.S;
     a.status = (int *)(ws + w.status);
     a.prefix = (int *)(ws + w.prefix);

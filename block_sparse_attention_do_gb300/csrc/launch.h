@@ -145,6 +145,7 @@ cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, 
 cudaError_t launch_cache_append(const Geo &g, const Cache &c, const void *k, const void *v, int dtype, int *err,
                                 cudaStream_t st);
 size_t cache_attn_ws_bytes(const Geo &g, bool sel);
+int cache_attn_max_rows();  // sequences of a call without an index
 // upper bound on the call's list of pages (counted in int)
 int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel);
 cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const int *idx, const float *sinks, void *o,

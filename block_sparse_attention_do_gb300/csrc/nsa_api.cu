@@ -1333,7 +1333,7 @@ nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t wind
         ((uintptr_t)sinks & 3u) || (block_idx && sinks))
         return NSA_ERR_INVALID_ARG;
     // the list of pages is counted in int, and its prefix over the sequences sits in shared memory
-    if (cache_attn_entries(g, c, block_idx != nullptr) >= INT32_MAX || (!block_idx && g.B > 8192))
+    if (cache_attn_entries(g, c, block_idx != nullptr) >= INT32_MAX || (!block_idx && g.B > cache_attn_max_rows()))
         return NSA_ERR_UNSUPPORTED;
     if ((s = check_ws(ws, ws_bytes, cache_attn_ws_bytes(g, block_idx != nullptr))) != NSA_OK)
         return s;
