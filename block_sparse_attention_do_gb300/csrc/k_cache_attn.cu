@@ -53,9 +53,34 @@ constexpr int kMaxRows = 8192;   // sequences of a call without an index (their 
 constexpr int kNoKey = 0x7f000000; // position of the keys of an entry that is left out
 constexpr float kLazy = 10.f;    // w may reach 2^10 before its row's maximum is raised (half holds 2^15)
 
+// Division of 0 <= n < 2^31 by a number that the host knows: with 2^(l-1) < d
+// <= 2^l and m = floor(2^(31+l) / d) + 1, m d exceeds 2^(31+l) by at most 2^l,
+// so n m / 2^(31+l) has the quotient as its whole part.
+struct FastDiv {
+    int d;
+    uint32_t m, sh;
+    FastDiv() = default;
+    explicit FastDiv(int d_) : d(d_)
+    {
+        uint32_t l = 0;
+        while (((int64_t)1 << l) < d)
+            ++l;
+        sh = 31 + l;
+        m = (uint32_t)(((uint64_t)1 << sh) / (uint32_t)d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((uint64_t)(uint32_t)n * m >> sh); }
+    __device__ __forceinline__ int divmod(int n, int &rem) const
+    {
+        const int q = div(n);
+        rem = n - q * d;
+        return q;
+    }
+};
+
 struct AttnArgs {
     Geo g;
     Cache c;
+    FastDiv by_G, by_Hkv, by_Hq, by_T, by_S, by_tiles, by_ncta, by_quantum;  // of G, .., row_tiles, ncta, quantum
     const void *q;
     const int *idx;      // selection: [.., S], else nullptr
     const float *sinks;  // or nullptr
@@ -186,20 +211,18 @@ struct UnitRows {
 
 // The list cut into equal runs, one per CTA, at multiples of the quantum.
 struct Runs {
-    int total, quantum, ncta, per, rem;
-    __device__ __forceinline__ Runs(int total_, const AttnArgs &a) : total(total_), quantum(a.quantum), ncta(a.ncta)
+    int total, quantum, per, rem;
+    __device__ __forceinline__ Runs(int total_, const AttnArgs &a) : total(total_), quantum(a.quantum)
     {
-        const int nq = (total + quantum - 1) / quantum;
-        per = nq / ncta;
-        rem = nq % ncta;
+        per = a.by_ncta.divmod(a.by_quantum.div(total + quantum - 1), rem);
     }
     __device__ __forceinline__ int begin(int cta) const
     {
         return (int)min((int64_t)total, (int64_t)(cta * per + min(cta, rem)) * quantum);
     }
-    __device__ __forceinline__ int cta_of(int entry) const
+    __device__ __forceinline__ int cta_of(int entry, const AttnArgs &a) const
     {
-        const int q = entry / quantum, longer = rem * (per + 1);
+        const int q = a.by_quantum.div(entry), longer = rem * (per + 1);
         return q < longer ? q / (per + 1) : rem + (q - longer) / max(per, 1);
     }
 };
@@ -213,6 +236,7 @@ template <int D, int NT, bool SPLIT> struct Smem {
     uint2 qf[SPLIT ? 2 : 1][KS][NT][32];
     float qmul[R];  // scale * log2(e) * 2^-e of each row
     int pos[R];     // key position of each row's token (-1: no such row)
+    int64_t o_at[R], lse_at[R];  // its places in o and lse
     int64_t off[kList];  // of the listed entries: byte offset of the page and head
     int key0[kList];     // first key (kNoKey: left out)
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
@@ -291,22 +315,17 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         // ---- the unit that holds list entry `at`
         UnitRows u;
         if (sel) {
-            const int unit = at / g.S;
+            const int unit = a.by_S.div(at);
             u.begin = unit * g.S;
             u.count = g.S;
-            const int rt = unit % a.row_tiles, row = unit / a.row_tiles;  // row: of the index
-            int t;
+            int rt, t;
+            const int row = a.by_tiles.divmod(unit, rt);  // of the index
             if (g.thd) {
-                const int tok = row / g.Hkv;
-                u.kvh = row % g.Hkv;
+                const int tok = a.by_Hkv.divmod(row, u.kvh);
                 u.b = seq_of_token(g, tok);
                 t = tok - g.cu[u.b];
-            } else {
-                t = row % g.T;
-                const int bg = row / g.T;
-                u.b = bg / g.Hkv;
-                u.kvh = bg % g.Hkv;
-            }
+            } else
+                u.b = a.by_Hkv.divmod(a.by_T.divmod(row, t), u.kvh);
             u.row0 = t * g.G + rt * R;
             u.nrows = t < query_tokens(g, u.b) ? min(R, g.G - rt * R) : 0;  // 0: a token of no sequence
             u.page_lo = 0;
@@ -324,8 +343,8 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
             const int in = (at - prefix[lo] * g.Hkv) / n;  // (kv head, row tile)
             u.begin = prefix[lo] * g.Hkv + in * n;
             u.count = n;
-            u.kvh = in / tiles;
-            u.row0 = in % tiles * R;
+            u.kvh = tiles == 1 ? in : in / tiles;
+            u.row0 = tiles == 1 ? 0 : in % tiles * R;
             u.nrows = min(R, query_tokens(g, lo) * g.G - u.row0);
         }
         const int seg1 = min(run1, u.begin + u.count);
@@ -335,7 +354,7 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         }
         const int len = held_tokens(a, u.b);
         const int pos0 = len - query_tokens(g, u.b);  // position of the sequence's first query token
-        const int t_first = u.row0 / g.G, t_last = (u.row0 + u.nrows - 1) / g.G;
+        const int t_first = a.by_G.div(u.row0), t_last = a.by_G.div(u.row0 + u.nrows - 1);
         const int pmin = pos0 + t_first, pmax = pos0 + t_last;  // of the tile's rows
         const int key_lo = g.window > 0 ? pmin - g.window - 14 : INT32_MIN;  // steps before it lie left of every window
 
@@ -363,12 +382,19 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         // page ids: all under way together
         constexpr int E = D / 32, QR = (R + kWarps - 1) / kWarps;
         float qx[QR][E];
+        int row_pos[QR];
+        int64_t row_o[QR], row_lse[QR];
 #pragma unroll
         for (int i = 0; i < QR; ++i) {
-            const int r = warp + i * kWarps, row = u.row0 + r;
-            if (r < u.nrows)
-                load_row<E>((const T *)a.q + q_off(g, u.b, u.kvh * g.G + row % g.G, row / g.G) + lane * E, qx[i]);
-            else
+            const int r = warp + i * kWarps;
+            if (r < u.nrows) {
+                int hh;
+                const int t = a.by_G.divmod(u.row0 + r, hh), h = u.kvh * g.G + hh;
+                load_row<E>((const T *)a.q + q_off(g, u.b, h, t) + lane * E, qx[i]);
+                row_pos[i] = pos0 + t;
+                row_o[i] = o_off(g, u.b, h, t);
+                row_lse[i] = stat_off(g, u.b, h, t);
+            } else
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     qx[i][e] = 0.f;
@@ -412,7 +438,9 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
             }
             if (lane == 0) {
                 sm.qmul[r] = g.scale_l2 * __uint_as_float((uint32_t)(127 - e2) << 23);
-                sm.pos[r] = r < u.nrows ? pos0 + (u.row0 + r) / g.G : -1;
+                sm.pos[r] = r < u.nrows ? row_pos[i] : -1;
+                sm.o_at[r] = row_o[i];
+                sm.lse_at[r] = row_lse[i];
             }
         }
         my_page = in_pool(my_block, my_page);
@@ -601,7 +629,7 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                     }
                 }
                 // ---- values that a row does not attend must not reach it, whatever they hold
-                unsigned nan_words = 0;  // bit (i * VW + w): word w of token i holds a NaN
+                bool nan = false;
                 if (part) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -612,59 +640,56 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                             if (out)
                                 vw[i][w] = 0u;
                             const uint32_t x = vw[i][w] & 0x7f7f7f7fu;
-                            if ((x + 0x01010101u) & 0x80808080u)
-                                nan_words |= 1u << (i * VW + w);
+                            nan |= ((x + 0x01010101u) & 0x80808080u) != 0;
                         }
                     }
                 }
-                const bool any_nan = part && __any_sync(0xffffffffu, nan_words != 0);
-                if (any_nan) {
-                    // a NaN value: it goes, whole, to the rows that attend its
-                    // token and to no other (0 * NaN would reach them all)
-#pragma unroll 1
-                    for (int from = 0; from < 4; ++from)
+                // ---- O^T += V^T P^T
+                if (!(part && __any_sync(0xffffffffu, nan))) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                    for (int w = 0; w < VW; ++w)
 #pragma unroll
-                            for (int w = 0; w < VW; ++w) {
-                                const uint32_t x = __shfl_sync(0xffffffffu, vw[i][w], (lane & ~3) | from);
-                                const int kk = key_now + from * 2 + (i & 1) + (i >> 1) * 8;
+                        for (int hf = 0; hf < 2; ++hf) {
+                            uint32_t af[4];
+                            e4m3x4_to_half(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), af[0], af[1]);
+                            e4m3x4_to_half(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), af[2], af[3]);
 #pragma unroll
-                                for (int y = 0; y < 4; ++y)
-                                    if (((x >> (8 * y)) & 0x7fu) == 0x7fu) {
-                                        // byte 4 w + y of the thread's dimensions: tile (4w + y) / 2, half y % 2
-#pragma unroll
-                                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                                            for (int h = 0; h < 2; ++h)
-                                                if (const int p = sm.pos[n * 8 + tq * 2 + h]; kk <= p && !(g.window > 0 && kk <= p - g.window))
-                                                    o[n][(4 * w + y) / 2][(y % 2) * 2 + h] = __int_as_float(0x7fffffff);
-                                    }
+                            for (int n = 0; n < NT; ++n) {
+                                mma_f16(o[n][w * 2 + hf], af, pb[0][n][0], pb[0][n][1]);
+                                if constexpr (SPLIT)
+                                    mma_f16(o[n][w * 2 + hf], af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
                             }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                        }
+                } else {
+                    // a NaN among the values: token by token, and the rows
+                    // that do not attend the token keep their sums (0 * NaN
+                    // would reach them)
+#pragma unroll 1
+                    for (int tok = 0; tok < 16; ++tok) {
+                        const int mine = tok - tq * 2;  // 0, 1, 8, 9: token `tok` is this thread's i = 0, 1, 2, 3
 #pragma unroll
                         for (int w = 0; w < VW; ++w)
 #pragma unroll
-                            for (int y = 0; y < 4; ++y)
-                                if (((vw[i][w] >> (8 * y)) & 0x7fu) == 0x7fu)
-                                    vw[i][w] &= ~(0xffu << (8 * y));
-                }
-                // ---- O^T += V^T P^T
+                            for (int hf = 0; hf < 2; ++hf) {
+                                uint32_t af[4];
+                                e4m3x4_to_half(__byte_perm(mine == 0 ? vw[0][w] : 0u, mine == 1 ? vw[1][w] : 0u, hf ? 0x7362 : 0x5140), af[0], af[1]);
+                                e4m3x4_to_half(__byte_perm(mine == 8 ? vw[2][w] : 0u, mine == 9 ? vw[3][w] : 0u, hf ? 0x7362 : 0x5140), af[2], af[3]);
 #pragma unroll
-                for (int w = 0; w < VW; ++w)
+                                for (int n = 0; n < NT; ++n) {
+                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                    mma_f16(d, af, pb[0][n][0], pb[0][n][1]);
+                                    if constexpr (SPLIT)
+                                        mma_f16(d, af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        uint32_t af[4];
-                        e4m3x4_to_half(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), af[0], af[1]);
-                        e4m3x4_to_half(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), af[2], af[3]);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16(o[n][w * 2 + hf], af, pb[0][n][0], pb[0][n][1]);
-                            if constexpr (SPLIT)
-                                mma_f16(o[n][w * 2 + hf], af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
-                        }
+                                    for (int i = 0; i < 4; ++i) {
+                                        const int p = sm.pos[n * 8 + tq * 2 + (i & 1)], kk = key_now + tok;
+                                        if (kk <= p && !(g.window > 0 && kk <= p - g.window))
+                                            o[n][w * 2 + hf][i] += d[i];
+                                    }
+                                }
+                            }
                     }
+                }
                 if (next)
                     load_v(s_now + kWarps);
             }
@@ -707,8 +732,10 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                 if (lane == 0)
                     a.part_ml[slot * R + r] = make_float2(top, sum);
             } else {
-                const int row = u.row0 + r, t = row / g.G, h = u.kvh * g.G + row % g.G;
                 if (a.sinks) {
+                    int hh;
+                    a.by_G.divmod(u.row0 + r, hh);
+                    const int h = u.kvh * g.G + hh;
                     const float sk = a.sinks[h] * 1.4426950408889634f, mn = fmaxf(top, sk), g0 = exp2f(top - mn);
                     sum = sum * g0 + exp2f(sk - mn);
                     f *= g0;
@@ -716,7 +743,7 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                 }
                 f = sum > 0.f || sum != sum ? f / sum : 0.f;
                 if (lane == 0)
-                    a.lse[stat_off(g, u.b, h, t)] = lse_of(top, sum);
+                    a.lse[sm.lse_at[r]] = lse_of(top, sum);
             }
             if (lane < kWarps)
                 sm.ml[lane][r].x = f;  // from here on the warp's factor
@@ -731,10 +758,9 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                 const float f = sm.ml[w][r].x;
                 y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
             }
-            if (whole) {
-                const int row = u.row0 + r;
-                store4((T *)a.o + o_off(g, u.b, u.kvh * g.G + row % g.G, row / g.G) + d, y);
-            } else
+            if (whole)
+                store4((T *)a.o + sm.o_at[r] + d, y);
+            else
                 *(float4 *)&a.part_o[((int64_t)slot * R + r) * D + d] = y;
         }
         at = seg1;
@@ -777,18 +803,17 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cac
     const bool sel = a.idx != nullptr;
     const int nrow = g.ntok * g.Hq;
     for (int w = blockIdx.x - 1; w < nrow; w += gridDim.x - 1) {
-        const int h = w % g.Hq, tok = w / g.Hq;
-        int b, t;
+        int h, b, t;
+        const int tok = a.by_Hq.divmod(w, h);
         if (g.thd) {
             b = seq_of_token(g, tok);
             t = tok - g.cu[b];
             if (t >= query_tokens(g, b))
                 continue;
-        } else {
-            b = tok / g.T;
-            t = tok % g.T;
-        }
-        const int kvh = h / g.G, hh = h % g.G;
+        } else
+            b = a.by_T.divmod(tok, t);
+        int hh;
+        const int kvh = a.by_G.divmod(h, hh);
         int count, r, in = 0;
         if (sel) {
             r = hh % R;
@@ -812,8 +837,8 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cac
                 total = a.prefix[g.B] * g.Hkv;
             }
             const Runs runs(total, a);
-            first = runs.cta_of(begin);
-            last = runs.cta_of(begin + count - 1);
+            first = runs.cta_of(begin, a);
+            last = runs.cta_of(begin + count - 1, a);
             if (first == last && runs.begin(first) <= begin && runs.begin(first + 1) >= begin + count)
                 continue;  // one CTA had it all and wrote the result
             begin = runs.begin(first) >= begin ? 0 : 1;  // slot of the first part; later runs start within the row's entries
@@ -1002,6 +1027,14 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     a.prefix = (int *)(ws + w.prefix);
     a.part_ml = (float2 *)(ws + w.ml);
     a.part_o = (float *)(ws + w.o);
+    a.by_G = FastDiv(g.G);
+    a.by_Hkv = FastDiv(g.Hkv);
+    a.by_Hq = FastDiv(g.Hq);
+    a.by_T = FastDiv(g.T);
+    a.by_S = FastDiv(max(g.S, 1));
+    a.by_tiles = FastDiv(a.row_tiles);
+    a.by_ncta = FastDiv(a.ncta);
+    a.by_quantum = FastDiv(a.quantum);
     int *err = (int *)ws;
     return dtype == NSA_DTYPE_BF16 ? attn_d<__nv_bfloat16>(a, nt, err, st) : attn_d<float>(a, nt, err, st);
 }
