@@ -1,0 +1,563 @@
+// k_cache_tc.cu -- attention of many new tokens (chunks of prompts) over the
+// paged 8-bit cache on the tcgen05 tensor cores; bf16 queries, D = 64 or 128.
+//
+// The formulas are those of k_cache_attn.cu (scales of a page's values in the
+// exponent, running maximum raised only when a weight would pass 2^10).  Here
+// the products bound the time: 4 D operations per query row and key, so each
+// code is converted once for 256 rows and the conversion leaves the critical
+// path to warps of its own:
+//   4 converter warps   codes from global memory (a tile's loads in flight
+//                       while the one before is converted) to halves in
+//                       shared memory, 128 keys x D, 128-byte swizzled
+//   1 issuing thread    S_q = Q_q K^T and O_q += P_q V for the two tiles of
+//                       128 rows, q = 0, 1, in turn: one tile's softmax runs
+//                       under the other's products
+//   2 x 4 softmax warps a row per thread: maximum, exponentials, P as halves
+//                       over S's own columns of tensor memory
+// Halves hold e4m3 exactly, bf16 queries scaled by a power of two per row
+// exactly (but for elements 2^-29 below the row's largest), and P with 11
+// bits, three more than bf16.  Tensor memory is full: S 2 x 128 columns, O 2 x D.
+#include <math.h>
+
+#include "cache_common.cuh"
+#include "tc_common.cuh"
+
+namespace nsa {
+
+using namespace tc;
+
+namespace {
+
+constexpr int kTileKeys = 128;
+constexpr int kTileRows = 256;  // query rows of a CTA: two tiles of 128
+constexpr int kSoftmaxWarps = 8, kConvWarps = 4;
+constexpr int kThreads = (kSoftmaxWarps + kConvWarps + 1) * 32;
+constexpr int kStages = 2;      // K and V tiles in shared memory
+constexpr int kScaleRing = 4;   // tiles whose page scales are kept: softmax lags the converters by up to 3
+constexpr float kNoMax = -1e30f, kLazy = 10.f;
+
+enum { B_Q, B_KF, B_KE = B_KF + kStages, B_VF = B_KE + kStages, B_VE = B_VF + kStages, B_SF = B_VE + kStages, B_P = B_SF + 2, B_O = B_P + 2, B_COUNT };
+
+struct Params {
+    Geo g;
+    Cache c;
+    const __nv_bfloat16 *q;
+    const float *sinks;
+    __nv_bfloat16 *o;
+    float *lse;
+    int *err;
+    int tiles;    // row tiles of the longest sequence
+    int wait_us;  // bounded-wait limit in microseconds (0: the default)
+};
+
+template <int D> struct Layout {
+    static constexpr int kHalves = D / 64;                 // 128-byte wide column halves
+    static constexpr int kHalf = 128 * 128;                // one half of 128 rows
+    static constexpr int kTile = kHalves * kHalf;          // 128 rows x D halves
+    static constexpr int q = 0, k = 2 * kTile, v = k + kStages * kTile;
+    static constexpr int scales = v + kStages * kTile;     // float4 [kScaleRing][8]
+    static constexpr int bars = scales + kScaleRing * 8 * 16;
+    static constexpr int misc = bars + B_COUNT * 8;        // wait context, tensor memory address, NaN flag
+    static constexpr int total = misc + 32 + 1024;         // and room to align
+};
+
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn)
+{
+    // accumulator f32, A and B f16
+    return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi)
+{
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *(const uint32_t *)&h;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
+// 16-byte chunk c of row r in a tile of 128-byte rows, 128-byte swizzled
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
+
+template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const Params p)
+{
+    using L = Layout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    uint64_t *bars = (uint64_t *)(sm + L::bars);
+    volatile int *ctx = (volatile int *)(sm + L::misc);
+    uint32_t *tmem_slot = (uint32_t *)(sm + L::misc + 8);
+    volatile int *nan_seen = (volatile int *)(sm + L::misc + 16);
+    float4 *scales = (float4 *)(sm + L::scales);
+    const Geo &g = p.g;
+    const Cache &c = p.c;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // the unit: 256 query rows (row = token * G + head) of one kv head, the
+    // latest tokens, which attend the most keys, first
+    const int nbg = g.B * g.Hkv, bg = blockIdx.x % nbg, tile = p.tiles - 1 - blockIdx.x / nbg;
+    const int b = bg / g.Hkv, kvh = bg % g.Hkv;
+    const int nq = seq_len(g, b), cap = c.cols * c.bs, lens = c.lens[b];
+    const int len = min(max(lens, 0), cap);
+    const bool packed_ok = !g.thd || (nq >= 0 && nq <= g.T && g.cu[b] >= 0 && g.cu[b + 1] <= g.ntok);
+    if (tile == p.tiles - 1 && kvh == 0 && threadIdx.x == 0 && (lens != len || !packed_ok))
+        set_error(p.err, NSA_ERR_BAD_INDEX);
+    const int row0 = tile * kTileRows;
+    const int nrows = packed_ok ? min(kTileRows, nq * g.G - row0) : 0;
+    if (nrows <= 0)
+        return;
+    const int pos0 = len - nq;
+    const int pmin = pos0 + row0 / g.G, pmax = pos0 + (row0 + nrows - 1) / g.G;
+    const int key_first = g.window > 0 ? max(0, pmin - g.window + 1) : 0;  // of any row
+    const int j0 = key_first / kTileKeys, ntiles = pmax < 0 ? 0 : pmax / kTileKeys - j0 + 1;
+    // whether some row attends a part of tile j only
+    auto masked = [&](int j) {
+        return (j + 1) * kTileKeys - 1 > pmin || (g.window > 0 && j * kTileKeys <= pmax - g.window);
+    };
+
+    if (threadIdx.x == 0) {
+        ctx[0] = 0;
+        ctx[1] = p.wait_us;
+        *nan_seen = 0;
+        mbar_init(&bars[B_Q], 2 * 128);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&bars[B_KF + s], kConvWarps * 32);
+            mbar_init(&bars[B_VF + s], kConvWarps * 32);
+            mbar_init(&bars[B_KE + s], 1);
+            mbar_init(&bars[B_VE + s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&bars[B_SF + x], 1);
+            mbar_init(&bars[B_P + x], 128);
+        }
+        mbar_init(&bars[B_O], 1);
+        fence_barrier_init();
+    }
+    if (warp == kSoftmaxWarps + kConvWarps) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    constexpr uint32_t TM_S = 0, TM_O = 256;  // S_q at q * 128, O_q at 256 + q * 128
+
+    if (warp < kSoftmaxWarps) {
+        // ------------------------------------------------- softmax, epilogue
+        const int q = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + q * 128 + r;
+        const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool have = q * 128 + r < nrows;
+        const int t = row / g.G, h = kvh * g.G + row % g.G;
+        const int pos = have ? pos0 + t : -1;
+        // the thread's row of Q: to halves, its largest element to [2^14, 2^15)
+        float qmul;
+        {
+            const __nv_bfloat16 *src = p.q + (have ? q_off(g, b, h, t) : 0);
+            uint4 x[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i)
+                x[i] = have ? __ldg((const uint4 *)src + i) : make_uint4(0, 0, 0, 0);
+            uint32_t top = 0;  // largest magnitude's bits
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t lo = u[e] << 16 & 0x7fffffffu, hi = u[e] & 0x7fff0000u;
+                    top = max(top, lo <= 0x7f800000u ? lo : 0u);  // (NaN does not count)
+                    top = max(top, hi <= 0x7f800000u ? hi : 0u);
+                }
+            }
+            const int be = (int)(top >> 23);
+            const int e2 = be == 0 || be == 255 ? 0 : min(max(14 - (be - 127), -120), 120);
+            const float up = __uint_as_float((uint32_t)(127 + e2) << 23);
+            qmul = g.scale_l2 * __uint_as_float((uint32_t)(127 - e2) << 23);
+            const uint32_t base = smem_u32(sm + L::q + q * L::kTile);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_half(__uint_as_float(u[e] << 16) * up, __uint_as_float(u[e] & 0xffff0000u) * up);
+                st_shared_v4(base + (i >> 3) * L::kHalf + chunk_at(r, i & 7), w[0], w[1], w[2], w[3]);
+            }
+            fence_async_smem();
+            mbar_arrive(&bars[B_Q]);
+        }
+        float m = kNoMax, l = 0.f;
+        const int page_sh = 31 - __clz(c.bs);
+        bool ok = true;
+        for (int i = 0; i < ntiles; ++i) {
+            const int j = j0 + i;
+            const bool part = masked(j);
+            const int cmax = pos - j * kTileKeys, cmin = g.window > 0 ? cmax - g.window + 1 : 0;  // the row's columns
+            if (!mbar_wait_warp(&bars[B_SF + q], i & 1, ctx)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const float4 *sc = scales + (i & (kScaleRing - 1)) * 8;
+            const uint32_t s_at = lanes + TM_S + q * 128;
+            // ---- the row's maximum: 16 columns lie in one page
+            float top = -INFINITY;
+#pragma unroll
+            for (int cc = 0; cc < 128; cc += 64) {
+                uint32_t s[64];
+                tmem_ld64(s_at + cc, s);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 64; k += 16) {
+                    float y = -INFINITY;
+                    if (part) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            y = fmaxf(y, cc + k + e <= cmax && cc + k + e >= cmin ? __uint_as_float(s[k + e]) : -INFINITY);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2)
+                            y = max3(y, __uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1]));
+                    }
+                    const float4 f = sc[(cc + k) >> page_sh];
+                    top = fmaxf(top, y == -INFINITY ? y : fmaf(y, f.x * qmul, f.y));
+                }
+            }
+            const bool raise = top > m + kLazy;
+            if (__any_sync(0xffffffffu, raise)) {
+                const float mn = raise ? top : m, f = ex2(m - mn);
+                m = mn;
+                l *= f;
+                if (i > 0) {  // (S_q of this tile follows P_q V of the last one: O_q is at rest)
+#pragma unroll
+                    for (int cc = 0; cc < D; cc += 32) {
+                        uint32_t a[32];
+                        tmem_ld32(lanes + TM_O + q * 128 + cc, a);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
+                        tmem_st32(lanes + TM_O + q * 128 + cc, a);
+                    }
+                    tmem_wait_st();
+                }
+            }
+            // ---- weights: P over the columns of S that have been read
+#pragma unroll
+            for (int cc = 0; cc < 128; cc += 64) {
+                uint32_t s[64], w[32];
+                tmem_ld64(s_at + cc, s);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 64; k += 16) {
+                    const float4 f = sc[(cc + k) >> page_sh];
+                    const float mul = f.x * qmul, add = f.y - m;
+                    const uint64_t mul2 = f2(mul, mul), add2 = f2(add, add);
+                    uint64_t sum2 = f2(0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float x0, x1;
+                        f2_split(f2_fma(f2(__uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1])), mul2, add2), x0, x1);
+                        if (part) {
+                            const int col = cc + k + e;
+                            x0 = col <= cmax && col >= cmin ? x0 : -INFINITY;
+                            x1 = col + 1 <= cmax && col + 1 >= cmin ? x1 : -INFINITY;
+                        }
+                        x0 = ex2(x0);
+                        x1 = ex2(x1);
+                        sum2 = f2_add(sum2, f2(x0, x1));
+                        w[(k + e) >> 1] = pack_half(x0, x1);
+                    }
+                    float a0, a1;
+                    f2_split(sum2, a0, a1);
+                    l = fmaf(a0 + a1, f.z, l);
+                }
+                tmem_st32(s_at + cc / 2, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars[B_P + q]);
+        }
+        // ---- O / l
+        if (ok && ntiles > 0)
+            ok = mbar_wait_warp(&bars[B_O], 0, ctx);
+        if (ok) {
+            tc_fence_after();
+            float f = 1.f;
+            if (p.sinks && have) {
+                const float sk = p.sinks[h] * 1.4426950408889634f, mn = fmaxf(m, sk);
+                f = ex2(m - mn);
+                l = l * f + ex2(sk - mn);
+                m = mn;
+            }
+            const bool some = l > 0.f || l != l;
+            f = some ? f / l : 0.f;
+            // values that were NaN in tiles that some rows attend in part
+            // were taken as 0 there: put them back for the rows that attend them
+            uint32_t nan_dim[D / 32];
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+                nan_dim[x] = 0;
+            if (*nan_seen && have) {
+#pragma unroll 1
+                for (int key = max(key_first, g.window > 0 ? pos - g.window + 1 : 0); key <= pos; ++key) {
+                    if (!masked(key / kTileKeys)) {
+                        key |= kTileKeys - 1;
+                        continue;
+                    }
+                    const int page = c.table[(int64_t)b * c.cols + key / c.bs];
+                    if (page < 0 || page >= c.pages)
+                        continue;
+                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key % c.bs) * c.st;
+#pragma unroll
+                    for (int x = 0; x < D / 4; ++x) {
+                        const uint32_t u = ((const uint32_t *)v)[x] & 0x7f7f7f7fu, hit = (u + 0x01010101u) & 0x80808080u;
+                        // bits 7, 15, 23, 31 to dimensions 4 x ..
+                        nan_dim[x / 8] |= ((hit >> 7 & 1u) | (hit >> 14 & 2u) | (hit >> 21 & 4u) | (hit >> 28 & 8u)) << (x % 8 * 4);
+                    }
+                }
+            }
+            __nv_bfloat16 *dst = p.o + (have ? o_off(g, b, h, t) : 0);
+#pragma unroll
+            for (int cc = 0; cc < D; cc += 32) {
+                uint32_t a[32];
+                if (ntiles > 0) {
+                    tmem_ld32(lanes + TM_O + q * 128 + cc, a);
+                    tmem_wait_ld();
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float y0 = nan_dim[cc / 32] >> (2 * e) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e]) * f;
+                    const float y1 = nan_dim[cc / 32] >> (2 * e + 1) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e + 1]) * f;
+                    w[e] = some && ntiles > 0 ? pack_bf16(y0, y1) : 0u;
+                }
+                if (have)
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *(uint4 *)(dst + cc + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            }
+            if (have)
+                p.lse[stat_off(g, b, h, t)] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        }
+    } else if (warp < kSoftmaxWarps + kConvWarps) {
+        // ------------------------------------------------------- converters
+        // A warp takes 32 keys of a tile, 16 codes per lane and load.
+        constexpr int PER = D / 16;  // lanes of a key; also loads of the warp's 32 keys
+        const int cw = warp - kSoftmaxWarps, sub = lane % PER, key_in = lane / PER;
+        const int page_sh = 31 - __clz(c.bs), npages = kTileKeys >> page_sh;
+        const int st = (int)c.st;
+        const int64_t head = (int64_t)kvh * c.sh + sub * 16;
+        const int last_page = pmax >> page_sh, first_page = key_first >> page_sh;
+        bool bad = false;
+        // ids of the (up to two) pages of the warp's keys; and, in the first
+        // warp, of page `lane` of the tile
+        auto page_id = [&](int j, int pg) {
+            const int n = (j * kTileKeys >> page_sh) + pg;
+            if (j >= j0 + ntiles || n < first_page || n > last_page)
+                return -1;
+            const int id = c.table[(int64_t)b * c.cols + n];
+            return id;
+        };
+        auto check = [&](int id, int j, int pg) {
+            const int n = (j * kTileKeys >> page_sh) + pg;
+            if (j < j0 + ntiles && n >= first_page && n <= last_page && (id < 0 || id >= c.pages)) {
+                bad = true;
+                return -1;
+            }
+            return id;
+        };
+        const int pg0 = cw * 32 >> page_sh, pg1 = (cw * 32 + 16) >> page_sh;
+        int id[2], id_next[2], sid, sid_next;
+        uint4 kx[PER], vx[PER];
+        float ks = 0.f, vs = 1.f;
+        auto load = [&](const uint8_t *pool, int j, uint4 (&x)[PER]) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int in = i * (32 / PER) + key_in, key = j * kTileKeys + cw * 32 + in, page = id[in >> 4];
+                x[i] = page >= 0 && key <= pmax && key >= key_first
+                           ? __ldcs((const uint4 *)(pool + (int64_t)page * c.sp + head + (key & (c.bs - 1)) * st))
+                           : make_uint4(0, 0, 0, 0);
+            }
+        };
+        auto store = [&](uint8_t *to, const uint4 (&x)[PER]) {
+            const uint32_t base = smem_u32(to);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int r = cw * 32 + i * (32 / PER) + key_in;
+                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    e4m3x4_to_half(u[e], w[2 * e], w[2 * e + 1]);
+                // lanes of the second half start with their odd chunk: the
+                // halves' rows share banks
+                const int hf = sub >> 2, ch = (sub & 3) * 2, odd = hf;
+                const uint32_t at = base + hf * L::kHalf;
+                st_shared_v4(at + chunk_at(r, ch + odd), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2], odd ? w[7] : w[3]);
+                st_shared_v4(at + chunk_at(r, ch + 1 - odd), odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6], odd ? w[3] : w[7]);
+            }
+        };
+        auto load_scales = [&](int id_) {
+            if (cw == 0 && lane < npages && id_ >= 0) {
+                ks = c.ks[(int64_t)id_ * c.Hkv + kvh];
+                vs = c.vs[(int64_t)id_ * c.Hkv + kvh];
+            }
+        };
+        id[0] = check(page_id(j0, pg0), j0, pg0);
+        id[1] = check(page_id(j0, pg1), j0, pg1);
+        sid = cw == 0 && lane < npages ? check(page_id(j0, lane), j0, lane) : -1;
+        load(c.k, j0, kx);
+        load(c.v, j0, vx);
+        load_scales(sid);
+        id_next[0] = page_id(j0 + 1, pg0);
+        id_next[1] = page_id(j0 + 1, pg1);
+        sid_next = cw == 0 && lane < npages ? page_id(j0 + 1, lane) : -1;
+        for (int i = 0; i < ntiles; ++i) {
+            const int j = j0 + i, s = i % kStages;
+            // a page that is not in the pool gets weight 0
+            if (cw == 0 && lane < npages) {
+                const float vsc = fmaxf(vs, kScaleFloor);
+                scales[(i & (kScaleRing - 1)) * 8 + lane] = sid >= 0 ? make_float4(ks, log2f(vsc), 1.f / vsc, 0.f) : make_float4(0.f, -INFINITY, 0.f, 0.f);
+            }
+            if (!mbar_wait_warp(&bars[B_KE + s], ((i / kStages) & 1) ^ 1, ctx))
+                break;
+            store(sm + L::k + s * L::kTile, kx);
+            fence_async_smem();
+            mbar_arrive(&bars[B_KF + s]);
+            const int now0 = id[0], now1 = id[1];
+            (void)now0;
+            (void)now1;
+            id[0] = check(id_next[0], j + 1, pg0);
+            id[1] = check(id_next[1], j + 1, pg1);
+            sid = cw == 0 && lane < npages ? check(sid_next, j + 1, lane) : -1;
+            load(c.k, j + 1, kx);
+            load_scales(sid);
+            id_next[0] = page_id(j + 2, pg0);
+            id_next[1] = page_id(j + 2, pg1);
+            sid_next = cw == 0 && lane < npages ? page_id(j + 2, lane) : -1;
+            if (masked(j)) {
+                bool nan = false;
+#pragma unroll
+                for (int y = 0; y < PER; ++y) {
+                    uint32_t *u = (uint32_t *)&vx[y];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t hit = ((u[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        nan |= hit != 0;
+                        hit = (hit >> 7) * 0xffu;  // the whole byte
+                        u[e] &= ~hit;
+                    }
+                }
+                if (nan)
+                    *nan_seen = 1;
+            }
+            if (!mbar_wait_warp(&bars[B_VE + s], ((i / kStages) & 1) ^ 1, ctx))
+                break;
+            store(sm + L::v + s * L::kTile, vx);
+            fence_async_smem();
+            mbar_arrive(&bars[B_VF + s]);
+            load(c.v, j + 1, vx);
+        }
+        if (bad)
+            set_error(p.err, NSA_ERR_BAD_INDEX);
+    } else if (lane == 0) {
+        // -------------------------------------------------------------- MMA
+        const uint32_t idS = idesc_f16(128, 128, false), idO = idesc_f16(128, D, true);
+        const uint32_t q_s = smem_u32(sm + L::q), k_s = smem_u32(sm + L::k), v_s = smem_u32(sm + L::v);
+        auto product_s = [&](int q, int i) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t at = (kk >> 2) * L::kHalf + (kk & 3) * 32;
+                mma_bf16(tmem + TM_S + q * 128, sdesc_sw128(q_s + q * L::kTile + at, 16, 1024),
+                         sdesc_sw128(k_s + (i % kStages) * L::kTile + at, 16, 1024), idS, kk > 0);
+            }
+        };
+        auto product_o = [&](int q, int i) {
+#pragma unroll
+            for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                mma_bf16_ts(tmem + TM_O + q * 128, tmem + TM_S + q * 128 + kk * 8,
+                            sdesc_sw128(v_s + (i % kStages) * L::kTile + kk * 2048, L::kHalf, 1024), idO, i > 0 || kk > 0);
+        };
+        bool ok = ntiles > 0 && mbar_wait(&bars[B_Q], 0, ctx) && mbar_wait(&bars[B_KF], 0, ctx);
+        if (ok) {
+            tc_fence_after();
+            product_s(0, 0);
+            mma_commit(&bars[B_SF + 0]);
+            product_s(1, 0);
+            mma_commit(&bars[B_SF + 1]);
+            mma_commit(&bars[B_KE + 0]);
+        }
+        for (int i = 0; ok && i < ntiles; ++i) {
+            const int s = i % kStages, s1 = (i + 1) % kStages;
+            const bool more = i + 1 < ntiles;
+            ok = mbar_wait(&bars[B_VF + s], (i / kStages) & 1, ctx) &&
+                 (!more || mbar_wait(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx));
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                ok = ok && mbar_wait(&bars[B_P + q], i & 1, ctx);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                product_o(q, i);
+                if (q == 1)
+                    mma_commit(&bars[B_VE + s]);
+                if (more) {  // over P_q, once the product that reads it is done: issued behind it
+                    product_s(q, i + 1);
+                    mma_commit(&bars[B_SF + q]);
+                    if (q == 1)
+                        mma_commit(&bars[B_KE + s1]);
+                }
+            }
+        }
+        // every product completes before tensor memory is freed
+        mma_commit(&bars[B_O]);
+        volatile int never[2] = {0, ctx[1]};  // own limit, no abort
+        mbar_wait(&bars[B_O], 0, never);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (ctx[0] && threadIdx.x == 0)
+        set_error(p.err, NSA_ERR_DEVICE_TIMEOUT);
+    if (warp == kSoftmaxWarps + kConvWarps) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+bool cache_chunk_supported(const Geo &g, int dtype, bool sel)
+{
+    return !sel && dtype == NSA_DTYPE_BF16 && (g.D == 64 || g.D == 128) && (int64_t)g.T * g.G > 64 &&
+           (((int64_t)g.T * g.G + kTileRows - 1) / kTileRows) * g.B * g.Hkv < INT32_MAX;
+}
+
+cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, const float *sinks, void *o, float *lse, int *err,
+                               cudaStream_t st)
+{
+    Params p;
+    p.g = g;
+    p.c = c;
+    p.q = (const __nv_bfloat16 *)q;
+    p.sinks = sinks;
+    p.o = (__nv_bfloat16 *)o;
+    p.lse = lse;
+    p.err = err;
+    p.tiles = (int)(((int64_t)g.T * g.G + kTileRows - 1) / kTileRows);
+    p.wait_us = wait_test().wait_us;
+    auto kernel = g.D == 128 ? cache_chunk_kernel<128> : cache_chunk_kernel<64>;
+    const int smem = g.D == 128 ? Layout<128>::total : Layout<64>::total;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    kernel<<<(unsigned)(p.tiles * g.B * g.Hkv), kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace nsa

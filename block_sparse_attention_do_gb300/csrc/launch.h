@@ -144,6 +144,10 @@ cudaError_t launch_cache_compact(const Cache &c, const CacheWs &ws, cudaStream_t
 cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, cudaStream_t st);
 cudaError_t launch_cache_append(const Geo &g, const Cache &c, const void *k, const void *v, int dtype, int *err,
                                 cudaStream_t st);
+// many query rows per kv head, on tcgen05 (k_cache_tc.cu); *err is zero at launch
+bool cache_chunk_supported(const Geo &g, int dtype, bool sel);
+cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, const float *sinks, void *o, float *lse, int *err,
+                               cudaStream_t st);
 size_t cache_attn_ws_bytes(const Geo &g, bool sel);
 int cache_attn_max_rows();  // sequences of a call without an index
 // upper bound on the call's list of pages (counted in int)
