@@ -6,9 +6,10 @@
 // the products bound the time: 4 D operations per query row and key, so each
 // code is converted once for 256 rows and the conversion leaves the critical
 // path to warps of its own:
-//   4 converter warps   codes from global memory (a tile's loads in flight
-//                       while the one before is converted) to halves in
-//                       shared memory, 128 keys x D, 128-byte swizzled
+//   2 + 2 converter warps  keys' and values' codes from global memory (a
+//                       tile's loads in flight as soon as the one before is
+//                       stored) to halves in shared memory, 128 keys x D,
+//                       128-byte swizzled
 //   1 issuing thread    S_q = Q_q K^T and O_q += P_q V for the two tiles of
 //                       128 rows, q = 0, 1, in turn: one tile's softmax runs
 //                       under the other's products
@@ -31,10 +32,16 @@ namespace {
 constexpr int kTileKeys = 128;
 constexpr int kTileRows = 256;  // query rows of a CTA: two tiles of 128
 constexpr int kSoftmaxWarps = 8, kConvWarps = 4;
-constexpr int kThreads = (kSoftmaxWarps + kConvWarps + 1) * 32;
+constexpr int kThreads = (kSoftmaxWarps + kConvWarps + 4) * 32;  // whole warpgroups: the issuing thread's is the last
+// Registers per thread of the softmax, converter and issuing warpgroups: a
+// row of S (128) stays in registers from its maximum to its exponentials.
+// 256 x 184 + 128 x 104 + 128 x 32 = 64,512 of the launch's 65,536.
+constexpr int kRegsSoftmax = 184, kRegsConv = 104, kRegsMma = 32;
 constexpr int kStages = 2;      // K and V tiles in shared memory
 constexpr int kScaleRing = 4;   // tiles whose page scales are kept: softmax lags the converters by up to 3
 constexpr float kNoMax = -1e30f, kLazy = 10.f;
+constexpr float kTiny = 1.17549435e-38f;    // keeps kNoScore * scale from being a NaN
+constexpr uint32_t kNoScore = 0xff800000u;  // -infinity
 
 enum { B_Q, B_KF, B_KE = B_KF + kStages, B_VF = B_KE + kStages, B_VE = B_VF + kStages, B_SF = B_VE + kStages, B_P = B_SF + 2, B_O = B_P + 2, B_COUNT };
 
@@ -97,19 +104,19 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
     const Cache &c = p.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // the unit: 256 query rows (row = token * G + head) of one kv head, the
-    // latest tokens, which attend the most keys, first
-    const int nbg = g.B * g.Hkv, bg = blockIdx.x % nbg, tile = p.tiles - 1 - blockIdx.x / nbg;
+    // the unit: 256 query rows (row = token * G + head) of one kv head.  Every
+    // sequence's last rows, which attend the most keys, come first
+    const int nbg = g.B * g.Hkv, bg = blockIdx.x % nbg, from_end = blockIdx.x / nbg;
     const int b = bg / g.Hkv, kvh = bg % g.Hkv;
     const int nq = seq_len(g, b), cap = c.cols * c.bs, lens = c.lens[b];
     const int len = min(max(lens, 0), cap);
     const bool packed_ok = !g.thd || (nq >= 0 && nq <= g.T && g.cu[b] >= 0 && g.cu[b + 1] <= g.ntok);
-    if (tile == p.tiles - 1 && kvh == 0 && threadIdx.x == 0 && (lens != len || !packed_ok))
+    if (from_end == 0 && kvh == 0 && threadIdx.x == 0 && (lens != len || !packed_ok))
         set_error(p.err, NSA_ERR_BAD_INDEX);
-    const int row0 = tile * kTileRows;
-    const int nrows = packed_ok ? min(kTileRows, nq * g.G - row0) : 0;
-    if (nrows <= 0)
+    const int tile = packed_ok ? (nq * g.G + kTileRows - 1) / kTileRows - 1 - from_end : -1;
+    if (tile < 0)
         return;
+    const int row0 = tile * kTileRows, nrows = min(kTileRows, nq * g.G - row0);
     const int pos0 = len - nq;
     const int pmin = pos0 + row0 / g.G, pmax = pos0 + (row0 + nrows - 1) / g.G;
     const int key_first = g.window > 0 ? max(0, pmin - g.window + 1) : 0;  // of any row
@@ -125,8 +132,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         *nan_seen = 0;
         mbar_init(&bars[B_Q], 2 * 128);
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&bars[B_KF + s], kConvWarps * 32);
-            mbar_init(&bars[B_VF + s], kConvWarps * 32);
+            mbar_init(&bars[B_KF + s], kConvWarps / 2 * 32);
+            mbar_init(&bars[B_VF + s], kConvWarps / 2 * 32);
             mbar_init(&bars[B_KE + s], 1);
             mbar_init(&bars[B_VE + s], 1);
         }
@@ -149,6 +156,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
 
     if (warp < kSoftmaxWarps) {
         // ------------------------------------------------- softmax, epilogue
+        setmaxnreg_inc<kRegsSoftmax>();
         const int q = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + q * 128 + r;
         const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const bool have = q * 128 + r < nrows;
@@ -204,73 +212,66 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
             tc_fence_after();
             const float4 *sc = scales + (i & (kScaleRing - 1)) * 8;
             const uint32_t s_at = lanes + TM_S + q * 128;
-            // ---- the row's maximum: 16 columns lie in one page
+            uint32_t s[128];
+            tmem_ld64(s_at, *(uint32_t(*)[64])s);
+            tmem_ld64(s_at + 64, *(uint32_t(*)[64])(s + 64));
+            tmem_wait_ld();
+            if (part) {  // columns that the row does not attend count as nothing
+#pragma unroll
+                for (int e = 0; e < 128; ++e)
+                    s[e] = e <= cmax && e >= cmin ? s[e] : kNoScore;
+            }
+            // ---- the row's maximum; 16 columns lie in one page
             float top = -INFINITY;
 #pragma unroll
-            for (int cc = 0; cc < 128; cc += 64) {
-                uint32_t s[64];
-                tmem_ld64(s_at + cc, s);
-                tmem_wait_ld();
+            for (int k = 0; k < 128; k += 16) {
+                float y0 = __uint_as_float(s[k]), y1 = __uint_as_float(s[k + 1]);
 #pragma unroll
-                for (int k = 0; k < 64; k += 16) {
-                    float y = -INFINITY;
-                    if (part) {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            y = fmaxf(y, cc + k + e <= cmax && cc + k + e >= cmin ? __uint_as_float(s[k + e]) : -INFINITY);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2)
-                            y = max3(y, __uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1]));
-                    }
-                    const float4 f = sc[(cc + k) >> page_sh];
-                    top = fmaxf(top, y == -INFINITY ? y : fmaf(y, f.x * qmul, f.y));
+                for (int e = 2; e < 16; e += 4) {
+                    y0 = max3(y0, __uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1]));
+                    if (e + 2 < 16)
+                        y1 = max3(y1, __uint_as_float(s[k + e + 2]), __uint_as_float(s[k + e + 3]));
                 }
+                const float4 f = sc[k >> page_sh];
+                top = fmaxf(top, fmaf(fmaxf(y0, y1), fmaxf(f.x * qmul, kTiny), f.y));
             }
-            const bool raise = top > m + kLazy;
+            const bool raise = top > m + kLazy;  // (no column attended: top is -infinity)
             if (__any_sync(0xffffffffu, raise)) {
                 const float mn = raise ? top : m, f = ex2(m - mn);
                 m = mn;
                 l *= f;
                 if (i > 0) {  // (S_q of this tile follows P_q V of the last one: O_q is at rest)
-#pragma unroll
-                    for (int cc = 0; cc < D; cc += 32) {
-                        uint32_t a[32];
-                        tmem_ld32(lanes + TM_O + q * 128 + cc, a);
+#pragma unroll 1
+                    for (int cc = 0; cc < D; cc += 16) {
+                        uint32_t a[16];
+                        tmem_ld16(lanes + TM_O + q * 128 + cc, a);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
+                        for (int e = 0; e < 16; ++e)
                             a[e] = __float_as_uint(__uint_as_float(a[e]) * f);
-                        tmem_st32(lanes + TM_O + q * 128 + cc, a);
+                        tmem_st16(lanes + TM_O + q * 128 + cc, a);
                     }
                     tmem_wait_st();
                 }
             }
-            // ---- weights: P over the columns of S that have been read
+            // ---- weights: P over the columns of S
 #pragma unroll
             for (int cc = 0; cc < 128; cc += 64) {
-                uint32_t s[64], w[32];
-                tmem_ld64(s_at + cc, s);
-                tmem_wait_ld();
+                uint32_t w[32];
 #pragma unroll
-                for (int k = 0; k < 64; k += 16) {
-                    const float4 f = sc[(cc + k) >> page_sh];
-                    const float mul = f.x * qmul, add = f.y - m;
+                for (int k = cc; k < cc + 64; k += 16) {
+                    const float4 f = sc[k >> page_sh];
+                    const float mul = fmaxf(f.x * qmul, kTiny), add = f.y - m;
                     const uint64_t mul2 = f2(mul, mul), add2 = f2(add, add);
                     uint64_t sum2 = f2(0.f, 0.f);
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float x0, x1;
                         f2_split(f2_fma(f2(__uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1])), mul2, add2), x0, x1);
-                        if (part) {
-                            const int col = cc + k + e;
-                            x0 = col <= cmax && col >= cmin ? x0 : -INFINITY;
-                            x1 = col + 1 <= cmax && col + 1 >= cmin ? x1 : -INFINITY;
-                        }
                         x0 = ex2(x0);
                         x1 = ex2(x1);
                         sum2 = f2_add(sum2, f2(x0, x1));
-                        w[(k + e) >> 1] = pack_half(x0, x1);
+                        w[(k - cc + e) >> 1] = pack_half(x0, x1);
                     }
                     float a0, a1;
                     f2_split(sum2, a0, a1);
@@ -346,126 +347,115 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         }
     } else if (warp < kSoftmaxWarps + kConvWarps) {
         // ------------------------------------------------------- converters
-        // A warp takes 32 keys of a tile, 16 codes per lane and load.
-        constexpr int PER = D / 16;  // lanes of a key; also loads of the warp's 32 keys
-        const int cw = warp - kSoftmaxWarps, sub = lane % PER, key_in = lane / PER;
+        // Two warps take a tile's keys, two its values: a warp half of the
+        // tile's 64 keys, 16 codes per lane and load, and the next tile's are
+        // under way as soon as these are stored.  Lane bits 0-1 (and, with D =
+        // 128, 4) name the 16 codes, the others the key, so that the 8 lanes
+        // of a shared-memory store phase hold two neighbouring keys, whose
+        // swizzled chunks lie in different banks.
+        setmaxnreg_dec<kRegsConv>();
+        constexpr int KEYS = 64, PER_LOAD = D == 128 ? 4 : 8, LOADS = KEYS / PER_LOAD;
+        const int cw = warp - kSoftmaxWarps, half = cw & 1;
+        const bool values = cw >= 2;
+        const int sub = D == 128 ? (lane & 3) | (lane >> 4 & 1) << 2 : lane & 3, key_in = D == 128 ? lane >> 2 & 3 : lane >> 2;
         const int page_sh = 31 - __clz(c.bs), npages = kTileKeys >> page_sh;
         const int st = (int)c.st;
-        const int64_t head = (int64_t)kvh * c.sh + sub * 16;
+        const uint8_t *pool = (values ? c.v : c.k) + (int64_t)kvh * c.sh + sub * 16;
         const int last_page = pmax >> page_sh, first_page = key_first >> page_sh;
         bool bad = false;
-        // ids of the (up to two) pages of the warp's keys; and, in the first
-        // warp, of page `lane` of the tile
-        auto page_id = [&](int j, int pg) {
-            const int n = (j * kTileKeys >> page_sh) + pg;
-            if (j >= j0 + ntiles || n < first_page || n > last_page)
-                return -1;
-            const int id = c.table[(int64_t)b * c.cols + n];
-            return id;
-        };
-        auto check = [&](int id, int j, int pg) {
-            const int n = (j * kTileKeys >> page_sh) + pg;
-            if (j < j0 + ntiles && n >= first_page && n <= last_page && (id < 0 || id >= c.pages)) {
+        // page n of the sequence, -1 where no row attends a key of it
+        auto page_id = [&](int n) { return n < first_page || n > last_page ? -1 : c.table[(int64_t)b * c.cols + n]; };
+        auto in_pool = [&](int id, int n) {
+            if (n >= first_page && n <= last_page && (id < 0 || id >= c.pages)) {
                 bad = true;
                 return -1;
             }
             return id;
         };
-        const int pg0 = cw * 32 >> page_sh, pg1 = (cw * 32 + 16) >> page_sh;
-        int id[2], id_next[2], sid, sid_next;
-        uint4 kx[PER], vx[PER];
+        // lane x holds the id of page x of the tile (of the next one: id_next);
+        // the warp's keys lie in up to 4 of them
+        auto tile_page = [&](int j) { return (j * kTileKeys >> page_sh) + lane; };
+        auto fetch_id = [&](int j) { return lane < npages && j < j0 + ntiles ? page_id(tile_page(j)) : -1; };
+        uint4 x[LOADS];
+        auto load = [&](int j, int id) {
+            const int key0 = j * kTileKeys + half * KEYS + key_in;
+#pragma unroll
+            for (int p = 0; p < KEYS / 16; ++p) {  // 16 keys lie in one page
+                const int page = __shfl_sync(0xffffffffu, id, (half * KEYS + p * 16) >> page_sh);
+                const uint8_t *at = pool + (int64_t)page * c.sp + ((key0 + p * 16) & (c.bs - 1)) * st;
+#pragma unroll
+                for (int i = 0; i < 16 / PER_LOAD; ++i) {
+                    const int key = key0 + p * 16 + i * PER_LOAD;
+                    x[p * (16 / PER_LOAD) + i] = page >= 0 && key <= pmax && key >= key_first ? __ldg((const uint4 *)(at + i * PER_LOAD * st))
+                                                                                              : make_uint4(0, 0, 0, 0);
+                }
+            }
+        };
+        uint64_t *full = &bars[values ? B_VF : B_KF], *empty = &bars[values ? B_VE : B_KE];
+        uint8_t *tiles = sm + (values ? L::v : L::k) + (sub >> 2) * L::kHalf;
+        int id = in_pool(fetch_id(j0), tile_page(j0)), id_next = fetch_id(j0 + 1);
         float ks = 0.f, vs = 1.f;
-        auto load = [&](const uint8_t *pool, int j, uint4 (&x)[PER]) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int in = i * (32 / PER) + key_in, key = j * kTileKeys + cw * 32 + in, page = id[in >> 4];
-                x[i] = page >= 0 && key <= pmax && key >= key_first
-                           ? __ldcs((const uint4 *)(pool + (int64_t)page * c.sp + head + (key & (c.bs - 1)) * st))
-                           : make_uint4(0, 0, 0, 0);
+        auto load_scales = [&]() {
+            if (cw == 0 && id >= 0) {
+                ks = c.ks[(int64_t)id * c.Hkv + kvh];
+                vs = c.vs[(int64_t)id * c.Hkv + kvh];
             }
         };
-        auto store = [&](uint8_t *to, const uint4 (&x)[PER]) {
-            const uint32_t base = smem_u32(to);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int r = cw * 32 + i * (32 / PER) + key_in;
-                const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t w[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    e4m3x4_to_half(u[e], w[2 * e], w[2 * e + 1]);
-                // lanes of the second half start with their odd chunk: the
-                // halves' rows share banks
-                const int hf = sub >> 2, ch = (sub & 3) * 2, odd = hf;
-                const uint32_t at = base + hf * L::kHalf;
-                st_shared_v4(at + chunk_at(r, ch + odd), odd ? w[4] : w[0], odd ? w[5] : w[1], odd ? w[6] : w[2], odd ? w[7] : w[3]);
-                st_shared_v4(at + chunk_at(r, ch + 1 - odd), odd ? w[0] : w[4], odd ? w[1] : w[5], odd ? w[2] : w[6], odd ? w[3] : w[7]);
-            }
-        };
-        auto load_scales = [&](int id_) {
-            if (cw == 0 && lane < npages && id_ >= 0) {
-                ks = c.ks[(int64_t)id_ * c.Hkv + kvh];
-                vs = c.vs[(int64_t)id_ * c.Hkv + kvh];
-            }
-        };
-        id[0] = check(page_id(j0, pg0), j0, pg0);
-        id[1] = check(page_id(j0, pg1), j0, pg1);
-        sid = cw == 0 && lane < npages ? check(page_id(j0, lane), j0, lane) : -1;
-        load(c.k, j0, kx);
-        load(c.v, j0, vx);
-        load_scales(sid);
-        id_next[0] = page_id(j0 + 1, pg0);
-        id_next[1] = page_id(j0 + 1, pg1);
-        sid_next = cw == 0 && lane < npages ? page_id(j0 + 1, lane) : -1;
+        load(j0, id);
+        load_scales();
         for (int i = 0; i < ntiles; ++i) {
             const int j = j0 + i, s = i % kStages;
-            // a page that is not in the pool gets weight 0
+            // (a page that is not in the pool gets weight 0)
             if (cw == 0 && lane < npages) {
                 const float vsc = fmaxf(vs, kScaleFloor);
-                scales[(i & (kScaleRing - 1)) * 8 + lane] = sid >= 0 ? make_float4(ks, log2f(vsc), 1.f / vsc, 0.f) : make_float4(0.f, -INFINITY, 0.f, 0.f);
+                scales[(i & (kScaleRing - 1)) * 8 + lane] = id >= 0 ? make_float4(ks, log2f(vsc), 1.f / vsc, 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
             }
-            if (!mbar_wait_warp(&bars[B_KE + s], ((i / kStages) & 1) ^ 1, ctx))
-                break;
-            store(sm + L::k + s * L::kTile, kx);
-            fence_async_smem();
-            mbar_arrive(&bars[B_KF + s]);
-            const int now0 = id[0], now1 = id[1];
-            (void)now0;
-            (void)now1;
-            id[0] = check(id_next[0], j + 1, pg0);
-            id[1] = check(id_next[1], j + 1, pg1);
-            sid = cw == 0 && lane < npages ? check(sid_next, j + 1, lane) : -1;
-            load(c.k, j + 1, kx);
-            load_scales(sid);
-            id_next[0] = page_id(j + 2, pg0);
-            id_next[1] = page_id(j + 2, pg1);
-            sid_next = cw == 0 && lane < npages ? page_id(j + 2, lane) : -1;
-            if (masked(j)) {
+            if (values && masked(j)) {
+                // a NaN value must not meet the weight 0 of a row that does
+                // not attend it: 0 in its place, and the epilogue told
                 bool nan = false;
 #pragma unroll
-                for (int y = 0; y < PER; ++y) {
-                    uint32_t *u = (uint32_t *)&vx[y];
+                for (int y = 0; y < LOADS; ++y) {
+                    uint32_t *u = (uint32_t *)&x[y];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint32_t hit = ((u[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        const uint32_t hit = ((u[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
                         nan |= hit != 0;
-                        hit = (hit >> 7) * 0xffu;  // the whole byte
-                        u[e] &= ~hit;
+                        u[e] &= ~((hit >> 7) * 0xffu);
                     }
                 }
                 if (nan)
                     *nan_seen = 1;
             }
-            if (!mbar_wait_warp(&bars[B_VE + s], ((i / kStages) & 1) ^ 1, ctx))
+            if (!mbar_wait_warp(&empty[s], ((i / kStages) & 1) ^ 1, ctx))
                 break;
-            store(sm + L::v + s * L::kTile, vx);
+            const uint32_t base = smem_u32(tiles + s * L::kTile);
+            const int ch = (sub & 3) * 2;
+#pragma unroll
+            for (int y = 0; y < LOADS; ++y) {
+                const int r = half * KEYS + y * PER_LOAD + key_in;
+                uint32_t w[8];
+                e4m3x4_to_half(x[y].x, w[0], w[1]);
+                e4m3x4_to_half(x[y].y, w[2], w[3]);
+                e4m3x4_to_half(x[y].z, w[4], w[5]);
+                e4m3x4_to_half(x[y].w, w[6], w[7]);
+                st_shared_v4(base + chunk_at(r, ch), w[0], w[1], w[2], w[3]);
+                st_shared_v4(base + chunk_at(r, ch + 1), w[4], w[5], w[6], w[7]);
+            }
+            id = in_pool(id_next, tile_page(j + 1));
+            if (i + 1 >= ntiles)
+                id = -1;
+            load(j + 1, id);
+            load_scales();
+            id_next = fetch_id(j + 2);
             fence_async_smem();
-            mbar_arrive(&bars[B_VF + s]);
-            load(c.v, j + 1, vx);
+            mbar_arrive(&full[s]);
         }
         if (bad)
             set_error(p.err, NSA_ERR_BAD_INDEX);
-    } else if (lane == 0) {
+    } else {
+        setmaxnreg_dec<kRegsMma>();
+        if (warp == kSoftmaxWarps + kConvWarps && lane == 0) {
         // -------------------------------------------------------------- MMA
         const uint32_t idS = idesc_f16(128, 128, false), idO = idesc_f16(128, D, true);
         const uint32_t q_s = smem_u32(sm + L::q), k_s = smem_u32(sm + L::k), v_s = smem_u32(sm + L::v);
@@ -495,8 +485,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         for (int i = 0; ok && i < ntiles; ++i) {
             const int s = i % kStages, s1 = (i + 1) % kStages;
             const bool more = i + 1 < ntiles;
-            ok = mbar_wait(&bars[B_VF + s], (i / kStages) & 1, ctx) &&
-                 (!more || mbar_wait(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx));
+            ok = mbar_wait(&bars[B_VF + s], (i / kStages) & 1, ctx);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 ok = ok && mbar_wait(&bars[B_P + q], i & 1, ctx);
@@ -506,6 +495,9 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                 product_o(q, i);
                 if (q == 1)
                     mma_commit(&bars[B_VE + s]);
+                ok = !more || q == 1 || mbar_wait(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx);
+                if (!ok)
+                    break;
                 if (more) {  // over P_q, once the product that reads it is done: issued behind it
                     product_s(q, i + 1);
                     mma_commit(&bars[B_SF + q]);
@@ -518,6 +510,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         mma_commit(&bars[B_O]);
         volatile int never[2] = {0, ctx[1]};  // own limit, no abort
         mbar_wait(&bars[B_O], 0, never);
+        }
     }
     __syncwarp();
     tc_fence_before();
