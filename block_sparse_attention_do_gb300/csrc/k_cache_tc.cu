@@ -35,8 +35,8 @@ constexpr int kSoftmaxWarps = 8, kConvWarps = 4;
 constexpr int kThreads = (kSoftmaxWarps + kConvWarps + 4) * 32;  // whole warpgroups: the issuing thread's is the last
 // Registers per thread of the softmax, converter and issuing warpgroups: a
 // row of S (128) stays in registers from its maximum to its exponentials.
-// 256 x 184 + 128 x 104 + 128 x 32 = 64,512 of the launch's 65,536.
-constexpr int kRegsSoftmax = 184, kRegsConv = 104, kRegsMma = 32;
+// 256 x 176 + 128 x 104 + 128 x 56 = 65,536, all that the launch has.
+constexpr int kRegsSoftmax = 176, kRegsConv = 104, kRegsMma = 56;
 constexpr int kStages = 2;      // K and V tiles in shared memory
 constexpr int kScaleRing = 4;   // tiles whose page scales are kept: softmax lags the converters by up to 3
 constexpr float kNoMax = -1e30f, kLazy = 10.f;
@@ -78,6 +78,14 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi)
 {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *(const uint32_t *)&h;
+}
+
+// true in one lane of the warp, always the same
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t y;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
+    return y != 0;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c)
@@ -377,17 +385,30 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         auto tile_page = [&](int j) { return (j * kTileKeys >> page_sh) + lane; };
         auto fetch_id = [&](int j) { return lane < npages && j < j0 + ntiles ? page_id(tile_page(j)) : -1; };
         uint4 x[LOADS];
+        // the warp's codes of tile j; lane n of `id` holds page n of the tile,
+        // and 16 keys lie in one page
         auto load = [&](int j, int id) {
-            const int key0 = j * kTileKeys + half * KEYS + key_in;
+            const int first = j * kTileKeys + half * KEYS;
+            const uint8_t *at[KEYS / 16];
+            bool there[KEYS / 16], all = first >= key_first && first + KEYS - 1 <= pmax;
 #pragma unroll
-            for (int p = 0; p < KEYS / 16; ++p) {  // 16 keys lie in one page
-                const int page = __shfl_sync(0xffffffffu, id, (half * KEYS + p * 16) >> page_sh);
-                const uint8_t *at = pool + (int64_t)page * c.sp + ((key0 + p * 16) & (c.bs - 1)) * st;
+            for (int n = 0; n < KEYS / 16; ++n) {
+                const int page = __shfl_sync(0xffffffffu, id, (half * KEYS + n * 16) >> page_sh);
+                there[n] = page >= 0;
+                all = all && there[n];
+                at[n] = pool + (int64_t)page * c.sp + (((first + n * 16) & (c.bs - 1)) + key_in) * st;
+            }
+            if (all) {
 #pragma unroll
-                for (int i = 0; i < 16 / PER_LOAD; ++i) {
-                    const int key = key0 + p * 16 + i * PER_LOAD;
-                    x[p * (16 / PER_LOAD) + i] = page >= 0 && key <= pmax && key >= key_first ? __ldg((const uint4 *)(at + i * PER_LOAD * st))
-                                                                                              : make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < LOADS; ++y)
+                    x[y] = __ldg((const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st));
+            } else {
+#pragma unroll
+                for (int y = 0; y < LOADS; ++y) {
+                    const int key = first + y * PER_LOAD + key_in;
+                    x[y] = there[y * PER_LOAD / 16] && key <= pmax && key >= key_first
+                               ? __ldg((const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st))
+                               : make_uint4(0, 0, 0, 0);
                 }
             }
         };
@@ -431,6 +452,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                 break;
             const uint32_t base = smem_u32(tiles + s * L::kTile);
             const int ch = (sub & 3) * 2;
+            id = i + 1 < ntiles ? in_pool(id_next, tile_page(j + 1)) : -1;
 #pragma unroll
             for (int y = 0; y < LOADS; ++y) {
                 const int r = half * KEYS + y * PER_LOAD + key_in;
@@ -442,74 +464,90 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                 st_shared_v4(base + chunk_at(r, ch), w[0], w[1], w[2], w[3]);
                 st_shared_v4(base + chunk_at(r, ch + 1), w[4], w[5], w[6], w[7]);
             }
-            id = in_pool(id_next, tile_page(j + 1));
-            if (i + 1 >= ntiles)
-                id = -1;
+            // (the issuing warp orders these writes for the tensor cores: a
+            // proxy fence of every converter costs more)
+            mbar_arrive(&full[s]);
             load(j + 1, id);
             load_scales();
             id_next = fetch_id(j + 2);
-            fence_async_smem();
-            mbar_arrive(&full[s]);
         }
         if (bad)
             set_error(p.err, NSA_ERR_BAD_INDEX);
     } else {
         setmaxnreg_dec<kRegsMma>();
-        if (warp == kSoftmaxWarps + kConvWarps && lane == 0) {
-        // -------------------------------------------------------------- MMA
-        const uint32_t idS = idesc_f16(128, 128, false), idO = idesc_f16(128, D, true);
-        const uint32_t q_s = smem_u32(sm + L::q), k_s = smem_u32(sm + L::k), v_s = smem_u32(sm + L::v);
-        auto product_s = [&](int q, int i) {
+        if (warp == kSoftmaxWarps + kConvWarps) {
+            // ---------------------------------------------------------- MMA
+            // The whole warp walks the loop, so that descriptors stay in
+            // uniform registers, and one elected lane issues.
+            const uint32_t idS = idesc_f16(128, 128, false), idO = idesc_f16(128, D, true);
+            const uint64_t q_d = sdesc_sw128(smem_u32(sm + L::q), 16, 1024), k_d = sdesc_sw128(smem_u32(sm + L::k), 16, 1024),
+                           v_d = sdesc_sw128(smem_u32(sm + L::v), L::kHalf, 1024);
+            auto product_s = [&](int q, int s) {
+                if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t at = (kk >> 2) * L::kHalf + (kk & 3) * 32;
-                mma_bf16(tmem + TM_S + q * 128, sdesc_sw128(q_s + q * L::kTile + at, 16, 1024),
-                         sdesc_sw128(k_s + (i % kStages) * L::kTile + at, 16, 1024), idS, kk > 0);
-            }
-        };
-        auto product_o = [&](int q, int i) {
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const int at = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
+                        mma_bf16(tmem + TM_S + q * 128, q_d + (q * L::kTile >> 4) + at, k_d + (s * L::kTile >> 4) + at, idS, kk > 0);
+                    }
+                }
+                __syncwarp();
+            };
+            auto product_o = [&](int q, int s, bool add) {
+                if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                mma_bf16_ts(tmem + TM_O + q * 128, tmem + TM_S + q * 128 + kk * 8,
-                            sdesc_sw128(v_s + (i % kStages) * L::kTile + kk * 2048, L::kHalf, 1024), idO, i > 0 || kk > 0);
-        };
-        bool ok = ntiles > 0 && mbar_wait(&bars[B_Q], 0, ctx) && mbar_wait(&bars[B_KF], 0, ctx);
-        if (ok) {
-            tc_fence_after();
-            product_s(0, 0);
-            mma_commit(&bars[B_SF + 0]);
-            product_s(1, 0);
-            mma_commit(&bars[B_SF + 1]);
-            mma_commit(&bars[B_KE + 0]);
-        }
-        for (int i = 0; ok && i < ntiles; ++i) {
-            const int s = i % kStages, s1 = (i + 1) % kStages;
-            const bool more = i + 1 < ntiles;
-            ok = mbar_wait(&bars[B_VF + s], (i / kStages) & 1, ctx);
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                ok = ok && mbar_wait(&bars[B_P + q], i & 1, ctx);
-                if (!ok)
-                    break;
+                    for (int kk = 0; kk < kTileKeys / 16; ++kk)
+                        mma_bf16_ts(tmem + TM_O + q * 128, tmem + TM_S + q * 128 + kk * 8, v_d + (s * L::kTile >> 4) + (kk * 2048 >> 4),
+                                    idO, add || kk > 0);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](int bar) {
+                if (elect_one())
+                    mma_commit(&bars[bar]);
+                __syncwarp();
+            };
+            bool ok = ntiles > 0 && mbar_wait_warp(&bars[B_Q], 0, ctx) && mbar_wait_warp(&bars[B_KF], 0, ctx);
+            if (ok) {
+                fence_async_smem();  // the converters' writes, for the tensor cores
                 tc_fence_after();
-                product_o(q, i);
-                if (q == 1)
-                    mma_commit(&bars[B_VE + s]);
-                ok = !more || q == 1 || mbar_wait(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx);
-                if (!ok)
-                    break;
-                if (more) {  // over P_q, once the product that reads it is done: issued behind it
-                    product_s(q, i + 1);
-                    mma_commit(&bars[B_SF + q]);
+                product_s(0, 0);
+                commit(B_SF + 0);
+                product_s(1, 0);
+                commit(B_SF + 1);
+                commit(B_KE + 0);
+            }
+            for (int i = 0; ok && i < ntiles; ++i) {
+                const int s = i % kStages, s1 = (i + 1) % kStages;
+                const bool more = i + 1 < ntiles;
+                ok = mbar_wait_warp(&bars[B_VF + s], (i / kStages) & 1, ctx);
+                fence_async_smem();
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    ok = ok && mbar_wait_warp(&bars[B_P + q], i & 1, ctx);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    product_o(q, s, i > 0);
                     if (q == 1)
-                        mma_commit(&bars[B_KE + s1]);
+                        commit(B_VE + s);
+                    if (!more)
+                        continue;
+                    if (q == 0 && !(ok = mbar_wait_warp(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx)))
+                        break;
+                    if (q == 0)
+                        fence_async_smem();
+                    tc_fence_after();
+                    // over P_q, once the product that reads it is done: issued behind it
+                    product_s(q, s1);
+                    commit(B_SF + q);
+                    if (q == 1)
+                        commit(B_KE + s1);
                 }
             }
-        }
-        // every product completes before tensor memory is freed
-        mma_commit(&bars[B_O]);
-        volatile int never[2] = {0, ctx[1]};  // own limit, no abort
-        mbar_wait(&bars[B_O], 0, never);
+            // every product completes before tensor memory is freed
+            commit(B_O);
+            volatile int never[2] = {0, ctx[1]};  // own limit, no abort
+            mbar_wait(&bars[B_O], 0, never);
         }
     }
     __syncwarp();
