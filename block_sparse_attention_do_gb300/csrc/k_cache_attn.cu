@@ -10,9 +10,9 @@
 //
 // What bounds it: the cache's bytes, 2 D per key and kv head, each read once;
 // 4 G D operations on them are far below the tensor cores' rate (G = 4: 4
-// operations a byte).  So the layout is made for the loads: codes go from
-// global memory straight into the registers of the matrix instruction that
-// consumes them.  The products are taken transposed, tokens (then head
+// operations a byte).  So the layout is made for the loads: every warp keeps
+// its next steps of 16 tokens under way into a ring of its own in shared
+// memory, and no warp waits for another before the end.  The products are taken transposed, tokens (then head
 // dimensions) as the 16 rows of mma.m16n8k16 and query rows as its 8 columns:
 //   S^T[token, row] = K q^T     A: a thread's 16 code bytes of one token are
 //       the pairs of four k-steps, in an order of the head dimension that q's
@@ -42,12 +42,15 @@ namespace nsa {
 
 namespace {
 
-// Warps of a CTA and CTAs of an SM, by the tiles of 8 query rows: a thread
-// holds O in 4 D / 16 registers a tile, and the codes in flight in 32.  One
-// tile: 16 warps an SM of 128 registers; two: 12 of 168 (128 spill); four: 8
-// of 255.
-__host__ __device__ constexpr int attn_warps(int nt) { return nt == 2 ? 6 : 8; }
+// Warps of a CTA, CTAs of an SM and steps of a warp under way, by the tiles of
+// 8 query rows.  A thread holds O in D / 4 registers a tile: up to two tiles 16
+// warps an SM of 128 registers, with four 8 of 255.  16 warps with two steps
+// of 4 KB ahead have 128 KB of codes under way on an SM; the memory's rate
+// times its latency asks for about 50.
+constexpr int kWarps = 8, kThreads = kWarps * 32;
+constexpr int kList = kThreads;  // pages of a run listed at a time, one per thread
 __host__ __device__ constexpr int attn_ctas(int nt) { return nt >= 4 ? 1 : 2; }
+__host__ __device__ constexpr int attn_stages(int nt) { return nt >= 4 ? 4 : 3; }
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 constexpr int kMaxRows = 8192;   // sequences of a call without an index (their prefix sits in shared memory)
 constexpr int kNoKey = 0x7f000000; // position of the keys of an entry that is left out
@@ -154,17 +157,26 @@ __device__ __forceinline__ void store4(__nv_bfloat16 *p, const float4 &x)
     *(uint2 *)p = make_uint2(tc::pack_bf16(x.x, x.y), tc::pack_bf16(x.z, x.w));
 }
 
-// BYTES (4, 8, 16) consecutive bytes as words
-template <int BYTES> __device__ __forceinline__ void load_bytes(const uint8_t *p, uint32_t *w)
+// BYTES (4, 8, 16) consecutive bytes of shared memory as words
+template <int BYTES> __device__ __forceinline__ void load_shared(uint32_t at, uint32_t *w)
 {
-    if constexpr (BYTES == 16) {
-        const uint4 x = __ldcs((const uint4 *)p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else if constexpr (BYTES == 8) {
-        const uint2 x = __ldcs((const uint2 *)p);
-        w[0] = x.x, w[1] = x.y;
-    } else
-        w[0] = __ldcs((const uint32_t *)p);
+    if constexpr (BYTES == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+    else if constexpr (BYTES == 8)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at) : "memory");
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at) : "memory");
+}
+
+// Place, in 16-byte units, of unit u of token t in a step's 16 tokens (D / 16
+// units each): exclusive-ors of the token's bits, so that the lanes that read
+// together find their fragments in different banks.  Keys are read by two
+// neighbouring tokens at a time (rows of 128 bytes would share banks), values
+// by every other token of eight.
+template <int D> __device__ __forceinline__ int k_at(int t, int u) { return (t * (D / 16) + u) ^ (D == 128 ? (t & 1) << 2 : 0); }
+template <int D> __device__ __forceinline__ int v_at(int t, int u)
+{
+    return (t * (D / 16) + u) ^ (D == 128 ? (t >> 1 & 3) << 1 : D == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 1) << 1 : (t >> 2 & 1) << 1);
 }
 
 // query tokens of sequence b; -1 for a packed range that is not one, or is
@@ -229,8 +241,6 @@ struct Runs {
 
 // NT: tiles of 8 query rows; SPLIT: fp32 queries (two halves)
 template <int D, int NT, bool SPLIT> struct Smem {
-    static constexpr int kWarps = attn_warps(NT);
-    static constexpr int kList = kWarps * 32;  // pages of a run listed at a time, one per thread
     static constexpr int R = NT * 8;
     static constexpr int KS = D / 16;  // k-steps of S
     uint2 qf[SPLIT ? 2 : 1][KS][NT][32];
@@ -241,11 +251,14 @@ template <int D, int NT, bool SPLIT> struct Smem {
     int key0[kList];     // first key (kNoKey: left out)
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
     float2 ml[kWarps][R];       // each warp's maximum and sum
-    float o[kWarps][R][D + 4];  // and its part of O
+    union {
+        float o[kWarps][R][D + 4];                     // its part of O
+        uint8_t ring[kWarps][attn_stages(NT)][32 * D];  // its steps under way: 16 tokens' keys, then values
+    };
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(const AttnArgs a)
 {
     constexpr bool SPLIT = sizeof(T) == 4;
     constexpr int R = NT * 8, KS = D / 16, MT = D / 16;
@@ -253,7 +266,7 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
     constexpr int KL = D / 4 / KB;             // K loads per token and thread
     constexpr int VB = D / 8;                  // bytes of a V load: one per token and thread
     constexpr int VW = VB / 4;                 // words
-    constexpr int kWarps = attn_warps(NT), kThreads = kWarps * 32, kList = kThreads;
+    constexpr int kStages = attn_stages(NT), kStageBytes = 32 * D, CPT = D / 16;
     using SM = Smem<D, NT, SPLIT>;
     extern __shared__ __align__(16) char smem_raw[];
     SM &sm = *(SM *)smem_raw;
@@ -307,6 +320,14 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
         __syncthreads();
         total = base * g.Hkv;
     }
+    // the lane's places in a stage of the warp's ring: where it copies to
+    // (16 bytes of each 512, a token's D / 16 units by neighbouring lanes),
+    // and where its fragments lie
+    const uint32_t ring = tc::smem_u32(sm.ring[warp]);
+    const uint32_t to_k = k_at<D>(lane / CPT, lane % CPT) * 16, to_v = 16 * D + v_at<D>(lane / CPT, lane % CPT) * 16;
+    const uint32_t from_k = k_at<D>(gq, tq * KB / 16) * 16 + tq * KB % 16;
+    const uint32_t from_v = 16 * D + v_at<D>(tq * 2, gq * VB / 16) * 16 + gq * VB % 16;
+    const int from_lane = lane / CPT * (int)c.st + lane % CPT * 16;
     const int st = (int)c.st, per_sh = 31 - __clz(c.bs) - 4, per_mask = (1 << per_sh) - 1;  // steps per page
     const Runs runs(total, a);
     const int run0 = runs.begin(cta), run1 = runs.begin(cta + 1);
@@ -480,31 +501,26 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
 
             // ---- 16-token steps of the listed pages, the warps in turn
             const int steps = ne << per_sh;
-            uint32_t kw[2][KL * KB / 4], vw[4][VW];
             // the step's first key; a step that no row attends is not read
             auto step_key = [&](int s) { return s < steps ? sm.key0[s >> per_sh] + (s & per_mask) * 16 : kNoKey; };
             auto attended = [&](int key) { return key <= pmax && key >= key_lo; };
-            auto load_k = [&](int s) {
-                const uint8_t *p = c.k + sm.off[s >> per_sh] + ((s & per_mask) * 16 + gq) * st + tq * KB;
+            // step s into a stage of the warp's ring, 16 bytes per lane and copy
+            auto fetch = [&](int s, int stage) {
+                if (attended(step_key(s))) {
+                    const int64_t from = sm.off[s >> per_sh] + (s & per_mask) * 16 * st + from_lane;
+                    const uint32_t to = ring + stage * kStageBytes;
 #pragma unroll
-                for (int i = 0; i < KL; ++i) {
-                    load_bytes<KB>(p + i * 4 * KB, &kw[0][i * (KB / 4)]);
-                    load_bytes<KB>(p + 8 * st + i * 4 * KB, &kw[1][i * (KB / 4)]);
+                    for (int i = 0; i < D / 32; ++i) {  // 512 bytes, 32 / CPT tokens each
+                        tc::cp_async_16(to + to_k + i * 512, c.k + from + i * (32 / CPT) * st, 16);
+                        tc::cp_async_16(to + (to_v ^ (D == 128 ? (i & 1) << 6 : 0)) + i * 512, c.v + from + i * (32 / CPT) * st, 16);
+                    }
                 }
+                tc::cp_async_commit();
             };
-            auto load_v = [&](int s) {
-                const uint8_t *p = c.v + sm.off[s >> per_sh] + ((s & per_mask) * 16 + tq * 2) * st + gq * VB;
-                load_bytes<VB>(p, vw[0]);
-                load_bytes<VB>(p + st, vw[1]);
-                load_bytes<VB>(p + 8 * st, vw[2]);
-                load_bytes<VB>(p + 9 * st, vw[3]);
-            };
-            int s = warp, key = step_key(s);
-            bool have = attended(key);
-            if (have) {
-                load_k(s);
-                load_v(s);
-            }
+            int stage = 0;
+#pragma unroll
+            for (int i = 0; i < kStages - 1; ++i)
+                fetch(warp + i * kWarps, i);
             if (tid < ne) {
                 float ks = 0.f, vs = 1.f;
                 if (my_page >= 0) {
@@ -523,21 +539,22 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                 }
             }
             __syncthreads();
-            if (sel)
-                key = step_key(s);
-            for (; s < steps; s += kWarps) {
-                const int key_now = key, s_now = s;
-                key = step_key(s + kWarps);
-                const bool next = attended(key);
-                if (!have) {
-                    have = next;
-                    if (next) {
-                        load_k(s + kWarps);
-                        load_v(s + kWarps);
-                    }
+            for (int s = warp; s < steps; s += kWarps) {
+                __syncwarp();  // the stage that is filled now has been read
+                fetch(s + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
+                tc::cp_async_wait<kStages - 1>();
+                __syncwarp();
+                const uint32_t at = ring + stage * kStageBytes;
+                stage = stage == kStages - 1 ? 0 : stage + 1;
+                const int key_now = step_key(s);
+                if (!attended(key_now))
                     continue;
-                }
-                have = next;
+                uint32_t kw[2][KL * KB / 4], vw[4][VW];
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < KL; ++i)
+                        load_shared<KB>(at + (from_k ^ i * 64) + r * 8 * D, &kw[r][i * (KB / 4)]);
                 // ---- S^T = K q^T
                 float x[NT][4];
 #pragma unroll
@@ -560,10 +577,8 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                         }
                     }
                 }
-                if (next)
-                    load_k(s + kWarps);  // in flight over the softmax and the second product
                 // ---- w = 2^(x + log2 vs - M)
-                const float4 sc = sm.sc[s_now >> per_sh];
+                const float4 sc = sm.sc[s >> per_sh];
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -628,6 +643,9 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                         }
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    load_shared<VB>(at + (from_v ^ (i & 1) * D) + (i >> 1) * 8 * D, vw[i]);
                 // ---- values that a row does not attend must not reach it, whatever they hold
                 bool nan = false;
                 if (part) {
@@ -690,12 +708,12 @@ __global__ void __launch_bounds__(attn_warps(NT) * 32, attn_ctas(NT)) cache_attn
                             }
                     }
                 }
-                if (next)
-                    load_v(s_now + kWarps);
             }
+            tc::cp_async_wait<0>();
         }
 
-        // ---- the warps' sums joined in shared memory
+        // ---- the warps' sums joined in shared memory (over the rings)
+        __syncthreads();
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -946,7 +964,7 @@ template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cu
         if (dev < 64)
             set.fetch_or((uint64_t)1 << dev, std::memory_order_release);
     }
-    cache_attn_kernel<T, D, NT><<<a.ncta, attn_warps(NT) * 32, smem, st>>>(a);
+    cache_attn_kernel<T, D, NT><<<a.ncta, kThreads, smem, st>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess)
         return e;
     // index rows that are whole (see launch_cache_attn) leave nothing to join: the error word alone
