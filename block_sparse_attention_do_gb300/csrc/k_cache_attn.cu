@@ -91,9 +91,10 @@ struct AttnArgs {
     float *lse;
     int row_tiles;       // selection: query-row tiles per index row
     int quantum;         // pages that are not cut
+    int start_cost;      // dense: list entries that stand before a unit's pages for what it costs to begin one
     int ncta;            // CTAs of the main kernel
     int *status;         // [ncta]: what each CTA found
-    int *prefix;         // [rows + 1] dense: list entries (pages x row tiles) of one kv head before each sequence
+    int *prefix;         // [rows + 1] dense: list entries of one kv head before each sequence
     float *part_o;       // [ncta * 2][rows of a tile][D]
     float2 *part_ml;     // [ncta * 2][rows of a tile]
 };
@@ -217,7 +218,7 @@ template <int R> __device__ __forceinline__ int row_tiles_of(const Geo &g, int b
 // belongs to it.
 struct UnitRows {
     int b, kvh, row0, nrows;  // rows row0 .. of sequence b (row = token * G + head), nrows of them valid
-    int begin, count;         // its entries in the list
+    int begin, count;         // its pages in the list
     int page_lo;              // dense: first page
 };
 
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         for (int b0 = 0; b0 < g.B; b0 += kThreads) {
             const int b = b0 + tid;
             int lo, n = b < g.B ? attended_pages(a, b, lo) : 0;
-            n *= n > 0 ? row_tiles_of<R>(g, b) : 0;
+            n = n > 0 ? (n + a.start_cost) * row_tiles_of<R>(g, b) : 0;
             int incl = n;
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
@@ -361,16 +362,17 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             }
             u.b = lo;
             const int n = attended_pages(a, lo, u.page_lo), tiles = row_tiles_of<R>(g, lo);
-            const int in = (at - prefix[lo] * g.Hkv) / n;  // (kv head, row tile)
-            u.begin = prefix[lo] * g.Hkv + in * n;
+            const int in = (at - prefix[lo] * g.Hkv) / (n + a.start_cost);  // (kv head, row tile)
+            u.begin = prefix[lo] * g.Hkv + in * (n + a.start_cost) + a.start_cost;
             u.count = n;
             u.kvh = tiles == 1 ? in : in / tiles;
             u.row0 = tiles == 1 ? 0 : in % tiles * R;
             u.nrows = min(R, query_tokens(g, lo) * g.G - u.row0);
         }
         const int seg1 = min(run1, u.begin + u.count);
-        if (u.nrows <= 0) {
-            at = seg1;
+        at = max(at, u.begin);
+        if (u.nrows <= 0 || at >= seg1) {
+            at = max(at, seg1);
             continue;
         }
         const int len = held_tokens(a, u.b);
@@ -841,7 +843,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cac
             const int row = t * g.G + hh, tiles = (query_tokens(g, b) * g.G + R - 1) / R;
             r = row % R;
             count = attended_pages(a, b, lo);
-            in = (kvh * tiles + row / R) * count;
+            in = (kvh * tiles + row / R) * (count + a.start_cost) + a.start_cost;
         }
         dependency_wait();
         int first = 0, last = -1, begin = 0;  // the CTAs with a part of the row
@@ -942,6 +944,12 @@ int row_tile(const Geo &g, bool sel)
     return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
 }
 
+// Beginning a unit (its first reads one behind the other, the warps' sums
+// joined) takes a CTA 5 to 9 us, the time of about 128 KB of codes: in a batch
+// of 32 rows of 128 .. 32768 tokens a CTA that had ten short rows ended at 201
+// us, the others at 155.  The list counts that many pages before each unit's.
+int start_cost(const Geo &g) { return max(1, 65536 / (g.D * g.bs)); }
+
 int ctas_of(const Geo &g, bool sel) { return num_sms() * attn_ctas(row_tile(g, sel)); }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1013,7 +1021,7 @@ int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)
 {
     const int R = row_tile(g, sel) * 8;
     return sel ? (int64_t)g.ntok * g.Hkv * g.S * ((g.G + R - 1) / R)
-               : (int64_t)g.B * c.cols * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
+               : (int64_t)g.B * (c.cols + start_cost(g)) * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
 }
 
 size_t cache_attn_ws_bytes(const Geo &g, bool sel) { return attn_layout(g, sel).total; }
@@ -1041,6 +1049,7 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     const int64_t units = (int64_t)g.ntok * g.Hkv * a.row_tiles;
     if (sel && (units + a.ncta - 1) / a.ncta * a.ncta * 4 <= units * 5)
         a.quantum = g.S;
+    a.start_cost = start_cost(g);
     a.status = (int *)(ws + w.status);
     a.prefix = (int *)(ws + w.prefix);
     a.part_ml = (float2 *)(ws + w.ml);
