@@ -13,6 +13,7 @@ namespace nsa {
 // bytes (one byte per code), the D codes of a token are contiguous.
 struct Cache {
     int pages, Hkv, D, bs, rows, cols;
+    int bsh;         // log2 of bs
     int64_t sp, sh, st;
     uint8_t *k, *v;
     float *ks, *vs;  // [pages, Hkv]

@@ -44,19 +44,26 @@ template <> struct Vec16<float> {
     }
 };
 
-// x / s for a scale that is usually a power of two (its reciprocal is then
-// exact and a product gives the quotient); a caller's own scale may not be
-struct Divide {
-    float s, inv;
-    bool pow2;
-    __device__ __forceinline__ explicit Divide(float scale) : s(scale)
-    {
-        const uint32_t u = __float_as_uint(scale);
-        pow2 = (u & 0x7fffffu) == 0 && (u >> 23) > 1 && (u >> 23) < 253;
-        inv = pow2 ? __uint_as_float((254u - (u >> 23)) << 23) : 0.f;
-    }
-    __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
-};
+// the reciprocal of a power of two (exact: a product with it is the
+// quotient), or 0 for a scale that is none
+__device__ __forceinline__ float pow2_inverse(float scale)
+{
+    const uint32_t u = __float_as_uint(scale);
+    return (u & 0x7fffffu) == 0 && (u >> 23) > 1 && (u >> 23) < 253 ? __uint_as_float((254u - (u >> 23)) << 23) : 0.f;
+}
+
+// N floats to N codes
+template <int N> __device__ __forceinline__ void store_codes(uint8_t *p, const float (&x)[N])
+{
+    uint32_t u[N / 4];
+#pragma unroll
+    for (int e = 0; e < N / 4; ++e)
+        u[e] = e4m3_pack2(x[4 * e], x[4 * e + 1]) | e4m3_pack2(x[4 * e + 2], x[4 * e + 3]) << 16;
+    if constexpr (N == 8)
+        *(uint2 *)p = make_uint2(u[0], u[1]);
+    else
+        *(uint32_t *)p = u[0];
+}
 
 // the new tokens of row b: their count and first position; false where the
 // row's length or packed range cannot hold them
@@ -88,41 +95,37 @@ __device__ void append_check(const Geo &g, const Cache &c, int per_row, int *err
         int n, start;
         if (!new_tokens(g, c, b, n, start))
             bad = 1;
-        else if (n > 0 && start / c.bs + j <= (start + n - 1) / c.bs)
-            bad |= !writable(c, c.table[(int64_t)b * c.cols + start / c.bs + j]);
+        else if (n > 0 && (start >> c.bsh) + j <= (start + n - 1) >> c.bsh)
+            bad |= !writable(c, c.table[(int64_t)b * c.cols + (start >> c.bsh) + j]);
     }
     bad = __syncthreads_or(bad);
     if (threadIdx.x == 0)
         *err = bad ? NSA_ERR_BAD_INDEX : NSA_OK;
 }
 
-// GROUP threads per (row, touched page, head, k or v); VPT vectors of the
+// GROUP threads per head of k or v of a touched page; VPT vectors of the
 // page's new tokens per thread (VPT * GROUP * N elements cover a page, or
 // the call's few new tokens).
 template <typename T, int GROUP, int VPT>
 __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const Cache c, const T *kn, const T *vn, int per_row,
-                                                            int64_t nunits, int *err)
+                                                            int *err)
 {
     constexpr int N = Vec16<T>::N;
     __shared__ float red[kCta / 32];
     if (blockIdx.x == gridDim.x - 1) {
-        append_check(g, c, per_row, err);
+        if (blockIdx.y == 0)
+            append_check(g, c, per_row, err);
         return;
     }
-    const int64_t unit = blockIdx.x * (int64_t)(kCta / GROUP) + threadIdx.x / GROUP;
-    const int lane = threadIdx.x % GROUP;
-    // unit = ((row * per_row + j) * 2 + which) * Hkv + h
-    const bool live = unit < nunits;
-    const int h = live ? (int)(unit % c.Hkv) : 0;
-    const int64_t u1 = live ? unit / c.Hkv : 0;
-    const int which = (int)(u1 & 1);
-    const int64_t u2 = u1 >> 1;
-    const int j = (int)(u2 % per_row), b = (int)(u2 / per_row);
+    // block x: a touched page (row * per_row + j); block y and group: a head of k or v
+    const int lane = threadIdx.x % GROUP, b = blockIdx.x / per_row, j = blockIdx.x - b * per_row;
+    const int part = blockIdx.y * (kCta / GROUP) + threadIdx.x / GROUP, which = part >= c.Hkv ? 1 : 0, h = part - which * c.Hkv;
+    const bool live = part < 2 * c.Hkv;
     int lo = 0, n = 0, page = -1, t0 = 0;  // the page's slots [lo, lo + n) get tokens t0 ..
     if (live) {
         int nn, start;
         if (new_tokens(g, c, b, nn, start)) {
-            const int col = start / c.bs + j, first = max(start, col * c.bs), end = min(start + nn, (col + 1) * c.bs);
+            const int col = (start >> c.bsh) + j, first = max(start, col * c.bs), end = min(start + nn, (col + 1) * c.bs);
             if (first < end) {
                 page = c.table[(int64_t)b * c.cols + col];
                 lo = first - col * c.bs;
@@ -136,13 +139,14 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
     const int vec_tok = c.D / N;  // vectors per token: a power of two
     const int shift = 31 - __clz(vec_tok);
     const int nvec = n << shift;
-    const T *src = which ? vn : kn;
+    const T *src = (which ? vn : kn) + (n > 0 ? kv_off(g, b, h, t0) : 0);
+    const int st = (int)c.st;
     uint4 w[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int x = lane + i * GROUP;
         if (x < nvec)
-            w[i] = __ldg((const uint4 *)(src + kv_off(g, b, h, t0 + (x >> shift)) + (x & (vec_tok - 1)) * N));
+            w[i] = __ldg((const uint4 *)(src + (x >> shift) * g.skv.t + (x & (vec_tok - 1)) * N));
     }
     float *scales = (which ? c.vs : c.ks) + (int64_t)(n > 0 ? page : 0) * c.Hkv + h;
     const float old = lo > 0 && n > 0 ? *scales : 0.f;
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
         const float ratio = __fdiv_rn(old, scale);
         const int per_tok = c.D / 16, sh16 = 31 - __clz(per_tok);
         for (int x = lane; x < lo << sh16; x += GROUP) {
-            uint4 *p = (uint4 *)(dst + (int64_t)(x >> sh16) * c.st + (x & (per_tok - 1)) * 16);
+            uint4 *p = (uint4 *)(dst + (x >> sh16) * st + (x & (per_tok - 1)) * 16);
             const uint4 q = *p;
             uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -188,22 +192,29 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
             *p = make_uint4(u[0], u[1], u[2], u[3]);
         }
     }
-    const Divide by(scale);
+    const float inv = pow2_inverse(scale);
+    if (inv != 0.f) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-        const int x = lane + i * GROUP;
-        if (x < nvec) {
+        for (int i = 0; i < VPT; ++i) {
+            const int x = lane + i * GROUP;
+            if (x < nvec) {
+                float f[N];
+                Vec16<T>::get(w[i], f);
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    f[e] *= inv;
+                store_codes<N>(dst + (lo + (x >> shift)) * st + (x & (vec_tok - 1)) * N, f);
+            }
+        }
+    } else {  // a scale of the caller's, larger than the new tokens need: divided, off the common path
+#pragma unroll 1
+        for (int x = lane; x < nvec; x += GROUP) {
             float f[N];
-            Vec16<T>::get(w[i], f);
-            uint32_t u[N / 4];
+            Vec16<T>::get(__ldg((const uint4 *)(src + (x >> shift) * g.skv.t + (x & (vec_tok - 1)) * N)), f);
 #pragma unroll
-            for (int e = 0; e < N / 4; ++e)
-                u[e] = e4m3_pack2(by(f[4 * e]), by(f[4 * e + 1])) | e4m3_pack2(by(f[4 * e + 2]), by(f[4 * e + 3])) << 16;
-            uint8_t *p = dst + (int64_t)(lo + (x >> shift)) * c.st + (x & (vec_tok - 1)) * N;
-            if constexpr (N == 8)
-                *(uint2 *)p = make_uint2(u[0], u[1]);
-            else
-                *(uint32_t *)p = u[0];
+            for (int e = 0; e < N; ++e)
+                f[e] = __fdiv_rn(f[e], scale);
+            store_codes<N>(dst + (lo + (x >> shift)) * st + (x & (vec_tok - 1)) * N, f);
         }
     }
     if (lane == 0)
@@ -214,24 +225,21 @@ template <typename T> cudaError_t append_t(const Geo &g, const Cache &c, const v
 {
     constexpr int N = Vec16<T>::N;
     const int per_row = (g.T + c.bs - 2) / c.bs + 1;
-    const int64_t nunits = (int64_t)c.rows * per_row * 2 * c.Hkv;
-    // few new tokens per row: a warp per unit, its values in 4 (fp32: 8)
-    // vectors per thread; else a block per unit
+    // few new tokens per row: a warp per head, its values in 4 (fp32: 8)
+    // vectors per thread; else a block per head
     constexpr int FEW = sizeof(T) == 2 ? 4 : 8;
     const int vecs = min(g.T, c.bs) * c.D / N;
     const bool few = vecs <= 32 * FEW;
-    const int64_t blocks = few ? (nunits + kCta / 32 - 1) / (kCta / 32) : nunits;
-    if (blocks + 1 > INT32_MAX)
-        return cudaErrorInvalidValue;
-    if (few && vecs <= 32)
-        cache_append_kernel<T, 32, 1><<<(unsigned)blocks + 1, kCta, 0, st>>>(g, c, (const T *)k, (const T *)v, per_row, nunits, err);
+    const dim3 grid((unsigned)((int64_t)c.rows * per_row + 1), (unsigned)(few ? (2 * c.Hkv + kCta / 32 - 1) / (kCta / 32) : 2 * c.Hkv));
+    const T *kn = (const T *)k, *vn = (const T *)v;
+    if (vecs <= 32)
+        cache_append_kernel<T, 32, 1><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
     else if (few)
-        cache_append_kernel<T, 32, FEW><<<(unsigned)blocks + 1, kCta, 0, st>>>(g, c, (const T *)k, (const T *)v, per_row, nunits, err);
+        cache_append_kernel<T, 32, FEW><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
     else if (vecs <= kCta * 4)
-        cache_append_kernel<T, kCta, 4><<<(unsigned)blocks + 1, kCta, 0, st>>>(g, c, (const T *)k, (const T *)v, per_row, nunits, err);
+        cache_append_kernel<T, kCta, 4><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
     else
-        cache_append_kernel<T, kCta, 64 * 128 / N / kCta>
-            <<<(unsigned)blocks + 1, kCta, 0, st>>>(g, c, (const T *)k, (const T *)v, per_row, nunits, err);
+        cache_append_kernel<T, kCta, 64 * 128 / N / kCta><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
     return cudaGetLastError();
 }
 

@@ -203,9 +203,9 @@ __device__ __forceinline__ int attended_pages(const AttnArgs &a, int b, int &lo)
         return 0;
     if (a.g.window > 0) {
         const int64_t first = (int64_t)len - nq - a.g.window + 1;  // the first row's left edge
-        lo = first > 0 ? (int)(first / a.c.bs) : 0;
+        lo = first > 0 ? (int)(first >> a.c.bsh) : 0;
     }
-    return max(0, (len - 1) / a.c.bs + 1 - lo);
+    return max(0, ((len - 1) >> a.c.bsh) + 1 - lo);
 }
 
 // tiles of R query rows of sequence b (dense)
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
     const uint32_t from_k = k_at<D>(gq, tq * KB / 16) * 16 + tq * KB % 16;
     const uint32_t from_v = 16 * D + v_at<D>(tq * 2, gq * VB / 16) * 16 + gq * VB % 16;
     const int from_lane = lane / CPT * (int)c.st + lane % CPT * 16;
-    const int st = (int)c.st, per_sh = 31 - __clz(c.bs) - 4, per_mask = (1 << per_sh) - 1;  // steps per page
+    const int st = (int)c.st, per_sh = c.bsh - 4, per_mask = (1 << per_sh) - 1;  // steps per page
     const Runs runs(total, a);
     const int run0 = runs.begin(cta), run1 = runs.begin(cta + 1);
 
@@ -797,10 +797,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
 // that of CTAs and warps, whatever order they ran in.  The kernel is a
 // programmatic dependent of the main one: it is set up while that runs and
 // waits before it reads what that wrote.
-constexpr int kJoinWarps = 8;
-constexpr int kJoinThreads = kJoinWarps * 32;
-template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const AttnArgs a, int R, int *err)
+// kJoinWarps: 8 for few rows of many parts, 2 where the rows alone fill the
+// GPU (1920 rows of 2 or 3 parts: 64 threads each have them all under way).
+template <typename T, int D, int kJoinWarps>
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnArgs a, int R, int *err)
 {
+    constexpr int kJoinThreads = kJoinWarps * 32;
     constexpr int E = D / 32;
     const Geo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -869,7 +871,7 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cac
 #pragma unroll
         for (int i = 0; i < E; ++i)
             acc[i] = 0.f;
-        for (int c0 = first; c0 <= last; c0 += kJoinThreads) {  // one round unless a row has over 256 parts
+        for (int c0 = first; c0 <= last; c0 += kJoinThreads) {  // one round unless a row has more parts than threads
             const int c = c0 + tid, n = min(kJoinThreads, last - c0 + 1);
             const float2 ml = c <= last ? a.part_ml[part_of(c)] : make_float2(kNoMax, 0.f);
             float x[4][E];  // the warp's first vectors, under way with the maxima
@@ -924,12 +926,14 @@ template <typename T, int D> __global__ void __launch_bounds__(kJoinThreads) cac
         for (int i = 0; i < E; ++i)
             part[warp][i * 32 + lane] = acc[i];
         __syncthreads();
-        if (tid < D) {
+        const float scale = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        T *dst = (T *)a.o + o_off(g, b, h, t);
+        for (int d = tid; d < D; d += kJoinThreads) {
             float y = 0.f;
 #pragma unroll
             for (int k = 0; k < kJoinWarps; ++k)
-                y += part[k][tid];
-            ((T *)a.o)[o_off(g, b, h, t) + tid] = from_f<T>(sum > 0.f || sum != sum ? y / sum : 0.f);
+                y += part[k][d];
+            dst[d] = from_f<T>(y * scale);
         }
         if (tid == 0)
             a.lse[stat_off(g, b, h, t)] = lse_of(top, sum);
@@ -977,8 +981,9 @@ template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cu
         return e;
     // index rows that are whole (see launch_cache_attn) leave nothing to join: the error word alone
     const int64_t rows = a.idx && a.quantum == a.g.S ? 0 : (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 8;
-    return launch_dependent(cache_join_kernel<T, D>, dim3((unsigned)(rows < most ? rows : most) + 1), dim3(kJoinThreads), 0, st,
-                            a, NT * 8, err);
+    if (rows <= most)
+        return launch_dependent(cache_join_kernel<T, D, 8>, dim3((unsigned)rows + 1), dim3(256), 0, st, a, NT * 8, err);
+    return launch_dependent(cache_join_kernel<T, D, 2>, dim3((unsigned)(rows < 4 * most ? rows : 4 * most) + 1), dim3(64), 0, st, a, NT * 8, err);
 }
 
 template <typename T> cudaError_t attn_d(const AttnArgs &a, int nt, int *err, cudaStream_t st)

@@ -34,8 +34,8 @@ __device__ __forceinline__ Where where(const cg::cluster_group &cl)
     return Where{(int)cl.block_rank(), (int)cl.block_rank() * kWarps + (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31)};
 }
 
-// blocks of `bs` that hold len tokens
-__device__ __forceinline__ int blocks_of(int len, int bs) { return (int)(((int64_t)len + bs - 1) / bs); }
+// blocks that hold len tokens
+__device__ __forceinline__ int blocks_of(int len, const Cache &c) { return (int)(((int64_t)len + c.bs - 1) >> c.bsh); }
 
 // Each warp of the cluster owns one run of pages: count() counts those that
 // pred() names, scan() turns the cluster's counts into the number before the
@@ -161,7 +161,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     };
     auto need = [&](int b) {
         const int len = c.lens[b], n = n_new[b];
-        return ok(b) ? blocks_of(len + n, c.bs) - blocks_of(len, c.bs) : 0;
+        return ok(b) ? blocks_of(len + n, c) - blocks_of(len, c) : 0;
     };
     // every CTA checks every row and knows the sum; CTA 0 writes the offsets
     for (int b = threadIdx.x; b < c.rows; b += kThreads)
@@ -188,7 +188,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cl.sync();
     for (int b = w.warp; b < c.rows; b += kAllWarps) {
         const int len = c.lens[b], n = n_new[b];
-        const int have = blocks_of(len, c.bs), want = blocks_of(len + n, c.bs), off = __ldcg(ws.r1 + b);
+        const int have = blocks_of(len, c), want = blocks_of(len + n, c), off = __ldcg(ws.r1 + b);
         for (int col = have + w.lane; col < want; col += 32)
             c.table[(int64_t)b * c.cols + col] = __ldcg(ws.p2 + off + col - have);
         __syncwarp();
@@ -269,7 +269,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
             bad = true;
             continue;
         }
-        for (int col = w.lane; col < blocks_of(len, c.bs); col += 32) {
+        for (int col = w.lane; col < blocks_of(len, c); col += 32) {
             const int p = c.table[(int64_t)s * c.cols + col];
             bad |= p < 0 || p >= c.pages || c.ref[p] < 1;
         }
@@ -293,7 +293,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const Runs run(c, w.warp);
     share_count(cl, counts, w, run.count(w.lane, [&](int p) { return __ldcg(c.ref + p) <= 0; }));
     if (w.rank == 0) {
-        const int64_t t = cta_prefix(n, ws.r1, [&](int i) { return c.lens[src[i]] % c.bs != 0 ? 1 : 0; });
+        const int64_t t = cta_prefix(n, ws.r1, [&](int i) { return (c.lens[src[i]] & (c.bs - 1)) != 0 ? 1 : 0; });
         if (threadIdx.x < kCluster)
             *cl.map_shared_rank(&tails_all, threadIdx.x) = t;
     }
@@ -316,8 +316,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cl.sync();
     for (int i = w.warp; i < n; i += kAllWarps) {
         const int s = src[i], d = dst[i], len = c.lens[s];
-        const int full = len / c.bs;
-        const bool tail = len % c.bs != 0;
+        const int full = len >> c.bsh;
+        const bool tail = (len & (c.bs - 1)) != 0;
         const int nth = __ldcg(ws.r1 + i);
         for (int col = w.lane; col < c.cols; col += 32) {
             const int theirs = col < full + (tail ? 1 : 0) ? c.table[(int64_t)s * c.cols + col] : -1;
@@ -451,7 +451,7 @@ constexpr int kChunk = kCopyThreads * kCopyVecs;      // vectors per step of a b
 __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const Cache c, const CacheWs ws)
 {
     const int n = *ws.npairs;
-    const int vtok = c.D / 16, sh_tok = 31 - __clz(vtok), sh_head = sh_tok + 31 - __clz(c.bs);
+    const int vtok = c.D / 16, sh_tok = 31 - __clz(vtok), sh_head = sh_tok + c.bsh;
     const int nvec = c.Hkv << sh_head;  // vectors of one page's keys
     const int chunks = (nvec + kChunk - 1) / kChunk;
     for (int64_t u = blockIdx.x; u < (int64_t)n * 2 * chunks; u += gridDim.x) {

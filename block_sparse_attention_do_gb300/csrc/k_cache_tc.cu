@@ -207,7 +207,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
             mbar_arrive(&bars[B_Q]);
         }
         float m = kNoMax, l = 0.f;
-        const int page_sh = 31 - __clz(c.bs);
+        const int page_sh = c.bsh;
         bool ok = true;
         for (int i = 0; i < ntiles; ++i) {
             const int j = j0 + i;
@@ -318,10 +318,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                         key |= kTileKeys - 1;
                         continue;
                     }
-                    const int page = c.table[(int64_t)b * c.cols + key / c.bs];
+                    const int page = c.table[(int64_t)b * c.cols + (key >> c.bsh)];
                     if (page < 0 || page >= c.pages)
                         continue;
-                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key % c.bs) * c.st;
+                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (c.bs - 1)) * c.st;
 #pragma unroll
                     for (int x = 0; x < D / 4; ++x) {
                         const uint32_t u = ((const uint32_t *)v)[x] & 0x7f7f7f7fu, hit = (u + 0x01010101u) & 0x80808080u;
@@ -366,7 +366,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         const int cw = warp - kSoftmaxWarps, half = cw & 1;
         const bool values = cw >= 2;
         const int sub = D == 128 ? (lane & 3) | (lane >> 4 & 1) << 2 : lane & 3, key_in = D == 128 ? lane >> 2 & 3 : lane >> 2;
-        const int page_sh = 31 - __clz(c.bs), npages = kTileKeys >> page_sh;
+        const int page_sh = c.bsh, npages = kTileKeys >> page_sh;
         const int st = (int)c.st;
         const uint8_t *pool = (values ? c.v : c.k) + (int64_t)kvh * c.sh + sub * 16;
         const int last_page = pmax >> page_sh, first_page = key_first >> page_sh;

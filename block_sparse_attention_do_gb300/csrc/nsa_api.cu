@@ -1139,6 +1139,7 @@ nsa_status make_cache(const nsa_cache *p, bool meta, bool counts, bool data, Cac
     c.Hkv = p->Hkv;
     c.D = p->D;
     c.bs = p->block_size;
+    c.bsh = c.bs == 16 ? 4 : c.bs == 32 ? 5 : 6;
     c.rows = p->rows;
     c.cols = p->max_pages;
     c.k = (uint8_t *)p->k;
@@ -1295,8 +1296,7 @@ nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *pc, const int
         return NSA_ERR_INVALID_ARG;
     if ((s = check_ws(ws, ws_bytes, kAlign)) != NSA_OK)
         return s;
-    const int64_t units = (int64_t)c.rows * ((g.T + c.bs - 2) / c.bs + 1) * 2 * c.Hkv;
-    if (units + 1 >= INT32_MAX)
+    if ((int64_t)c.rows * ((g.T + c.bs - 2) / c.bs + 1) + 1 >= INT32_MAX || 2 * (int64_t)c.Hkv > 65535)
         return NSA_ERR_UNSUPPORTED;
     cudaStream_t st = (cudaStream_t)stream;
     NSA_LAUNCH("cache_append", launch_cache_append(g, c, k, v, p->dtype, (int *)ws, st));
