@@ -34,6 +34,12 @@ struct CacheWs {
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
 
+// The cache's kernels run one behind the other in steps of a few microseconds,
+// so each is launched as a programmatic dependent: it is set up while the one
+// before it ends, and waits here before it reads or writes anything.
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // The least power of two s with amax <= 448 s, at least 2^-100 (amax finite,
 // >= 0): 448 = 1.75 * 2^8, so with amax = m * 2^e, 1 <= m < 2, s is 2^(e-8)
 // for m <= 1.75 and 2^(e-7) above.  A power of two makes x / s exact, so a

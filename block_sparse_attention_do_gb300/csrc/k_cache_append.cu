@@ -12,6 +12,7 @@
 
 #include "cache_common.cuh"
 #include "launch.h"
+#include "tc_common.cuh"
 
 namespace nsa {
 
@@ -112,6 +113,8 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
 {
     constexpr int N = Vec16<T>::N;
     __shared__ float red[kCta / 32];
+    dependents_may_start();
+    dependency_wait();
     if (blockIdx.x == gridDim.x - 1) {
         if (blockIdx.y == 0)
             append_check(g, c, per_row, err);
@@ -233,14 +236,12 @@ template <typename T> cudaError_t append_t(const Geo &g, const Cache &c, const v
     const dim3 grid((unsigned)((int64_t)c.rows * per_row + 1), (unsigned)(few ? (2 * c.Hkv + kCta / 32 - 1) / (kCta / 32) : 2 * c.Hkv));
     const T *kn = (const T *)k, *vn = (const T *)v;
     if (vecs <= 32)
-        cache_append_kernel<T, 32, 1><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
-    else if (few)
-        cache_append_kernel<T, 32, FEW><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
-    else if (vecs <= kCta * 4)
-        cache_append_kernel<T, kCta, 4><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
-    else
-        cache_append_kernel<T, kCta, 64 * 128 / N / kCta><<<grid, kCta, 0, st>>>(g, c, kn, vn, per_row, err);
-    return cudaGetLastError();
+        return launch_dependent(cache_append_kernel<T, 32, 1>, grid, dim3(kCta), 0, st, g, c, kn, vn, per_row, err);
+    if (few)
+        return launch_dependent(cache_append_kernel<T, 32, FEW>, grid, dim3(kCta), 0, st, g, c, kn, vn, per_row, err);
+    if (vecs <= kCta * 4)
+        return launch_dependent(cache_append_kernel<T, kCta, 4>, grid, dim3(kCta), 0, st, g, c, kn, vn, per_row, err);
+    return launch_dependent(cache_append_kernel<T, kCta, 64 * 128 / N / kCta>, grid, dim3(kCta), 0, st, g, c, kn, vn, per_row, err);
 }
 
 }  // namespace

@@ -116,11 +116,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// programmatic dependents: the next kernel may be set up from here on; wait
-// for the kernel before this one to complete
-__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t y;
@@ -277,6 +272,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
     const int gq = lane >> 2, tq = lane & 3;  // the fragment's row group and column pair
     const int cta = blockIdx.x;
     dependents_may_start();
+    dependency_wait();
     const bool sel = a.idx != nullptr;
     bool bad = false;
 
@@ -806,6 +802,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
     constexpr int E = D / 32;
     const Geo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    dependents_may_start();
     __shared__ float part[kJoinWarps][D];
     __shared__ float factor[kJoinThreads], red[2][kJoinWarps];
     if (blockIdx.x == 0) {  // the call's error word
@@ -976,8 +973,7 @@ template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cu
         if (dev < 64)
             set.fetch_or((uint64_t)1 << dev, std::memory_order_release);
     }
-    cache_attn_kernel<T, D, NT><<<a.ncta, kThreads, smem, st>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess)
+    if ((e = launch_dependent(cache_attn_kernel<T, D, NT>, dim3(a.ncta), dim3(kThreads), smem, st, a)) != cudaSuccess)
         return e;
     // index rows that are whole (see launch_cache_attn) leave nothing to join: the error word alone
     const int64_t rows = a.idx && a.quantum == a.g.S ? 0 : (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 8;

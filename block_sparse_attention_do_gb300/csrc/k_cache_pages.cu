@@ -14,6 +14,7 @@
 
 #include "cache_common.cuh"
 #include "launch.h"
+#include "tc_common.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -106,39 +107,70 @@ template <typename F> __device__ int64_t cta_prefix(int n, int *out, F need)
     return base;
 }
 
+constexpr int kBatch = 8;  // reads of a thread under way together
+
 // Takes the `total` lowest free pages: order[i] = the i-th, its count 1.
 __device__ __forceinline__ void take_free(const Cache &c, const Runs &r, int lane, int before, int total, int *order)
 {
-    for (int p0 = r.begin; p0 < r.end && before < total; p0 += 32) {
-        const int p = p0 + lane;
-        const bool free = p < r.end && __ldcg(c.ref + p) <= 0;
-        const unsigned m = __ballot_sync(0xffffffffu, free);
-        const int nth = before + __popc(m & ((1u << lane) - 1u));
-        if (free && nth < total) {
-            order[nth] = p;
-            c.ref[p] = 1;
+    for (int p0 = r.begin + lane; p0 - lane < r.end && before < total; p0 += 32 * kBatch) {
+        int count[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            count[u] = p0 + u * 32 < r.end ? __ldcg(c.ref + p0 + u * 32) : 1;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const unsigned m = __ballot_sync(0xffffffffu, count[u] <= 0);
+            const int nth = before + __popc(m & ((1u << lane) - 1u));
+            if (count[u] <= 0 && nth < total) {
+                order[nth] = p0 + u * 32;
+                c.ref[p0 + u * 32] = 1;
+            }
+            before += __popc(m);
         }
-        before += __popc(m);
     }
 }
 
-// Gives back the pages of row r (lanes over its columns): true if an entry
-// names no page or a page that nobody holds.
-__device__ __forceinline__ bool release_row(const Cache &c, int r, int lane, bool clear)
+// Rows' columns in pieces of kPiece, a warp each: for_pieces calls f(i, col0)
+// for piece col0 .. of list position i.
+constexpr int kPiece = 32 * kBatch;
+template <typename F> __device__ __forceinline__ void for_pieces(const Cache &c, const Where &w, int n, F f)
 {
+    const int per = (c.cols + kPiece - 1) / kPiece;
+    for (int64_t x = w.warp; x < (int64_t)n * per; x += kAllWarps) {
+        const int i = per == 1 ? (int)x : (int)(x / per);
+        f(i, (int)(x - (int64_t)i * per) * kPiece);
+    }
+}
+// a piece of row r's table entries, lane by lane (-1 past the table's width)
+__device__ __forceinline__ void load_piece(const Cache &c, int r, int col0, int lane, int (&p)[kBatch])
+{
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+        const int col = col0 + u * 32 + lane;
+        p[u] = col < c.cols ? c.table[(int64_t)r * c.cols + col] : -1;
+    }
+}
+
+// Gives back a piece of the pages of row r: true if an entry names no page or
+// a page that nobody holds.
+__device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, int lane, bool clear)
+{
+    int p[kBatch], was[kBatch];
+    load_piece(c, r, col0, lane, p);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+        was[u] = p[u] >= 0 && p[u] < c.pages ? atomicSub(c.ref + p[u], 1) : p[u] == -1 ? 1 : 0;
     bool bad = false;
-    for (int col = lane; col < c.cols; col += 32) {
-        int *e = c.table + (int64_t)r * c.cols + col;
-        const int p = *e;
-        if (p >= 0 && p < c.pages) {
-            if (atomicSub(c.ref + p, 1) <= 0) {
-                atomicAdd(c.ref + p, 1);
-                bad = true;
-            }
-        } else if (p != -1)
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+        if (was[u] <= 0) {
             bad = true;
-        if (clear)
-            *e = -1;
+            if (p[u] >= 0 && p[u] < c.pages)
+                atomicAdd(c.ref + p[u], 1);
+        }
+        const int col = col0 + u * 32 + lane;
+        if (clear && col < c.cols)
+            c.table[(int64_t)r * c.cols + col] = -1;
     }
     return bad;
 }
@@ -147,6 +179,8 @@ __device__ __forceinline__ bool release_row(const Cache &c, int r, int lane, boo
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cache_reserve_kernel(const Cache c, const int *n_new, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     __shared__ int counts[kAllWarps];
     __shared__ int bad;
@@ -189,6 +223,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     for (int b = w.warp; b < c.rows; b += kAllWarps) {
         const int len = c.lens[b], n = n_new[b];
         const int have = blocks_of(len, c), want = blocks_of(len + n, c), off = __ldcg(ws.r1 + b);
+#pragma unroll 4
         for (int col = have + w.lane; col < want; col += 32)
             c.table[(int64_t)b * c.cols + col] = __ldcg(ws.p2 + off + col - have);
         __syncwarp();
@@ -216,6 +251,8 @@ __device__ __forceinline__ void claim(const int *list, int n, int limit, int *ma
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cache_free_kernel(const Cache c, const int *rows, int n, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     const Where w = where(cl);
     if (w.rank == 0 && threadIdx.x == 0)
@@ -225,16 +262,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     claim(rows, n, c.rows, ws.r0, w, false);
     cl.sync();
     bool bad = false;
-    for (int i = w.warp; i < n; i += kAllWarps) {
+    for_pieces(c, w, n, [&](int i, int col0) {
         const int r = rows[i];
         if (r < 0 || r >= c.rows || __ldcg(ws.r0 + r) != i) {  // no row, or listed before
             bad = true;
-            continue;
+            return;
         }
-        bad |= release_row(c, r, w.lane, true);
-        if (w.lane == 0)
+        bad |= release_piece(c, r, col0, w.lane, true);
+        if (col0 == 0 && w.lane == 0)
             c.lens[r] = 0;
-    }
+    });
     if (bad)
         set_error(ws.err, NSA_ERR_BAD_INDEX);
 }
@@ -243,6 +280,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cache_fork_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     __shared__ int counts[kAllWarps];
     __shared__ int64_t tails_all;
@@ -258,26 +297,32 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     claim(src, n, c.rows, ws.r0, w, true);
     cl.sync();
     bool bad = false;
-    for (int i = w.warp; i < n; i += kAllWarps) {
+    for_pieces(c, w, n, [&](int i, int col0) {
         const int s = src[i], d = dst[i];
         if (s < 0 || s >= c.rows || d < 0 || d >= c.rows || __ldcg(ws.r0 + d) != i) {
             bad = true;
-            continue;
+            return;
         }
         const int len = c.lens[s];
-        if (len < 0 || (int64_t)len > (int64_t)c.cols * c.bs) {
+        if (len < 0 || len > c.cols * c.bs) {
             bad = true;
-            continue;
+            return;
         }
-        for (int col = w.lane; col < blocks_of(len, c); col += 32) {
-            const int p = c.table[(int64_t)s * c.cols + col];
-            bad |= p < 0 || p >= c.pages || c.ref[p] < 1;
+        int p[kBatch], x[kBatch];
+        load_piece(c, s, col0, w.lane, p);
+        load_piece(c, d, col0, w.lane, x);
+        const int used = blocks_of(len, c);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {  // src's pages, and what dst gives up, are pages in use
+            const bool needed = col0 + u * 32 + w.lane < used;
+            bad |= p[u] >= c.pages || (needed && p[u] < 0) || x[u] < -1 || x[u] >= c.pages;
+            p[u] = needed && p[u] >= 0 && p[u] < c.pages ? c.ref[p[u]] : 1;
+            x[u] = x[u] >= 0 && x[u] < c.pages ? c.ref[x[u]] : 1;
         }
-        for (int col = w.lane; col < c.cols; col += 32) {
-            const int p = c.table[(int64_t)d * c.cols + col];
-            bad |= p < -1 || p >= c.pages || (p >= 0 && c.ref[p] < 1);
-        }
-    }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            bad |= p[u] < 1 || x[u] < 1;
+    });
     if (bad)
         set_error(ws.err, NSA_ERR_BAD_INDEX);
     cl.sync();
@@ -285,8 +330,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         return;  // the same in every CTA: nothing has changed
     // the destinations' own pages come back first: a tail may reuse them (an
     // error here: more table entries name a page than its count says)
-    for (int i = w.warp; i < n; i += kAllWarps)
-        bad |= release_row(c, dst[i], w.lane, false);
+    for_pieces(c, w, n, [&](int i, int col0) { bad |= release_piece(c, dst[i], col0, w.lane, false); });
     cl.sync();  // every thread has read ws.err: it may be written again
     if (bad)
         set_error(ws.err, NSA_ERR_BAD_INDEX);
@@ -302,39 +346,45 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     int before, free;
     scan_counts(counts, w, before, free);
     if (tails > free) {  // undo: nothing has changed
-        for (int i = w.warp; i < n; i += kAllWarps)
-            for (int col = w.lane; col < c.cols; col += 32) {
-                const int p = c.table[(int64_t)dst[i] * c.cols + col];
-                if (p >= 0)
-                    atomicAdd(c.ref + p, 1);
-            }
+        for_pieces(c, w, n, [&](int i, int col0) {
+            int p[kBatch];
+            load_piece(c, dst[i], col0, w.lane, p);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (p[u] >= 0)
+                    atomicAdd(c.ref + p[u], 1);
+        });
         if (w.rank == 0 && threadIdx.x == 0)
             *ws.err = NSA_ERR_CACHE_FULL;
         return;
     }
     take_free(c, run, w.lane, before, (int)tails, ws.p2);
     cl.sync();
-    for (int i = w.warp; i < n; i += kAllWarps) {
+    for_pieces(c, w, n, [&](int i, int col0) {
         const int s = src[i], d = dst[i], len = c.lens[s];
         const int full = len >> c.bsh;
         const bool tail = (len & (c.bs - 1)) != 0;
         const int nth = __ldcg(ws.r1 + i);
-        for (int col = w.lane; col < c.cols; col += 32) {
-            const int theirs = col < full + (tail ? 1 : 0) ? c.table[(int64_t)s * c.cols + col] : -1;
+        int p[kBatch];
+        load_piece(c, s, col0, w.lane, p);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int col = col0 + u * 32 + w.lane;
             int mine = -1;
             if (col < full) {
-                mine = theirs;
+                mine = p[u];
                 atomicAdd(c.ref + mine, 1);
             } else if (col == full && tail) {
                 mine = __ldcg(ws.p2 + nth);
-                ws.p0[nth] = theirs;
+                ws.p0[nth] = p[u];
                 ws.p1[nth] = mine;
             }
-            c.table[(int64_t)d * c.cols + col] = mine;
+            if (col < c.cols)
+                c.table[(int64_t)d * c.cols + col] = mine;
         }
-        if (w.lane == 0)
+        if (col0 == 0 && w.lane == 0)
             c.lens[d] = len;
-    }
+    });
     if (w.rank == 0 && threadIdx.x == 0)
         *ws.npairs = (int)tails;
 }
@@ -345,6 +395,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cache_copy_check_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     const Where w = where(cl);
     if (w.rank == 0 && threadIdx.x == 0) {
@@ -374,6 +426,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 // free pages below n, in order.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cache_compact_kernel(const Cache c, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     __shared__ int counts[kAllWarps];
     __shared__ int low;  // live pages below n
@@ -393,6 +447,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cac
             low = n;
     } else if (n >= run.begin && n < run.end) {
         int k = before;
+#pragma unroll 4
         for (int p0 = run.begin; p0 < n; p0 += 32) {
             const int p = p0 + w.lane;
             k += __popc(__ballot_sync(0xffffffffu, p < n && c.ref[p] > 0));
@@ -403,17 +458,24 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cac
     cl.sync();
     const int moved = n - low;
     int rank = before;
-    for (int p0 = run.begin; p0 < run.end; p0 += 32) {
-        const int p = p0 + w.lane;
-        const bool live = p < run.end && c.ref[p] > 0;
-        const unsigned m = __ballot_sync(0xffffffffu, live);
-        const int r = rank + __popc(m & ((1u << w.lane) - 1u));  // live pages below p
-        if (live && p >= n) {
-            ws.p0[r - low] = p;
-            ws.p2[p] = r - low;
-        } else if (!live && p < n)
-            ws.p1[p - r] = p;
-        rank += __popc(m);
+    for (int p0 = run.begin + w.lane; p0 - w.lane < run.end; p0 += 32 * kBatch) {
+        int count[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            count[u] = p0 + u * 32 < run.end ? c.ref[p0 + u * 32] : 0;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int p = p0 + u * 32;
+            const bool live = count[u] > 0;
+            const unsigned m = __ballot_sync(0xffffffffu, live);
+            const int r = rank + __popc(m & ((1u << w.lane) - 1u));  // live pages below p
+            if (live && p >= n) {
+                ws.p0[r - low] = p;
+                ws.p2[p] = r - low;
+            } else if (!live && p < n && p < run.end)
+                ws.p1[p - r] = p;
+            rank += __popc(m);
+        }
     }
     cl.sync();
     bool bad = false;
@@ -450,6 +512,8 @@ constexpr int kChunk = kCopyThreads * kCopyVecs;      // vectors per step of a b
 // Pairs p0 -> p1, each in chunks of 16 KB of its keys, then of its values.
 __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const Cache c, const CacheWs ws)
 {
+    dependents_may_start();
+    dependency_wait();
     const int n = *ws.npairs;
     const int vtok = c.D / 16, sh_tok = 31 - __clz(vtok), sh_head = sh_tok + c.bsh;
     const int nvec = c.Hkv << sh_head;  // vectors of one page's keys
@@ -487,33 +551,28 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const Cache c,
 
 cudaError_t launch_cache_reserve(const Cache &c, const int *n_new, const CacheWs &ws, cudaStream_t st)
 {
-    cache_reserve_kernel<<<kCluster, kThreads, 0, st>>>(c, n_new, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_reserve_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, n_new, ws);
 }
 
 cudaError_t launch_cache_free(const Cache &c, const int *rows, int n, const CacheWs &ws, cudaStream_t st)
 {
-    cache_free_kernel<<<kCluster, kThreads, 0, st>>>(c, rows, n, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_free_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, rows, n, ws);
 }
 
 cudaError_t launch_cache_fork(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws, cudaStream_t st)
 {
-    cache_fork_kernel<<<kCluster, kThreads, 0, st>>>(c, src, dst, n, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_fork_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, src, dst, n, ws);
 }
 
 cudaError_t launch_cache_copy_check(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws,
                                     cudaStream_t st)
 {
-    cache_copy_check_kernel<<<kCluster, kThreads, 0, st>>>(c, src, dst, n, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_copy_check_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, src, dst, n, ws);
 }
 
 cudaError_t launch_cache_compact(const Cache &c, const CacheWs &ws, cudaStream_t st)
 {
-    cache_compact_kernel<<<kCluster, kThreads, 0, st>>>(c, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_compact_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, ws);
 }
 
 cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, cudaStream_t st)
@@ -521,8 +580,7 @@ cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, 
     const int nvec = c.Hkv * c.bs * (c.D / 16);
     const int64_t units = (int64_t)max_pairs * 2 * ((nvec + kChunk - 1) / kChunk);
     const int64_t most = (int64_t)num_sms() * 8;
-    cache_move_kernel<<<(unsigned)(units < most ? units : most), kCopyThreads, 0, st>>>(c, ws);
-    return cudaGetLastError();
+    return launch_dependent(cache_move_kernel, dim3((unsigned)(units < most ? units : most)), dim3(kCopyThreads), 0, st, c, ws);
 }
 
 }  // namespace nsa

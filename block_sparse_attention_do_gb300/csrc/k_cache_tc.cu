@@ -110,6 +110,8 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
     float4 *scales = (float4 *)(sm + L::scales);
     const Geo &g = p.g;
     const Cache &c = p.c;
+    dependents_may_start();
+    dependency_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the unit: 256 query rows (row = token * G + head) of one kv head.  Every
@@ -587,8 +589,7 @@ cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, cons
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
-    kernel<<<(unsigned)(p.tiles * g.B * g.Hkv), kThreads, smem, st>>>(p);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3((unsigned)(p.tiles * g.B * g.Hkv)), dim3(kThreads), smem, st, p);
 }
 
 }  // namespace nsa
