@@ -768,7 +768,7 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     each token's latest keys, with `block_idx` the selected blocks; `sinks` as
     for sel_fwd.  Returns (o, lse).  A ws of the caller's
     (nsa_cache_fwd_workspace_size) holds the error word that get_error reads;
-    without one each call has its own."""
+    without one each call has its own, and bad entries are left out unreported."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_fwd(q, cache, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)
@@ -788,10 +788,11 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     if q.numel() == 0:
         return o, lse
     _, p, n = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
-    if ws is None:
+    if ws is None and n > 256:
         ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    at, size = (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
     _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
                                block_idx.data_ptr() if block_idx is not None else None,
                                sinks.data_ptr() if sinks is not None else None, q.data_ptr(), o.data_ptr(),
-                               lse.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(cache)), "nsa_cache_fwd")
+                               lse.data_ptr(), at, size, _raw_stream(cache)), "nsa_cache_fwd")
     return o, lse

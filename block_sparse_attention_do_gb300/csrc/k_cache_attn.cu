@@ -32,11 +32,15 @@
 // busy, and tcgen05 would take the codes through shared memory first.
 #include <math.h>
 
+#include <cooperative_groups.h>
+
 #include <atomic>
 
 #include "cache_common.cuh"
 #include "launch.h"
 #include "tc_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace nsa {
 
@@ -89,10 +93,12 @@ struct AttnArgs {
     const float *sinks;  // or nullptr
     void *o;
     float *lse;
-    int row_tiles;       // selection: query-row tiles per index row
+    int row_tiles;       // query-row tiles per index row (clustered form without one: per sequence, at most)
     int quantum;         // pages that are not cut
     int start_cost;      // dense: list entries that stand before a unit's pages for what it costs to begin one
     int ncta;            // CTAs of the main kernel
+    int units, cs;       // clustered form: its units, and the CTAs of one
+    int *err;            // clustered form: the call's error word (may be null)
     int *status;         // [ncta]: what each CTA found
     int *prefix;         // [rows + 1] dense: list entries of one kv head before each sequence
     float *part_o;       // [ncta * 2][rows of a tile][D]
@@ -247,13 +253,66 @@ template <int D, int NT, bool SPLIT> struct Smem {
     int key0[kList];     // first key (kNoKey: left out)
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
     float2 ml[kWarps][R];       // each warp's maximum and sum
+    float2 cta_ml[R];           // the CTA's, for its cluster
     union {
         float o[kWarps][R][D + 4];                     // its part of O
         uint8_t ring[kWarps][attn_stages(NT)][32 * D];  // its steps under way: 16 tokens' keys, then values
     };
 };
 
-template <typename T, int D, int NT>
+// Every length, index entry and page of a call, checked by one block, which
+// alone writes the error word (the clustered form's calls are small).
+__device__ void attn_check(const AttnArgs &a)
+{
+    const Geo &g = a.g;
+    const Cache &c = a.c;
+    const int tid = threadIdx.x, lane = tid & 31;
+    int bad = 0;
+    auto bad_page = [&](int b, int col) {
+        const int page = c.table[(int64_t)b * c.cols + col];
+        return page < 0 || page >= c.pages;
+    };
+    for (int b = tid; b < g.B; b += kThreads)
+        bad |= c.lens[b] < 0 || c.lens[b] > c.cols * c.bs || query_tokens(g, b) < 0;
+    if (!a.idx)
+        for (int b = tid >> 5; b < g.B; b += kWarps) {
+            int lo;
+            const int n = attended_pages(a, b, lo);
+#pragma unroll 8
+            for (int col = lo + lane; col < lo + n; col += 32)
+                bad |= bad_page(b, col);
+        }
+    else
+#pragma unroll 2
+        for (int i = tid; i < g.ntok * g.Hkv * g.S; i += kThreads) {
+            const int j = a.idx[i];
+            if (j == -1)
+                continue;
+            int s, h, b, t;
+            const int row = a.by_S.divmod(i, s);
+            if (g.thd) {
+                const int tok = a.by_Hkv.divmod(row, h);
+                b = seq_of_token(g, tok);
+                t = tok - g.cu[b];
+                if (t >= query_tokens(g, b))
+                    continue;  // a token of no sequence
+            } else
+                b = a.by_Hkv.divmod(a.by_T.divmod(row, t), h);
+            const int pos = held_tokens(a, b) - query_tokens(g, b) + t;
+            if (j < 0 || j >= c.cols || j * c.bs > pos || bad_page(b, j))
+                bad = 1;
+            for (int k = i - s; k < i; ++k)
+                bad |= a.idx[k] == j;
+        }
+    bad = __syncthreads_or(bad);
+    if (tid == 0)
+        *a.err = bad ? NSA_ERR_BAD_INDEX : NSA_OK;
+}
+
+// CLUSTER: a unit's pages are cut into equal runs for the CTAs of a cluster,
+// which join their sums through one another's shared memory: one launch, for
+// calls that are a few microseconds of latencies.
+template <typename T, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(const AttnArgs a)
 {
     constexpr bool SPLIT = sizeof(T) == 4;
@@ -280,7 +339,15 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
     __shared__ int part_s[kWarps];
     int *prefix = (int *)(smem_raw + sizeof(SM));  // dense: as a.prefix
     int total;
-    if (sel)
+    const int rank = CLUSTER ? cta & (a.cs - 1) : 0, cunit = CLUSTER ? cta / a.cs : 0;
+    if (CLUSTER) {
+        if (cunit == a.units) {  // the cluster behind the units'
+            if (rank == 0)
+                attn_check(a);
+            return;
+        }
+        total = 0;
+    } else if (sel)
         total = g.ntok * g.Hkv * a.row_tiles * g.S;
     else {
         int base = 0;
@@ -329,12 +396,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
     const Runs runs(total, a);
     const int run0 = runs.begin(cta), run1 = runs.begin(cta + 1);
 
-    for (int at = run0; at < run1;) {
+    for (int at = run0; CLUSTER || at < run1;) {
         // ---- the unit that holds list entry `at`
         UnitRows u;
         if (sel) {
-            const int unit = a.by_S.div(at);
-            u.begin = unit * g.S;
+            const int unit = CLUSTER ? cunit : a.by_S.div(at);
+            u.begin = CLUSTER ? 0 : unit * g.S;
             u.count = g.S;
             int rt, t;
             const int row = a.by_tiles.divmod(unit, rt);  // of the index
@@ -347,6 +414,13 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             u.row0 = t * g.G + rt * R;
             u.nrows = t < query_tokens(g, u.b) ? min(R, g.G - rt * R) : 0;  // 0: a token of no sequence
             u.page_lo = 0;
+        } else if (CLUSTER) {
+            int rt;
+            u.b = a.by_Hkv.divmod(a.by_tiles.divmod(cunit, rt), u.kvh);
+            u.begin = 0;
+            u.count = attended_pages(a, u.b, u.page_lo);
+            u.row0 = rt * R;
+            u.nrows = min(R, query_tokens(g, u.b) * g.G - u.row0);
         } else {
             int lo = 0, hi = g.B - 1;  // the sequence: prefix[b] * Hkv <= at < prefix[b + 1] * Hkv
             while (lo < hi) {
@@ -365,11 +439,20 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             u.row0 = tiles == 1 ? 0 : in % tiles * R;
             u.nrows = min(R, query_tokens(g, lo) * g.G - u.row0);
         }
-        const int seg1 = min(run1, u.begin + u.count);
-        at = max(at, u.begin);
-        if (u.nrows <= 0 || at >= seg1) {
-            at = max(at, seg1);
-            continue;
+        int seg1;
+        if constexpr (CLUSTER) {
+            const int per = (u.count + a.cs - 1) / a.cs;
+            at = min(u.count, rank * per);
+            seg1 = min(u.count, at + per);
+            if (u.nrows <= 0)
+                return;  // (the whole cluster)
+        } else {
+            seg1 = min(run1, u.begin + u.count);
+            at = max(at, u.begin);
+            if (u.nrows <= 0 || at >= seg1) {
+                at = max(at, seg1);
+                continue;
+            }
         }
         const int len = held_tokens(a, u.b);
         const int pos0 = len - query_tokens(g, u.b);  // position of the sequence's first query token
@@ -730,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                 }
             }
         __syncthreads();
-        const bool whole = at == u.begin && seg1 == u.begin + u.count;
+        const bool whole = CLUSTER ? a.cs == 1 : at == u.begin && seg1 == u.begin + u.count;
         // a part: the first of the run in slot 0, its last in slot 1 (a run
         // within one unit has one part)
         const int slot = cta * 2 + (at == run0 ? 0 : 1);
@@ -745,8 +828,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             for (int i = 4; i > 0; i >>= 1)
                 sum += __shfl_xor_sync(0xffffffffu, sum, i);
             if (!whole) {
-                if (lane == 0)
-                    a.part_ml[slot * R + r] = make_float2(top, sum);
+                if (lane == 0) {
+                    if constexpr (CLUSTER)
+                        sm.cta_ml[r] = make_float2(top, sum);
+                    else
+                        a.part_ml[slot * R + r] = make_float2(top, sum);
+                }
             } else {
                 if (a.sinks) {
                     int hh;
@@ -765,6 +852,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                 sm.ml[lane][r].x = f;  // from here on the warp's factor
         }
         __syncthreads();
+        // (thread x has vector x of each warp's part, and puts the sum, of a
+        // cluster's CTA, into the first warp's place, which it alone has read)
         for (int x = tid; x < u.nrows * (D / 4); x += kThreads) {
             const int r = x / (D / 4), d = x % (D / 4) * 4;
             float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -776,8 +865,46 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             }
             if (whole)
                 store4((T *)a.o + sm.o_at[r] + d, y);
+            else if constexpr (CLUSTER)
+                *(float4 *)&sm.o[0][r][d] = y;
             else
                 *(float4 *)&a.part_o[((int64_t)slot * R + r) * D + d] = y;
+        }
+        if constexpr (CLUSTER) {
+            if (whole)
+                return;
+            cg::cluster_group cl = cg::this_cluster();
+            cl.sync();
+            for (int x = tid * a.cs + rank; x < u.nrows * (D / 4); x += kThreads * a.cs) {
+                const int r = x / (D / 4), d = x % (D / 4) * 4;
+                float top = kNoMax;
+#pragma unroll 4
+                for (int k = 0; k < a.cs; ++k)
+                    top = fmaxf(top, cl.map_shared_rank(&sm.cta_ml[r], k)->x);
+                float f = 1.f, sum = 0.f;
+                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (a.sinks) {
+                    int hh;
+                    a.by_G.divmod(u.row0 + r, hh);
+                    const float sk = a.sinks[u.kvh * g.G + hh] * 1.4426950408889634f;
+                    top = fmaxf(top, sk);
+                    sum = exp2f(sk - top);
+                }
+#pragma unroll 4
+                for (int k = 0; k < a.cs; ++k) {
+                    const float2 ml = *cl.map_shared_rank(&sm.cta_ml[r], k);
+                    const float4 p = *(const float4 *)cl.map_shared_rank(&sm.o[0][r][d], k);
+                    f = exp2f(ml.x - top);
+                    sum += ml.y * f;
+                    y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
+                }
+                f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+                store4((T *)a.o + sm.o_at[r] + d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+                if (d == 0)
+                    a.lse[sm.lse_at[r]] = lse_of(top, sum);
+            }
+            cl.sync();  // no CTA leaves while another reads its sums
+            return;
         }
         at = seg1;
     }
@@ -955,40 +1082,88 @@ int ctas_of(const Geo &g, bool sel) { return num_sms() * attn_ctas(row_tile(g, s
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <typename T, int D, int NT> cudaError_t attn_t(AttnArgs a, int *err, cudaStream_t st)
+// The clustered form: CTAs of a unit (0: the list's form).  For calls whose
+// units fit the GPU at once, cut as far as CTAs and 128 tokens each go.  The
+// cut goes by the table's width, not by lengths, so with several sequences
+// (which may be of any length) it has to be short: 128 KB of codes for a CTA;
+// one sequence alone 512 KB, or an index's equal rows any.  A token over 8192
+// cached ones (8 kv heads): 14.6 us by the list, of which the join's launch
+// and the list's own reads were 5.
+int cluster_size(const Geo &g, const Cache &c, bool sel)
 {
-    using SM = Smem<D, NT, sizeof(T) == 4>;
-    const size_t smem = sizeof(SM) + (a.idx ? 0 : sizeof(int) * (size_t)(a.g.B + 1));
-    // the largest size that a call can ask for, set once per device
-    static std::atomic<uint64_t> set{0};
+    const int nt = row_tile(g, sel), R = nt * 8, slots = num_sms() * attn_ctas(nt);
+    const int64_t units = sel ? (int64_t)g.ntok * g.Hkv * ((g.G + R - 1) / R) : (int64_t)g.B * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
+    const int64_t checks = sel ? (int64_t)g.ntok * g.Hkv * g.S : (int64_t)g.B * c.cols;
+    int64_t pages = sel ? g.S : c.cols;
+    if (g.window > 0)
+        pages = min(pages, ((int64_t)g.window + g.T) / c.bs + 2);
+    if (units + 1 > slots || checks > 8192)
+        return 0;
+    int cs = 1;
+    while (cs < 16 && (units + 1) * cs * 2 <= slots && pages * c.bs > (int64_t)cs * 128)
+        cs *= 2;
+    const int64_t bytes = (pages + cs - 1) / cs * c.bs * 2 * g.D;
+    return sel || bytes <= (g.B == 1 ? 512 << 10 : 128 << 10) ? cs : 0;
+}
+
+// shared memory above the default, and clusters of 16, allowed once per device
+template <typename K> cudaError_t allow(K kernel, int smem, std::atomic<uint64_t> &done)
+{
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess)
+    if (e != cudaSuccess || (dev < 64 && (done.load(std::memory_order_acquire) >> dev & 1)))
         return e;
-    if (dev >= 64 || !(set.load(std::memory_order_acquire) >> dev & 1)) {
-        e = cudaFuncSetAttribute(cache_attn_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)(sizeof(SM) + sizeof(int) * (kMaxRows + 1)));
-        if (e != cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+        return e;
+    if (dev < 64)
+        done.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename T, int D, int NT> cudaError_t attn_t(const AttnArgs &a, cudaStream_t st)
+{
+    using SM = Smem<D, NT, sizeof(T) == 4>;
+    cudaError_t e;
+    if (a.cs > 0) {
+        static std::atomic<uint64_t> done{0};
+        if ((e = allow(cache_attn_kernel<T, D, NT, true>, (int)sizeof(SM), done)) != cudaSuccess)
             return e;
-        if (dev < 64)
-            set.fetch_or((uint64_t)1 << dev, std::memory_order_release);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)((a.units + (a.err ? 1 : 0)) * a.cs));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = sizeof(SM);
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = a.cs;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, cache_attn_kernel<T, D, NT, true>, a);
     }
-    if ((e = launch_dependent(cache_attn_kernel<T, D, NT>, dim3(a.ncta), dim3(kThreads), smem, st, a)) != cudaSuccess)
+    static std::atomic<uint64_t> done{0};
+    if ((e = allow(cache_attn_kernel<T, D, NT, false>, (int)(sizeof(SM) + sizeof(int) * (kMaxRows + 1)), done)) != cudaSuccess)
+        return e;
+    const size_t smem = sizeof(SM) + (a.idx ? 0 : sizeof(int) * (size_t)(a.g.B + 1));
+    if ((e = launch_dependent(cache_attn_kernel<T, D, NT, false>, dim3(a.ncta), dim3(kThreads), smem, st, a)) != cudaSuccess)
         return e;
     // index rows that are whole (see launch_cache_attn) leave nothing to join: the error word alone
     const int64_t rows = a.idx && a.quantum == a.g.S ? 0 : (int64_t)a.g.ntok * a.g.Hq, most = (int64_t)num_sms() * 8;
     if (rows <= most)
-        return launch_dependent(cache_join_kernel<T, D, 8>, dim3((unsigned)rows + 1), dim3(256), 0, st, a, NT * 8, err);
-    return launch_dependent(cache_join_kernel<T, D, 2>, dim3((unsigned)(rows < 4 * most ? rows : 4 * most) + 1), dim3(64), 0, st, a, NT * 8, err);
+        return launch_dependent(cache_join_kernel<T, D, 8>, dim3((unsigned)rows + 1), dim3(256), 0, st, a, NT * 8, a.err);
+    return launch_dependent(cache_join_kernel<T, D, 2>, dim3((unsigned)(rows < 4 * most ? rows : 4 * most) + 1), dim3(64), 0, st, a, NT * 8, a.err);
 }
 
-template <typename T> cudaError_t attn_d(const AttnArgs &a, int nt, int *err, cudaStream_t st)
+template <typename T> cudaError_t attn_d(const AttnArgs &a, int nt, cudaStream_t st)
 {
 #define NSA_NT(D)                                   \
     switch (nt) {                                   \
-    case 1: return attn_t<T, D, 1>(a, err, st);     \
-    case 2: return attn_t<T, D, 2>(a, err, st);     \
-    default: return attn_t<T, D, 4>(a, err, st);    \
+    case 1: return attn_t<T, D, 1>(a, st);     \
+    case 2: return attn_t<T, D, 2>(a, st);     \
+    default: return attn_t<T, D, 4>(a, st);    \
     }
     if (a.g.D == 128)
         NSA_NT(128)
@@ -1025,7 +1200,7 @@ int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)
                : (int64_t)g.B * (c.cols + start_cost(g)) * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
 }
 
-size_t cache_attn_ws_bytes(const Geo &g, bool sel) { return attn_layout(g, sel).total; }
+size_t cache_attn_ws_bytes(const Geo &g, const Cache &c, bool sel) { return cluster_size(g, c, sel) > 0 ? 256 : attn_layout(g, sel).total; }
 
 cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const int *idx, const float *sinks, void *o,
                               float *lse, int dtype, char *ws, cudaStream_t st)
@@ -1043,6 +1218,13 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     const int nt = row_tile(g, sel);
     a.row_tiles = (g.G + nt * 8 - 1) / (nt * 8);
     a.ncta = ctas_of(g, sel);
+    a.cs = cluster_size(g, c, sel);
+    a.err = (int *)ws;
+    if (a.cs > 0) {
+        if (!sel)
+            a.row_tiles = (int)(((int64_t)g.T * g.G + nt * 8 - 1) / (nt * 8));
+        a.units = (sel ? g.ntok : g.B) * g.Hkv * a.row_tiles;
+    }
     // a run is cut at multiples of 128 tokens, a step of the CTA's warps; of
     // index rows, whole ones where that leaves the fullest CTA at most a
     // quarter above the average (nothing is to join then)
@@ -1063,8 +1245,7 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     a.by_tiles = FastDiv(a.row_tiles);
     a.by_ncta = FastDiv(a.ncta);
     a.by_quantum = FastDiv(a.quantum);
-    int *err = (int *)ws;
-    return dtype == NSA_DTYPE_BF16 ? attn_d<__nv_bfloat16>(a, nt, err, st) : attn_d<float>(a, nt, err, st);
+    return dtype == NSA_DTYPE_BF16 ? attn_d<__nv_bfloat16>(a, nt, st) : attn_d<float>(a, nt, st);
 }
 
 }  // namespace nsa

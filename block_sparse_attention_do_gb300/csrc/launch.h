@@ -148,7 +148,8 @@ cudaError_t launch_cache_append(const Geo &g, const Cache &c, const void *k, con
 bool cache_chunk_supported(const Geo &g, int dtype, bool sel);
 cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, const float *sinks, void *o, float *lse, int *err,
                                cudaStream_t st);
-size_t cache_attn_ws_bytes(const Geo &g, bool sel);
+// 256: nothing but the error word, and ws may be null
+size_t cache_attn_ws_bytes(const Geo &g, const Cache &c, bool sel);
 int cache_attn_max_rows();  // sequences of a call without an index
 // upper bound on the call's list of pages (counted in int)
 int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel);

@@ -1317,7 +1317,7 @@ size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *pc, i
     const bool thd = p->layout == NSA_LAYOUT_THD;
     if (cache_geo(p, &shape, thd ? kFakeCuQ : nullptr, selection != 0, 0, g, c) != NSA_OK)
         return 0;
-    return cache_chunk_supported(g, p->dtype, selection != 0) ? kAlign : cache_attn_ws_bytes(g, selection != 0);
+    return cache_chunk_supported(g, p->dtype, selection != 0) ? kAlign : cache_attn_ws_bytes(g, c, selection != 0);
 }
 
 nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t window, const int32_t *cu_seqlens,
@@ -1336,11 +1336,13 @@ nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t wind
     // the list of pages is counted in int, and its prefix over the sequences sits in shared memory
     if (!chunk && (cache_attn_entries(g, c, sel) >= INT32_MAX || (!sel && g.B > cache_attn_max_rows())))
         return NSA_ERR_UNSUPPORTED;
-    if ((s = check_ws(ws, ws_bytes, chunk ? kAlign : cache_attn_ws_bytes(g, sel))) != NSA_OK)
+    const size_t need = chunk ? kAlign : cache_attn_ws_bytes(g, c, sel);
+    if ((ws || need > kAlign) && (s = check_ws(ws, ws_bytes, need)) != NSA_OK)
         return s;
     cudaStream_t st = (cudaStream_t)stream;
     if (chunk) {
-        NSA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));
+        if (ws)
+            NSA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));
         NSA_LAUNCH("cache_chunk", launch_cache_chunk(g, c, q, sinks, o, lse, (int *)ws, st));
         return NSA_OK;
     }

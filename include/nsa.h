@@ -522,7 +522,9 @@ nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *c, const int3
  * anything, NaN included.  Rows of THD tensors that belong to no sequence are
  * left as they were.  p->B = rows, p->Hkv, D and block_size the cache's,
  * p->kv_stride unused.  `selection`: whether block_idx will be given.
- * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).
+ * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).  A call that
+ * needs a workspace of 256 bytes needs it for the error word alone: its ws may
+ * be NULL, and errors are then not reported.
  */
 size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *c, int32_t selection);
 nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *c, int32_t window, const int32_t *cu_seqlens,

@@ -59,8 +59,8 @@ def test_workspace_sizes(lib):
     assert lib.nsa_cache_workspace_size(cache()) == 256 + 3 * up(400) + 2 * up(12)
     for kw in SHAPES + LIMITS + (dict(stride=(64, 24, 16)),):
         assert lib.nsa_cache_workspace_size(cache(**kw)) == 0, kw
-    assert lib.nsa_cache_fwd_workspace_size(problem(), cache(), 0) > 256
-    assert lib.nsa_cache_fwd_workspace_size(problem(), cache(k=None, page_table=None), 1) > 256
+    assert lib.nsa_cache_fwd_workspace_size(problem(), cache(), 0) >= 256
+    assert lib.nsa_cache_fwd_workspace_size(problem(), cache(k=None, page_table=None), 1) >= 256
     for kw in (dict(B=2), dict(Hq=3), dict(D=64), dict(block_size=32), dict(T=0)):
         assert lib.nsa_cache_fwd_workspace_size(problem(**kw), cache(), 0) == 0, kw
     assert lib.nsa_cache_fwd_workspace_size(problem(S=0), cache(), 1) == 0
