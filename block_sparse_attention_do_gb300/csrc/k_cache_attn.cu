@@ -609,14 +609,20 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                     vs = fmaxf(c.vs[(int64_t)my_page * c.Hkv + u.kvh], kScaleFloor);
                 }
                 sm.sc[tid] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
-                if (sel && my_page >= 0) {  // an entry that its row has before is left out: no row attends its keys
-                    bool twice = false;
-                    for (int k = 0; k < e0 + tid - u.begin; ++k)
-                        twice |= a.idx[irow + k] == my_block;
-                    if (twice) {
-                        bad = true;
-                        sm.key0[tid] = kNoKey;
+            }
+            if (sel && warp * 32 < ne) {  // an entry that its row has before is left out: no row attends its keys
+                bool twice = false;
+                const int s = e0 + tid - u.begin;  // (warp-uniform rounds of 32 of the row's entries)
+                for (int k0 = 0; k0 < min(g.S, e0 + warp * 32 + 32 - u.begin); k0 += 32) {
+                    const int v = k0 + lane < g.S ? a.idx[irow + k0 + lane] : -1;
+                    for (int k = 0; k < min(32, g.S - k0); ++k) {
+                        const int w = __shfl_sync(0xffffffffu, v, k);
+                        twice |= k0 + k < s && w == my_block;
                     }
+                }
+                if (tid < ne && my_page >= 0 && twice) {
+                    bad = true;
+                    sm.key0[tid] = kNoKey;
                 }
             }
             __syncthreads();
@@ -875,33 +881,39 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                 return;
             cg::cluster_group cl = cg::this_cluster();
             cl.sync();
-            for (int x = tid * a.cs + rank; x < u.nrows * (D / 4); x += kThreads * a.cs) {
-                const int r = x / (D / 4), d = x % (D / 4) * 4;
-                float top = kNoMax;
-#pragma unroll 4
-                for (int k = 0; k < a.cs; ++k)
-                    top = fmaxf(top, cl.map_shared_rank(&sm.cta_ml[r], k)->x);
-                float f = 1.f, sum = 0.f;
-                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+            // cs threads to an output vector, one for each CTA's sum
+            const int k = tid & (a.cs - 1), per = kThreads / a.cs, n = u.nrows * (D / 4);
+            for (int x0 = rank * per; x0 < n; x0 += kThreads) {  // (uniform over the block)
+                const int x = x0 + tid / a.cs, r = min(x, n - 1) / (D / 4), d = x % (D / 4) * 4;
+                const float2 ml = *cl.map_shared_rank(&sm.cta_ml[r], k);
+                float4 y = *(const float4 *)cl.map_shared_rank(&sm.o[0][r][d], k);
+                float top = ml.x;
+                for (int i = 1; i < a.cs; i <<= 1)
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, i));
+                float sink = 0.f;
                 if (a.sinks) {
                     int hh;
                     a.by_G.divmod(u.row0 + r, hh);
                     const float sk = a.sinks[u.kvh * g.G + hh] * 1.4426950408889634f;
                     top = fmaxf(top, sk);
-                    sum = exp2f(sk - top);
+                    sink = exp2f(sk - top);
                 }
-#pragma unroll 4
-                for (int k = 0; k < a.cs; ++k) {
-                    const float2 ml = *cl.map_shared_rank(&sm.cta_ml[r], k);
-                    const float4 p = *(const float4 *)cl.map_shared_rank(&sm.o[0][r][d], k);
-                    f = exp2f(ml.x - top);
-                    sum += ml.y * f;
-                    y.x += p.x * f, y.y += p.y * f, y.z += p.z * f, y.w += p.w * f;
+                float f = exp2f(ml.x - top), sum = ml.y * f;
+                y.x *= f, y.y *= f, y.z *= f, y.w *= f;
+                for (int i = 1; i < a.cs; i <<= 1) {
+                    sum += __shfl_xor_sync(0xffffffffu, sum, i);
+                    y.x += __shfl_xor_sync(0xffffffffu, y.x, i);
+                    y.y += __shfl_xor_sync(0xffffffffu, y.y, i);
+                    y.z += __shfl_xor_sync(0xffffffffu, y.z, i);
+                    y.w += __shfl_xor_sync(0xffffffffu, y.w, i);
                 }
+                sum += sink;
                 f = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
-                store4((T *)a.o + sm.o_at[r] + d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
-                if (d == 0)
-                    a.lse[sm.lse_at[r]] = lse_of(top, sum);
+                if (k == 0 && x < n) {
+                    store4((T *)a.o + sm.o_at[r] + d, make_float4(y.x * f, y.y * f, y.z * f, y.w * f));
+                    if (d == 0)
+                        a.lse[sm.lse_at[r]] = lse_of(top, sum);
+                }
             }
             cl.sync();  // no CTA leaves while another reads its sums
             return;
