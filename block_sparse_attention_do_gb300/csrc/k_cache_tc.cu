@@ -10,9 +10,9 @@
 //                       tile's loads in flight as soon as the one before is
 //                       stored) to halves in shared memory, 128 keys x D,
 //                       128-byte swizzled
-//   1 issuing thread    S_q = Q_q K^T and O_q += P_q V for the two tiles of
-//                       128 rows, q = 0, 1, in turn: one tile's softmax runs
-//                       under the other's products
+//   2 issuing warps     S_q = Q_q K^T and O_q += P_q V for the tile q = 0, 1
+//                       of 128 rows: one tile's softmax runs under the
+//                       other's products
 //   2 x 4 softmax warps a row per thread: maximum, exponentials, P as halves
 //                       over S's own columns of tensor memory
 // Halves hold e4m3 exactly, bf16 queries scaled by a power of two per row
@@ -43,7 +43,7 @@ constexpr float kNoMax = -1e30f, kLazy = 10.f;
 constexpr float kTiny = 1.17549435e-38f;    // keeps kNoScore * scale from being a NaN
 constexpr uint32_t kNoScore = 0xff800000u;  // -infinity
 
-enum { B_Q, B_KF, B_KE = B_KF + kStages, B_VF = B_KE + kStages, B_VE = B_VF + kStages, B_SF = B_VE + kStages, B_P = B_SF + 2, B_O = B_P + 2, B_COUNT };
+enum { B_Q, B_KF, B_KE = B_KF + kStages, B_VF = B_KE + kStages, B_VE = B_VF + kStages, B_SF = B_VE + kStages, B_P = B_SF + 2, B_TURN = B_P + 4, B_O = B_TURN + 2, B_COUNT };
 
 struct Params {
     Geo g;
@@ -98,8 +98,10 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // 16-byte chunk c of row r in a tile of 128-byte rows, 128-byte swizzled
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) { return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const Params p)
+// D and BS, the tokens of a page, are the cache's.
+template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kernel(const Params p)
 {
+    constexpr int PAGES = kTileKeys / BS;
     using L = Layout<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
@@ -144,14 +146,16 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&bars[B_KF + s], kConvWarps / 2 * 32);
             mbar_init(&bars[B_VF + s], kConvWarps / 2 * 32);
-            mbar_init(&bars[B_KE + s], 1);
-            mbar_init(&bars[B_VE + s], 1);
+            mbar_init(&bars[B_KE + s], 2);
+            mbar_init(&bars[B_VE + s], 2);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&bars[B_SF + x], 1);
-            mbar_init(&bars[B_P + x], 128);
+            mbar_init(&bars[B_P + 2 * x], 128);  // tile x, the first half of a tile's keys
+            mbar_init(&bars[B_P + 2 * x + 1], 128);
+            mbar_init(&bars[B_TURN + x], 1);
         }
-        mbar_init(&bars[B_O], 1);
+        mbar_init(&bars[B_O], 2);
         fence_barrier_init();
     }
     if (warp == kSoftmaxWarps + kConvWarps) {
@@ -209,7 +213,6 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
             mbar_arrive(&bars[B_Q]);
         }
         float m = kNoMax, l = 0.f;
-        const int page_sh = c.bsh;
         bool ok = true;
         for (int i = 0; i < ntiles; ++i) {
             const int j = j0 + i;
@@ -231,19 +234,23 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                 for (int e = 0; e < 128; ++e)
                     s[e] = e <= cmax && e >= cmin ? s[e] : kNoScore;
             }
-            // ---- the row's maximum; 16 columns lie in one page
+            // ---- the row's maximum, page by page
             float top = -INFINITY;
+            float4 f[PAGES];
 #pragma unroll
-            for (int k = 0; k < 128; k += 16) {
-                float y0 = __uint_as_float(s[k]), y1 = __uint_as_float(s[k + 1]);
+            for (int n = 0; n < PAGES; ++n)
+                f[n] = sc[n];
 #pragma unroll
-                for (int e = 2; e < 16; e += 4) {
-                    y0 = max3(y0, __uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1]));
-                    if (e + 2 < 16)
-                        y1 = max3(y1, __uint_as_float(s[k + e + 2]), __uint_as_float(s[k + e + 3]));
-                }
-                const float4 f = sc[k >> page_sh];
-                top = fmaxf(top, fmaf(fmaxf(y0, y1), fmaxf(f.x * qmul, kTiny), f.y));
+            for (int n = 0; n < PAGES; ++n) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[e] = __uint_as_float(s[n * BS + e]);
+#pragma unroll
+                for (int e = 4; e < BS; e += 2)
+                    y[e / 2 % 4] = max3(y[e / 2 % 4], __uint_as_float(s[n * BS + e]), __uint_as_float(s[n * BS + e + 1]));
+                f[n].x = fmaxf(f[n].x * qmul, kTiny);
+                top = fmaxf(top, fmaf(fmaxf(max3(y[0], y[1], y[2]), y[3]), f[n].x, f[n].y));
             }
             const bool raise = top > m + kLazy;  // (no column attended: top is -infinity)
             if (__any_sync(0xffffffffu, raise)) {
@@ -264,34 +271,36 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                     tmem_wait_st();
                 }
             }
-            // ---- weights: P over the columns of S
+            // ---- weights: P over the columns of S, handed on by halves
 #pragma unroll
-            for (int cc = 0; cc < 128; cc += 64) {
+            for (int hf = 0; hf < 2; ++hf) {
                 uint32_t w[32];
 #pragma unroll
-                for (int k = cc; k < cc + 64; k += 16) {
-                    const float4 f = sc[k >> page_sh];
-                    const float mul = fmaxf(f.x * qmul, kTiny), add = f.y - m;
-                    const uint64_t mul2 = f2(mul, mul), add2 = f2(add, add);
-                    uint64_t sum2 = f2(0.f, 0.f);
+                for (int n = 0; n < (PAGES + 1) / 2; ++n) {
+                    constexpr int COLS = BS < 64 ? BS : 64;
+                    const float4 fn = f[hf * (PAGES / 2) + n];
+                    const float add = fn.y - m;
+                    const uint64_t mul2 = f2(fn.x, fn.x), add2 = f2(add, add);
+                    uint64_t sum[2];
 #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
+                    for (int e = 0; e < COLS; e += 2) {
+                        const int k = hf * 64 + n * COLS + e;
                         float x0, x1;
-                        f2_split(f2_fma(f2(__uint_as_float(s[k + e]), __uint_as_float(s[k + e + 1])), mul2, add2), x0, x1);
+                        f2_split(f2_fma(f2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), mul2, add2), x0, x1);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
-                        sum2 = f2_add(sum2, f2(x0, x1));
-                        w[(k - cc + e) >> 1] = pack_half(x0, x1);
+                        sum[e / 2 % 2] = e >= 4 ? f2_add(sum[e / 2 % 2], f2(x0, x1)) : f2(x0, x1);
+                        w[(n * COLS + e) >> 1] = pack_half(x0, x1);
                     }
                     float a0, a1;
-                    f2_split(sum2, a0, a1);
-                    l = fmaf(a0 + a1, f.z, l);
+                    f2_split(f2_add(sum[0], sum[1]), a0, a1);
+                    l = fmaf(a0 + a1, fn.z, l);
                 }
-                tmem_st32(s_at + cc / 2, w);
+                tmem_st32(s_at + hf * 32, w);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars[B_P + q * 2 + hf]);
             }
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars[B_P + q]);
         }
         // ---- O / l
         if (ok && ntiles > 0)
@@ -320,10 +329,10 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                         key |= kTileKeys - 1;
                         continue;
                     }
-                    const int page = c.table[(int64_t)b * c.cols + (key >> c.bsh)];
+                    const int page = c.table[(int64_t)b * c.cols + (key / BS)];
                     if (page < 0 || page >= c.pages)
                         continue;
-                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (c.bs - 1)) * c.st;
+                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (BS - 1)) * c.st;
 #pragma unroll
                     for (int x = 0; x < D / 4; ++x) {
                         const uint32_t u = ((const uint32_t *)v)[x] & 0x7f7f7f7fu, hit = (u + 0x01010101u) & 0x80808080u;
@@ -368,7 +377,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
         const int cw = warp - kSoftmaxWarps, half = cw & 1;
         const bool values = cw >= 2;
         const int sub = D == 128 ? (lane & 3) | (lane >> 4 & 1) << 2 : lane & 3, key_in = D == 128 ? lane >> 2 & 3 : lane >> 2;
-        const int page_sh = c.bsh, npages = kTileKeys >> page_sh;
+        constexpr int page_sh = BS == 64 ? 6 : BS == 32 ? 5 : 4, npages = PAGES;
         const int st = (int)c.st;
         const uint8_t *pool = (values ? c.v : c.k) + (int64_t)kvh * c.sh + sub * 16;
         const int last_page = pmax >> page_sh, first_page = key_first >> page_sh;
@@ -398,7 +407,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
                 const int page = __shfl_sync(0xffffffffu, id, (half * KEYS + n * 16) >> page_sh);
                 there[n] = page >= 0;
                 all = all && there[n];
-                at[n] = pool + (int64_t)page * c.sp + (((first + n * 16) & (c.bs - 1)) + key_in) * st;
+                at[n] = pool + (int64_t)page * c.sp + (((first + n * 16) & (BS - 1)) + key_in) * st;
             }
             if (all) {
 #pragma unroll
@@ -477,77 +486,75 @@ template <int D> __global__ void __launch_bounds__(kThreads, 1) cache_chunk_kern
             set_error(p.err, NSA_ERR_BAD_INDEX);
     } else {
         setmaxnreg_dec<kRegsMma>();
-        if (warp == kSoftmaxWarps + kConvWarps) {
+        const int q = warp - kSoftmaxWarps - kConvWarps;
+        if (q < 2) {
             // ---------------------------------------------------------- MMA
-            // The whole warp walks the loop, so that descriptors stay in
-            // uniform registers, and one elected lane issues.
+            // One warp per tile of rows (one for both, on a scheduler that
+            // also runs softmax and converter warps, issues a product only
+            // every 100 cycles or so).  The whole warp walks the loop, so that
+            // descriptors stay in uniform registers, and one elected lane issues.
             const uint32_t idS = idesc_f16(128, 128, false), idO = idesc_f16(128, D, true);
-            const uint64_t q_d = sdesc_sw128(smem_u32(sm + L::q), 16, 1024), k_d = sdesc_sw128(smem_u32(sm + L::k), 16, 1024),
+            const uint64_t q_d = sdesc_sw128(smem_u32(sm + L::q) + q * L::kTile, 16, 1024), k_d = sdesc_sw128(smem_u32(sm + L::k), 16, 1024),
                            v_d = sdesc_sw128(smem_u32(sm + L::v), L::kHalf, 1024);
-            auto product_s = [&](int q, int s) {
+            const uint32_t tm_s = tmem + TM_S + q * 128, tm_o = tmem + TM_O + q * 128;
+            auto product_s = [&](int s) {
+                const uint64_t k_s = k_d + (s * L::kTile >> 4);
                 if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const int at = ((kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4;
-                        mma_bf16(tmem + TM_S + q * 128, q_d + (q * L::kTile >> 4) + at, k_d + (s * L::kTile >> 4) + at, idS, kk > 0);
+                        mma_bf16(tm_s, q_d + at, k_s + at, idS, kk > 0);
                     }
+                    mma_commit(&bars[B_SF + q]);
+                    mma_commit(&bars[B_KE + s]);
                 }
                 __syncwarp();
             };
-            auto product_o = [&](int q, int s, bool add) {
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kTileKeys / 16; ++kk)
-                        mma_bf16_ts(tmem + TM_O + q * 128, tmem + TM_S + q * 128 + kk * 8, v_d + (s * L::kTile >> 4) + (kk * 2048 >> 4),
-                                    idO, add || kk > 0);
-                }
-                __syncwarp();
-            };
-            auto commit = [&](int bar) {
-                if (elect_one())
-                    mma_commit(&bars[bar]);
-                __syncwarp();
-            };
+            // The warps take turns: a turn is P_q V and the next S_q, so that
+            // one tile's softmax lies under the other's products (left to
+            // themselves the two fall into step: 449 us for 389).
             bool ok = ntiles > 0 && mbar_wait_warp(&bars[B_Q], 0, ctx) && mbar_wait_warp(&bars[B_KF], 0, ctx);
             if (ok) {
                 fence_async_smem();  // the converters' writes, for the tensor cores
                 tc_fence_after();
-                product_s(0, 0);
-                commit(B_SF + 0);
-                product_s(1, 0);
-                commit(B_SF + 1);
-                commit(B_KE + 0);
+                product_s(0);
             }
             for (int i = 0; ok && i < ntiles; ++i) {
                 const int s = i % kStages, s1 = (i + 1) % kStages;
                 const bool more = i + 1 < ntiles;
-                ok = mbar_wait_warp(&bars[B_VF + s], (i / kStages) & 1, ctx);
+                ok = mbar_wait_warp(&bars[B_VF + s], (i / kStages) & 1, ctx) &&
+                     (!more || mbar_wait_warp(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx)) &&
+                     mbar_wait_warp(&bars[B_P + q * 2], i & 1, ctx) &&
+                     (q == 1 ? mbar_wait_warp(&bars[B_TURN + 1], i & 1, ctx) : i == 0 || mbar_wait_warp(&bars[B_TURN], (i - 1) & 1, ctx));
+                if (!ok)
+                    break;
                 fence_async_smem();
+                tc_fence_after();
+                const uint64_t v_s = v_d + (s * L::kTile >> 4);
+                auto product_o = [&](int hf) {  // 64 keys
+                    if (elect_one()) {
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    ok = ok && mbar_wait_warp(&bars[B_P + q], i & 1, ctx);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    product_o(q, s, i > 0);
-                    if (q == 1)
-                        commit(B_VE + s);
-                    if (!more)
-                        continue;
-                    if (q == 0 && !(ok = mbar_wait_warp(&bars[B_KF + s1], ((i + 1) / kStages) & 1, ctx)))
-                        break;
-                    if (q == 0)
-                        fence_async_smem();
-                    tc_fence_after();
-                    // over P_q, once the product that reads it is done: issued behind it
-                    product_s(q, s1);
-                    commit(B_SF + q);
-                    if (q == 1)
-                        commit(B_KE + s1);
-                }
+                        for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)
+                            mma_bf16_ts(tm_o, tm_s + kk * 8, v_s + (kk * 2048 >> 4), idO, i > 0 || kk > 0);
+                        if (hf == 1)
+                            mma_commit(&bars[B_VE + s]);
+                    }
+                    __syncwarp();
+                };
+                product_o(0);  // while the softmax takes the second half
+                if (!(ok = mbar_wait_warp(&bars[B_P + q * 2 + 1], i & 1, ctx)))
+                    break;
+                tc_fence_after();
+                product_o(1);
+                if (more)  // over P_q, once the product that reads it is done: issued behind it
+                    product_s(s1);
+                if (lane == 0)
+                    mbar_arrive(&bars[B_TURN + 1 - q]);
             }
             // every product completes before tensor memory is freed
-            commit(B_O);
+            if (elect_one())
+                mma_commit(&bars[B_O]);
+            __syncwarp();
             volatile int never[2] = {0, ctx[1]};  // own limit, no abort
             mbar_wait(&bars[B_O], 0, never);
         }
@@ -584,7 +591,9 @@ cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, cons
     p.err = err;
     p.tiles = (int)(((int64_t)g.T * g.G + kTileRows - 1) / kTileRows);
     p.wait_us = wait_test().wait_us;
-    auto kernel = g.D == 128 ? cache_chunk_kernel<128> : cache_chunk_kernel<64>;
+    void (*const kernels[2][3])(const Params) = {{cache_chunk_kernel<64, 16>, cache_chunk_kernel<64, 32>, cache_chunk_kernel<64, 64>},
+                                                 {cache_chunk_kernel<128, 16>, cache_chunk_kernel<128, 32>, cache_chunk_kernel<128, 64>}};
+    auto kernel = kernels[g.D == 128][c.bsh - 4];
     const int smem = g.D == 128 ? Layout<128>::total : Layout<64>::total;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
