@@ -1203,6 +1203,8 @@ AttnLayout attn_layout(const Geo &g, bool sel)
 
 }  // namespace
 
+bool cache_attn_clustered(const Geo &g, const Cache &c, bool sel) { return cluster_size(g, c, sel) > 0; }
+
 int cache_attn_max_rows() { return kMaxRows; }
 
 int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)

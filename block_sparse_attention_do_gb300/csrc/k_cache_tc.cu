@@ -385,7 +385,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
         // page n of the sequence, -1 where no row attends a key of it
         auto page_id = [&](int n) { return n < first_page || n > last_page ? -1 : c.table[(int64_t)b * c.cols + n]; };
         auto in_pool = [&](int id, int n) {
-            if (n >= first_page && n <= last_page && (id < 0 || id >= c.pages)) {
+            if (lane < npages && n >= first_page && n <= last_page && (id < 0 || id >= c.pages)) {
                 bad = true;
                 return -1;
             }
@@ -572,10 +572,22 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
 
 }  // namespace
 
+// Rows of the longest sequence, as far as the host knows.
+static int64_t longest_rows(const Geo &g) { return (int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G; }
+
+// Where this kernel takes over from the list's (k_cache_attn.cu), whose time
+// goes by 32-row tiles, all SMs together, while a CTA here takes 256 rows by
+// itself.  Measured over 4096 cached tokens, 8 kv heads of 4 query heads: 16
+// sequences of 5, 8, 16 and 32 tokens (128 .. 512 tiles of 32 rows) 57, 62, 105
+// and 192 us by the list, 69, 69, 69 and 70 here; one of 64, 128 and 256 tokens
+// 32, 58 and 99 us there, 67, 67 and 68 here; 64 sequences of 8 and 16 (2048
+// cached, four rounds of CTAs) 127 and 237 us there, 145 and 146 here.
 bool cache_chunk_supported(const Geo &g, int dtype, bool sel)
 {
-    return !sel && dtype == NSA_DTYPE_BF16 && (g.D == 64 || g.D == 128) && (int64_t)g.T * g.G > 64 &&
-           (((int64_t)g.T * g.G + kTileRows - 1) / kTileRows) * g.B * g.Hkv < INT32_MAX;
+    const int64_t rows = longest_rows(g), seqs = (int64_t)g.B * g.Hkv;
+    const int64_t units = (rows + kTileRows - 1) / kTileRows * seqs, tiles32 = (rows + 31) / 32 * seqs;
+    return !sel && dtype == NSA_DTYPE_BF16 && (g.D == 64 || g.D == 128) && units < INT32_MAX && rows > 32 &&
+           tiles32 > 150 * ((units + num_sms() - 1) / num_sms());
 }
 
 cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, const float *sinks, void *o, float *lse, int *err,
@@ -589,7 +601,7 @@ cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, cons
     p.o = (__nv_bfloat16 *)o;
     p.lse = lse;
     p.err = err;
-    p.tiles = (int)(((int64_t)g.T * g.G + kTileRows - 1) / kTileRows);
+    p.tiles = (int)((longest_rows(g) + kTileRows - 1) / kTileRows);
     p.wait_us = wait_test().wait_us;
     void (*const kernels[2][3])(const Params) = {{cache_chunk_kernel<64, 16>, cache_chunk_kernel<64, 32>, cache_chunk_kernel<64, 64>},
                                                  {cache_chunk_kernel<128, 16>, cache_chunk_kernel<128, 32>, cache_chunk_kernel<128, 64>}};

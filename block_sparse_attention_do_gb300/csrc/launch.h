@@ -150,6 +150,7 @@ cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, cons
                                cudaStream_t st);
 // 256: nothing but the error word, and ws may be null
 size_t cache_attn_ws_bytes(const Geo &g, const Cache &c, bool sel);
+bool cache_attn_clustered(const Geo &g, const Cache &c, bool sel);
 int cache_attn_max_rows();  // sequences of a call without an index
 // upper bound on the call's list of pages (counted in int)
 int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel);

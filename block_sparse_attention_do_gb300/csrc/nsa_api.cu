@@ -1346,7 +1346,7 @@ nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t wind
         NSA_LAUNCH("cache_chunk", launch_cache_chunk(g, c, q, sinks, o, lse, (int *)ws, st));
         return NSA_OK;
     }
-    NSA_LAUNCH("cache_attn", launch_cache_attn(g, c, q, block_idx, sinks, o, lse, p->dtype, (char *)ws, st));
+    NSA_LAUNCH(cache_attn_clustered(g, c, sel) ? "cache_attn_cluster" : "cache_attn", launch_cache_attn(g, c, q, block_idx, sinks, o, lse, p->dtype, (char *)ws, st));
     return NSA_OK;
 }
 

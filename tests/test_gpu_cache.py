@@ -478,6 +478,148 @@ def test_calls_on_two_streams_and_in_graphs():
             assert all(torch.equal(x, y) for x, y in zip(a, b)) and all(torch.equal(x, y) for x, y in zip(a, c))
 
 
+# --------------------------------------- each of the attention's three forms
+
+def form_of(call):
+    """The name under which the call's kernel was launched: the form it took."""
+    api.trace_enable(64)
+    try:
+        call()
+        torch.cuda.synchronize()
+        return [name for name, _ in api.trace_records()][-1]
+    finally:
+        api.trace_enable(0)
+
+
+def takes(form, *a, **kw):
+    assert form_of(lambda: attend_case(*a, **kw)) == form
+
+
+MASKS = [dict(), dict(window=1), dict(window=37), dict(window=200), dict(sinks=True), dict(window=70, sinks=True)]
+
+
+@pytest.mark.parametrize("kw", MASKS)
+@pytest.mark.parametrize("Hq,Hkv,D,bs", [(16, 8, 128, 64), (8, 8, 64, 16), (24, 8, 128, 32), (40, 8, 64, 64), (16, 8, 128, 16),
+                                         (16, 8, 64, 32)])
+def test_chunk_form(kw, Hq, Hkv, D, bs):
+    T = -(-256 // (Hq // Hkv))  # 256 rows and, of the last sequence, some more
+    lens, new = [T + 130, 40, 0, 3 * T, T + 1], [T, 40, 0, 1, T + 1]
+    takes("cache_chunk", lens, new, Hq, Hkv, D, bs, BF, ragged=True, **kw)
+
+
+@pytest.mark.parametrize("layout", ["dense", "token", "both"])
+def test_chunk_form_fixed_length(layout):
+    """Rows before the first key, one tile of rows and a part of another, strided pools."""
+    takes("cache_chunk", [100, 500, 3, 150], [150] * 4, 16, 8, 128, 64, BF, layout=layout)
+    takes("cache_chunk", [100, 500, 3, 150], [150] * 4, 16, 8, 64, 16, BF, layout=layout, sinks=True, window=90)
+
+
+def test_chunk_form_long():
+    takes("cache_chunk", [1500, 700], [600, 700], 16, 2, 128, 64, BF, ragged=True)
+
+
+@pytest.mark.parametrize("D,bs", [(128, 64), (64, 16)])
+def test_chunk_form_nan_values(D, bs):
+    """NaN among the chunk's own tokens (some rows see them) and among earlier
+    ones (every row does; with the window the early rows alone), values and a key."""
+    def edit(cache):
+        for t, h, d in ((150, 0, 3), (199, 1, 30), (199, 0, D - 1), (130, 7, 0), (20, 3, 11)):
+            p = int(cache.page_table[0, t // bs])
+            cache.v.view(torch.uint8)[p, h, t % bs, d] = 0xff
+        p = int(cache.page_table[1, 180 // bs])
+        cache.k.view(torch.uint8)[p, 2, 180 % bs, 5] = 0x7f
+    for kw in (dict(), dict(window=60)):
+        takes("cache_chunk", [200, 230, 90, 160], [130, 130, 90, 160], 16, 8, D, bs, BF, ragged=True, edit=edit, **kw)
+
+
+def test_chunk_form_scales_and_bad_pages():
+    def edit(cache):
+        cache.v_scale[::2] = 2.0 ** -60
+        cache.v_scale[1::3] = 2.0 ** 40
+        cache.k_scale[::3] *= 2.0 ** -20
+        cache.k_scale[1::5] = 0.0
+    takes("cache_chunk", [300, 700], [300, 200], 16, 8, 128, 64, BF, ragged=True, edit=edit)
+    cache = filled([700, 400], 8, 128, 64, 3)
+    q = torch.randn(2, 16, 400, 128, device=DEV).to(BF)
+    cu = torch.tensor([0, 400, 800], dtype=torch.int32, device=DEV)
+    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    packed = q.transpose(1, 2).reshape(800, 16, 128).contiguous()
+    for bad in (-1, -9, cache.k.shape[0], 2 ** 31 - 1):
+        cache.page_table[0, 2] = bad
+        o, lse = api.cache_fwd(packed, cache, cu_seqlens=cu, max_seqlen=400, ws=ws)
+        assert api.get_error(ws) == 3
+        # the page's tokens are absent: the same rows with those keys out of every row's scores
+        plain = Plain(cache)
+        plain.table = plain.table.copy()
+        plain.table[0, 2] = 0
+        for t in (0, 250, 399):
+            K, V = plain.keys(0, 3)
+            keep = np.ones(301 + t, bool)
+            keep[128:192] = False
+            z = K[:301 + t][keep] @ packed[t, 7].double().cpu().numpy() / math.sqrt(128)
+            w = np.exp(z - z.max())
+            want = w @ V[:301 + t][keep] / w.sum()
+            tol = 2.0 ** -8 * np.abs(want) + (2.0 ** -10 + 2.0 ** -14) * np.abs(V[:301 + t][keep]).max()
+            assert (np.abs(o[t, 7].double().cpu().numpy() - want) <= tol).all()
+    cache.page_table[0, 2] = 0
+    lens = cache.seq_lens.clone()
+    for n in (-1, 11 * 64 + 1, 2 ** 31 - 1):
+        cache.seq_lens[1] = n
+        api.cache_fwd(packed, cache, cu_seqlens=cu, max_seqlen=400, ws=ws)
+        assert api.get_error(ws) == 3
+    cache.seq_lens.copy_(lens)
+    api.cache_fwd(packed, cache, cu_seqlens=cu, max_seqlen=400, ws=ws)
+    assert api.get_error(ws) == 0
+
+
+def test_chunk_form_leaves_rows_behind_the_last_sequence():
+    cache = filled([400, 300], 8, 64, 32, 1)
+    cu = torch.tensor([0, 300, 600], dtype=torch.int32, device=DEV)
+    q = torch.randn(620, 16, 64, device=DEV).to(BF)
+    p = api.problem(2, 16, 8, 300, 64, 32, 1, BF, layout=api.LAYOUT_THD, total_tokens=620)
+    o, lse = torch.full((620, 16, 64), 7.0, device=DEV).to(BF), torch.full((620, 16), 7.0, device=DEV)
+    call = lambda: api._check(api.lib().nsa_cache_fwd(p, cache.ref, 0, cu.data_ptr(), None, None, q.data_ptr(), o.data_ptr(), lse.data_ptr(), None, 0, api._stream()), "fwd")  # noqa: E731
+    assert form_of(call) == "cache_chunk"
+    assert (o[600:] == 7).all() and (lse[600:] == 7).all() and (lse[:600] != 7).all()
+
+
+@pytest.mark.parametrize("kw", MASKS + [dict(S=1), dict(S=5), dict(S=40)])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,bs,T", [(BF, 8, 2, 128, 64, 1), (F32, 6, 2, 64, 32, 2), (BF, 32, 2, 128, 16, 1),
+                                                 (F32, 2, 1, 32, 16, 7), (BF, 20, 1, 64, 64, 1), (F32, 16, 1, 128, 64, 1)])
+def test_list_form(kw, dtype, Hq, Hkv, D, bs, T):
+    g = np.random.default_rng(5)
+    B = 320 // Hkv
+    lens = [int(n) for n in g.integers(0, 300, B)]
+    takes("cache_attn", lens, [T] * B, Hq, Hkv, D, bs, dtype, **kw)
+
+
+@pytest.mark.parametrize("T", [1, 4])
+def test_list_form_nan_values(T):
+    def edit(cache):
+        for b in (0, 17, 100):
+            t = int(cache.seq_lens[b]) - 1
+            p = int(cache.page_table[b, t // 32])
+            cache.v.view(torch.uint8)[p, 1, t % 32, 5] = 0x7f
+    g = np.random.default_rng(6)
+    takes("cache_attn", [int(n) for n in g.integers(4, 200, 160)], [T] * 160, 8, 2, 64, 32, BF, edit=edit)
+
+
+@pytest.mark.parametrize("kw", MASKS + [dict(S=1), dict(S=5), dict(S=40)])
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (2, 2), (5, 4), (12, 8)])
+def test_cluster_form(kw, B, Hkv):
+    """One CTA a unit (12 x 8) up to 16 (one unit alone)."""
+    g = np.random.default_rng(7)
+    lens = [int(n) for n in g.integers(0, 700, B)]
+    for dtype, G, D, bs, T in ((BF, 4, 128, 64, 1), (F32, 3, 64, 16, 4), (BF, 20, 32, 32, 1)):
+        T = 1 if "S" in kw else T  # (a unit for each token there)
+        takes("cache_attn_cluster", lens, [T] * B, Hkv * G, Hkv, D, bs, dtype, **kw)
+
+
+def test_one_long_sequence_takes_the_cluster_form_and_a_longer_one_the_list():
+    takes("cache_attn_cluster", [9000], [1], 4, 2, 128, 64, BF)
+    takes("cache_attn", [66000], [1], 4, 1, 128, 64, BF)
+
+
 # ------------------------------------------------------------------ append
 
 def same_pool(cache, plain):
