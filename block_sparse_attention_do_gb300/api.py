@@ -609,7 +609,7 @@ class KVCache:
             _int32(refcount, "KVCache: refcount", dev, (k.shape[0],))
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.page_table, self.seq_lens, self.refcount = page_table, seq_lens, refcount
-        self.device = dev
+        self.device, self.index = dev, dev.index
         s = CacheStruct(k.shape[0], k.shape[1], k.shape[3], k.shape[2], page_table.shape[0], page_table.shape[1])
         if not k.is_contiguous():
             s.stride[:] = k.stride()[:3]
@@ -631,6 +631,8 @@ class KVCache:
         if got is None:
             s = self.struct
             _need(x.dtype in DTYPE and x.shape[-1] == s.D, "cache: float32 or bfloat16 rows of the cache's head dimension")
+            _need(x.dim() == (4 if cu_seqlens is None else 3) and (cu_seqlens is not None or x.shape[0] == s.rows),
+                  "cache: x is [rows, heads, T, D], or packed [total, heads, D] with cu_seqlens")
             Hq = x.shape[1]
             if cu_seqlens is None:
                 p = problem(x.shape[0], Hq, s.Hkv, x.shape[2], s.D, s.block_size, S, x.dtype, scale=scale)
@@ -644,10 +646,11 @@ class KVCache:
                 if n == 0:
                     raise NsaError(1, "nsa_cache_fwd_workspace_size")
             else:
+                _need(Hq == s.Hkv, "cache: new keys and values have the cache's heads")
                 declare_strides(p, cu_seqlens is not None, k=x)
             if len(self._problems) >= 256:
                 self._problems.clear()
-            got = self._problems[key] = (p, C.byref(p), n)
+            got = self._problems[key] = (p, C.byref(p), n, x.shape[:-1], x.is_contiguous())
         return got
 
 
@@ -665,13 +668,13 @@ def make_cache(num_pages, Hkv, D, block_size, rows, max_pages, device="cuda"):
 def _elsewhere(cache, stream):
     """Whether a call has to leave the current device or stream for the
     cache's device and the caller's stream."""
-    return stream is not None or cache.device.index != torch.cuda.current_device()
+    return stream is not None or cache.index != torch._C._cuda_getDevice()
 
 
 def _raw_stream(cache):
     """The current stream of the cache's device (a step of a served batch is
     a few microseconds: the plain handle, without a Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(cache.device.index)
+    return torch._C._cuda_getCurrentRawStream(cache.index)
 
 
 def _there(cache, stream):
@@ -680,12 +683,8 @@ def _there(cache, stream):
     return torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream)
 
 
-def _cu(cache, x, cu_seqlens, max_seqlen):
+def _cu(cache, cu_seqlens, max_seqlen):
     """The longest of the new tokens' runs, the packed offsets checked."""
-    if cu_seqlens is None:
-        _need(x.dim() == 4 and x.shape[0] == cache.struct.rows, "cache: x is [rows, heads, T, D], or packed with cu_seqlens")
-        return None
-    _need(x.dim() == 3, "cache: packed x is [total, heads, D]")
     _int32(cu_seqlens, "cache: cu_seqlens", cache.device, (cache.struct.rows + 1,))
     return int((cu_seqlens[1:] - cu_seqlens[:-1]).max().item()) if max_seqlen is None else int(max_seqlen)
 
@@ -750,13 +749,13 @@ def cache_append(cache, k, v, cu_seqlens=None, max_seqlen=None, stream=None):
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_append(cache, k, v, cu_seqlens, max_seqlen)
-    longest = _cu(cache, k, cu_seqlens, max_seqlen)
-    _need(k.shape == v.shape and k.dtype == v.dtype and k.shape[1] == cache.struct.Hkv and
-          k.device == v.device == cache.device, "cache_append: k and v alike, on the cache's device, with its heads")
+    longest = None if cu_seqlens is None else _cu(cache, cu_seqlens, max_seqlen)
+    _need(k.shape == v.shape and k.dtype == v.dtype and k.device == v.device == cache.device,
+          "cache_append: k and v alike, on the cache's device")
     _same_strides(k, v, "k and v")
     if k.numel() == 0:
         return
-    _, p, _ = cache.problem(k, 1, None, cu_seqlens, longest, False, False)
+    p = cache.problem(k, 1, None, cu_seqlens, longest, False, False)[1]
     _check(lib().nsa_cache_append(p, cache.ref, cu_seqlens.data_ptr() if cu_seqlens is not None else None, k.data_ptr(),
                                   v.data_ptr(), cache.ws.data_ptr(), cache.ws.numel(), _raw_stream(cache)), "nsa_cache_append")
 
@@ -772,27 +771,27 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_fwd(q, cache, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)
-    longest = _cu(cache, q, cu_seqlens, max_seqlen)
-    _need(q.device == cache.device, "cache_fwd: q is on the cache's device")
+    dev = cache.device
+    longest = None if cu_seqlens is None else _cu(cache, cu_seqlens, max_seqlen)
+    _need(q.device == dev, "cache_fwd: q is on the cache's device")
     S = 1
     if block_idx is not None:
         _need(window is None and sinks is None, "cache_fwd: a window or sinks go with the whole cache only")
         S = block_idx.shape[-1]
         head = (q.shape[0], cache.struct.Hkv) + ((q.shape[2],) if cu_seqlens is None else ())
-        _int32(block_idx, "cache_fwd: block_idx", cache.device, head + (S,))
+        _int32(block_idx, "cache_fwd: block_idx", dev, head + (S,))
     if sinks is not None:
         _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and tuple(sinks.shape) == (q.shape[1],) and
-              sinks.device == cache.device, "cache_fwd: sinks are float32 [Hq]")
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+              sinks.device == dev, "cache_fwd: sinks are float32 [Hq]")
     if q.numel() == 0:
-        return o, lse
-    _, p, n = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
+        return torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    _, p, n, stats, dense = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
+    o = torch.empty_like(q) if dense else torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty(stats, dtype=torch.float32, device=dev)
     if ws is None and n > 256:
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-    at, size = (ws.data_ptr(), ws.numel()) if ws is not None else (None, 0)
-    _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), cu_seqlens.data_ptr() if cu_seqlens is not None else None,
-                               block_idx.data_ptr() if block_idx is not None else None,
-                               sinks.data_ptr() if sinks is not None else None, q.data_ptr(), o.data_ptr(),
-                               lse.data_ptr(), at, size, _raw_stream(cache)), "nsa_cache_fwd")
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
+    _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), None if cu_seqlens is None else cu_seqlens.data_ptr(),
+                               None if block_idx is None else block_idx.data_ptr(), None if sinks is None else sinks.data_ptr(),
+                               q.data_ptr(), o.data_ptr(), lse.data_ptr(), at, size, _raw_stream(cache)), "nsa_cache_fwd")
     return o, lse

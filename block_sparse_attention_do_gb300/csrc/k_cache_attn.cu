@@ -1094,13 +1094,14 @@ int ctas_of(const Geo &g, bool sel) { return num_sms() * attn_ctas(row_tile(g, s
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// The clustered form: CTAs of a unit (0: the list's form).  For calls whose
-// units fit the GPU at once, cut as far as CTAs and 128 tokens each go.  The
+// The clustered form: CTAs of a unit (0: the list's form).  One launch and no
+// workspace, for calls whose time is latencies: units are cut as far as the
+// GPU's CTAs and 128 tokens each go, and are whole where there are many.  The
 // cut goes by the table's width, not by lengths, so with several sequences
-// (which may be of any length) it has to be short: 128 KB of codes for a CTA;
+// (which may be of any length) a CTA's share has to be short: 128 KB of codes;
 // one sequence alone 512 KB, or an index's equal rows any.  A token over 8192
 // cached ones (8 kv heads): 14.6 us by the list, of which the join's launch
-// and the list's own reads were 5.
+// and the list's own reads were 5, and 22 us of host time; 13.2 and 15 here.
 int cluster_size(const Geo &g, const Cache &c, bool sel)
 {
     const int nt = row_tile(g, sel), R = nt * 8, slots = num_sms() * attn_ctas(nt);
@@ -1109,7 +1110,7 @@ int cluster_size(const Geo &g, const Cache &c, bool sel)
     int64_t pages = sel ? g.S : c.cols;
     if (g.window > 0)
         pages = min(pages, ((int64_t)g.window + g.T) / c.bs + 2);
-    if (units + 1 > slots || checks > 8192)
+    if (units >= INT32_MAX / 16 || checks > 8192)
         return 0;
     int cs = 1;
     while (cs < 16 && (units + 1) * cs * 2 <= slots && pages * c.bs > (int64_t)cs * 128)

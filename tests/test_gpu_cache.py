@@ -251,9 +251,9 @@ def index_rows(lens, new, Hkv, S, bs, g):
 
 
 def attend_case(lens, new, Hq, Hkv, D, bs, dtype, ragged=False, S=0, window=0, sinks=False, seed=0, layout="dense",
-                cache=None, scale=None, edit=None):
+                cache=None, scale=None, edit=None, cols=None):
     g = np.random.default_rng(seed + 1)
-    cache = cache or filled(lens, Hkv, D, bs, seed, layout=layout)
+    cache = cache or filled(lens, Hkv, D, bs, seed, layout=layout, cols=cols)
     if edit is not None:
         edit(cache)
     total = sum(new)
@@ -583,14 +583,24 @@ def test_chunk_form_leaves_rows_behind_the_last_sequence():
     assert (o[600:] == 7).all() and (lse[600:] == 7).all() and (lse[:600] != 7).all()
 
 
-@pytest.mark.parametrize("kw", MASKS + [dict(S=1), dict(S=5), dict(S=40)])
+@pytest.mark.parametrize("kw", MASKS + [dict(S=27), dict(S=130)])
 @pytest.mark.parametrize("dtype,Hq,Hkv,D,bs,T", [(BF, 8, 2, 128, 64, 1), (F32, 6, 2, 64, 32, 2), (BF, 32, 2, 128, 16, 1),
                                                  (F32, 2, 1, 32, 16, 7), (BF, 20, 1, 64, 64, 1), (F32, 16, 1, 128, 64, 1)])
 def test_list_form(kw, dtype, Hq, Hkv, D, bs, T):
     g = np.random.default_rng(5)
     B = 320 // Hkv
     lens = [int(n) for n in g.integers(0, 300, B)]
-    takes("cache_attn", lens, [T] * B, Hq, Hkv, D, bs, dtype, **kw)
+    cols = None if "S" in kw else 1100 * 128 // (bs * D)  # a table wide enough for long sequences
+    if kw.get("window", 0) or cols is None:
+        attend_case(lens, [T] * B, Hq, Hkv, D, bs, dtype, cols=cols, **kw)
+    else:
+        takes("cache_attn", lens, [T] * B, Hq, Hkv, D, bs, dtype, cols=cols, **kw)
+
+
+@pytest.mark.parametrize("window", [600, 1500])
+def test_list_form_window(window):
+    g = np.random.default_rng(8)
+    takes("cache_attn", [int(n) for n in g.integers(0, 2000, 40)], [2] * 40, 16, 8, 128, 64, BF, window=window)
 
 
 @pytest.mark.parametrize("T", [1, 4])
@@ -601,17 +611,18 @@ def test_list_form_nan_values(T):
             p = int(cache.page_table[b, t // 32])
             cache.v.view(torch.uint8)[p, 1, t % 32, 5] = 0x7f
     g = np.random.default_rng(6)
-    takes("cache_attn", [int(n) for n in g.integers(4, 200, 160)], [T] * 160, 8, 2, 64, 32, BF, edit=edit)
+    takes("cache_attn", [int(n) for n in g.integers(4, 200, 160)], [T] * 160, 8, 2, 64, 32, BF, edit=edit, cols=40)
 
 
 @pytest.mark.parametrize("kw", MASKS + [dict(S=1), dict(S=5), dict(S=40)])
-@pytest.mark.parametrize("B,Hkv", [(1, 1), (2, 2), (5, 4), (12, 8)])
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (2, 2), (5, 4), (12, 8), (50, 8)])
 def test_cluster_form(kw, B, Hkv):
-    """One CTA a unit (12 x 8) up to 16 (one unit alone)."""
+    """One CTA a unit (12 x 8, and 50 x 8 in several rounds) up to 16 (one unit alone)."""
     g = np.random.default_rng(7)
-    lens = [int(n) for n in g.integers(0, 700, B)]
+    lens = [int(n) for n in g.integers(0, 700 if B < 50 else 200, B)]
     for dtype, G, D, bs, T in ((BF, 4, 128, 64, 1), (F32, 3, 64, 16, 4), (BF, 20, 32, 32, 1)):
         T = 1 if "S" in kw else T  # (a unit for each token there)
+        kw = dict(S=15) if B == 50 and kw.get("S") == 40 else kw  # (8192 entries at most)
         takes("cache_attn_cluster", lens, [T] * B, Hkv * G, Hkv, D, bs, dtype, **kw)
 
 
