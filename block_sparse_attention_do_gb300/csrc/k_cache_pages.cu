@@ -4,12 +4,13 @@
 // The pool's whole state is one reference count per page (0: free), the
 // page table and the rows' lengths.  "The lowest free pages first" makes the
 // choice of pages a function of that state alone, whatever order the threads
-// run in.  The metadata of a call is one cluster of 8 CTAs: the counts are
-// read by all 4096 threads at once, the clusters' barriers stand between the
-// steps, and the calls need no host round trip.  What bounds it is the chain
-// of those steps (a few dependent reads each), not the bytes: 0.26 MB of
-// counts for 65,536 pages.  The pages' contents move in a second, wide launch
-// that is bound by memory bandwidth.
+// run in.  The metadata of a call is one cluster of 1 to 8 CTAs, by the size of
+// pool and lists: the counts are read by all its threads at once, barriers
+// stand between the steps, and the calls need no host round trip.  What bounds
+// it is the chain of those steps (a few dependent reads each, about 0.6 us, and
+// as much for a barrier of several CTAs), not the bytes: 0.26 MB of counts for
+// 65,536 pages.  The pages' contents move in a wide launch that is bound by
+// memory bandwidth: 300 pages of 131 KB in 11.6 us, 6.8 TB/s.
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"
@@ -22,17 +23,21 @@ namespace nsa {
 
 namespace {
 
-constexpr int kCluster = 8;      // CTAs of a metadata call (the portable cluster size)
+constexpr int kMaxCluster = 8;  // (the portable size)
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kAllWarps = kCluster * kWarps;
 
 struct Where {
-    int rank, warp, lane;  // CTA of the cluster, warp of the cluster, lane
+    int rank, ctas;        // CTA of the cluster, and their number
+    int warp, warps;       // warp of the cluster, and their number
+    int lane;
+    int thread, threads;   // of the cluster
 };
 __device__ __forceinline__ Where where(const cg::cluster_group &cl)
 {
-    return Where{(int)cl.block_rank(), (int)cl.block_rank() * kWarps + (int)(threadIdx.x >> 5), (int)(threadIdx.x & 31)};
+    const int rank = (int)cl.block_rank(), ctas = (int)cl.num_blocks();
+    return Where{rank, ctas, rank * kWarps + (int)(threadIdx.x >> 5), ctas * kWarps, (int)(threadIdx.x & 31),
+                 rank * kThreads + (int)threadIdx.x, ctas * kThreads};
 }
 
 // blocks that hold len tokens
@@ -43,10 +48,10 @@ __device__ __forceinline__ int blocks_of(int len, const Cache &c) { return (int)
 // calling warp's run and the total.
 struct Runs {
     int begin, end;
-    __device__ __forceinline__ Runs(const Cache &c, int warp)
+    __device__ __forceinline__ Runs(const Cache &c, const Where &w)
     {
-        const int per = ((c.pages + kAllWarps - 1) / kAllWarps + 31) & ~31;
-        begin = min(c.pages, warp * per);
+        const int per = ((c.pages + w.warps - 1) / w.warps + 31) & ~31;
+        begin = (int)min((int64_t)c.pages, (int64_t)w.warp * per);
         end = min(c.pages, begin + per);
     }
     template <typename P> __device__ __forceinline__ int count(int lane, P pred) const
@@ -62,13 +67,13 @@ struct Runs {
 // every warp's count into every CTA's table (the cluster synchronises after)
 __device__ __forceinline__ void share_count(const cg::cluster_group &cl, int *counts, const Where &w, int n)
 {
-    if (w.lane < kCluster)
+    if (w.lane < w.ctas)
         cl.map_shared_rank(counts, w.lane)[w.warp] = n;
 }
 __device__ __forceinline__ void scan_counts(const int *counts, const Where &w, int &before, int &total)
 {
     int b = 0, t = 0;
-    for (int i = w.lane; i < kAllWarps; i += 32) {
+    for (int i = w.lane; i < w.warps; i += 32) {
         t += counts[i];
         b += i < w.warp ? counts[i] : 0;
     }
@@ -135,10 +140,10 @@ __device__ __forceinline__ void take_free(const Cache &c, const Runs &r, int lan
 constexpr int kPiece = 32 * kBatch;
 template <typename F> __device__ __forceinline__ void for_pieces(const Cache &c, const Where &w, int n, F f)
 {
-    const int per = (c.cols + kPiece - 1) / kPiece;
-    for (int64_t x = w.warp; x < (int64_t)n * per; x += kAllWarps) {
-        const int i = per == 1 ? (int)x : (int)(x / per);
-        f(i, (int)(x - (int64_t)i * per) * kPiece);
+    const int per = (c.cols + kPiece - 1) / kPiece;  // (n * per is below rows * columns: an int)
+    for (int x = w.warp; x < n * per; x += w.warps) {
+        const int i = per == 1 ? x : x / per;
+        f(i, (x - i * per) * kPiece);
     }
 }
 // a piece of row r's table entries, lane by lane (-1 past the table's width)
@@ -176,13 +181,13 @@ __device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, i
 }
 
 // ---- reserve: row b grows by n_new[b] tokens; all rows or none ------------
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     cache_reserve_kernel(const Cache c, const int *n_new, const CacheWs ws)
 {
     dependents_may_start();
     dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    __shared__ int counts[kAllWarps];
+    __shared__ int counts[kMaxCluster * kWarps];
     __shared__ int bad;
     __shared__ int64_t need_all;
     const Where w = where(cl);
@@ -201,12 +206,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     for (int b = threadIdx.x; b < c.rows; b += kThreads)
         if (!ok(b))
             bad = 1;
-    const Runs run(c, w.warp);
+    const Runs run(c, w);
     share_count(cl, counts, w, run.count(w.lane, [&](int p) { return c.ref[p] <= 0; }));
     int64_t total;
     if (w.rank == 0) {
         total = cta_prefix(c.rows, ws.r1, need);
-        if (threadIdx.x < kCluster)
+        if (threadIdx.x < w.ctas)
             *cl.map_shared_rank(&need_all, threadIdx.x) = total;
     }
     cl.sync();
@@ -220,7 +225,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         return;  // the same in every CTA: nothing has changed
     take_free(c, run, w.lane, before, (int)total, ws.p2);
     cl.sync();
-    for (int b = w.warp; b < c.rows; b += kAllWarps) {
+    for (int b = w.warp; b < c.rows; b += w.warps) {
         const int len = c.lens[b], n = n_new[b];
         const int have = blocks_of(len, c), want = blocks_of(len + n, c), off = __ldcg(ws.r1 + b);
 #pragma unroll 4
@@ -232,23 +237,44 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     }
 }
 
-// Claims: mark[x] = the first list position that names x.  The caller
-// synchronises between the two steps and before it reads.
-__device__ __forceinline__ void claim_clear(const int *list, int n, int limit, int *mark, const Where &w)
-{
-    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads)
-        if (list[i] >= 0 && list[i] < limit)
-            mark[list[i]] = INT32_MAX;
-}
-__device__ __forceinline__ void claim(const int *list, int n, int limit, int *mark, const Where &w, bool by_source)
-{
-    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads)
-        if (list[i] >= 0 && list[i] < limit)
-            atomicMin(mark + list[i], by_source ? -1 : i);
-}
+// Claims: first(x) = the first position of `list` that names x, -1 where `no`
+// (if given) names it.  Few names are marked in each CTA's shared memory, by
+// every CTA for itself; many in global memory, by the cluster together.
+constexpr int kMarks = 2048;
+struct Claims {
+    int *mark;
+    bool shared;
+    __device__ Claims(const cg::cluster_group &cl, const Where &w, const int *list, const int *no, int n, int names, int *own, int *global)
+        : mark(names <= kMarks ? own : global), shared(names <= kMarks)
+    {
+        const int step = shared ? kThreads : w.threads, first = shared ? (int)threadIdx.x : w.thread;
+        for (int i = first; i < n; i += step) {
+            if (list[i] >= 0 && list[i] < names)
+                mark[list[i]] = INT32_MAX;
+            if (no && no[i] >= 0 && no[i] < names)
+                mark[no[i]] = INT32_MAX;
+        }
+        sync(cl);
+        for (int i = first; i < n; i += step) {
+            if (list[i] >= 0 && list[i] < names)
+                atomicMin(mark + list[i], i);
+            if (no && no[i] >= 0 && no[i] < names)
+                atomicMin(mark + no[i], -1);
+        }
+        sync(cl);
+    }
+    __device__ __forceinline__ void sync(const cg::cluster_group &cl) const
+    {
+        if (shared)
+            __syncthreads();
+        else
+            cl.sync();
+    }
+    __device__ __forceinline__ int first(int x) const { return shared ? mark[x] : __ldcg(mark + x); }
+};
 
 // ---- free: the listed rows give back their pages ---------------------------
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     cache_free_kernel(const Cache c, const int *rows, int n, const CacheWs ws)
 {
     dependents_may_start();
@@ -257,14 +283,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     const Where w = where(cl);
     if (w.rank == 0 && threadIdx.x == 0)
         *ws.err = NSA_OK;
-    claim_clear(rows, n, c.rows, ws.r0, w);
-    cl.sync();
-    claim(rows, n, c.rows, ws.r0, w, false);
-    cl.sync();
+    __shared__ int marks[kMarks];
+    const Claims claims(cl, w, rows, nullptr, n, c.rows, marks, ws.r0);
+    cl.sync();  // (the error word is clear)
     bool bad = false;
     for_pieces(c, w, n, [&](int i, int col0) {
         const int r = rows[i];
-        if (r < 0 || r >= c.rows || __ldcg(ws.r0 + r) != i) {  // no row, or listed before
+        if (r < 0 || r >= c.rows || claims.first(r) != i) {  // no row, or listed before
             bad = true;
             return;
         }
@@ -277,29 +302,26 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 }
 
 // ---- fork: row dst[i] becomes a continuation of row src[i] -----------------
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     cache_fork_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
 {
     dependents_may_start();
     dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    __shared__ int counts[kAllWarps];
+    __shared__ int counts[kMaxCluster * kWarps];
     __shared__ int64_t tails_all;
     const Where w = where(cl);
     if (w.rank == 0 && threadIdx.x == 0) {
         *ws.err = NSA_OK;
         *ws.npairs = 0;
     }
-    claim_clear(src, n, c.rows, ws.r0, w);
-    claim_clear(dst, n, c.rows, ws.r0, w);
-    cl.sync();
-    claim(dst, n, c.rows, ws.r0, w, false);
-    claim(src, n, c.rows, ws.r0, w, true);
-    cl.sync();
+    __shared__ int marks[kMarks];
+    const Claims claims(cl, w, dst, src, n, c.rows, marks, ws.r0);
+    cl.sync();  // (the error word is clear; every CTA runs: its shared memory may be written)
     bool bad = false;
     for_pieces(c, w, n, [&](int i, int col0) {
         const int s = src[i], d = dst[i];
-        if (s < 0 || s >= c.rows || d < 0 || d >= c.rows || __ldcg(ws.r0 + d) != i) {
+        if (s < 0 || s >= c.rows || d < 0 || d >= c.rows || claims.first(d) != i) {
             bad = true;
             return;
         }
@@ -334,11 +356,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     cl.sync();  // every thread has read ws.err: it may be written again
     if (bad)
         set_error(ws.err, NSA_ERR_BAD_INDEX);
-    const Runs run(c, w.warp);
+    const Runs run(c, w);
     share_count(cl, counts, w, run.count(w.lane, [&](int p) { return __ldcg(c.ref + p) <= 0; }));
     if (w.rank == 0) {
         const int64_t t = cta_prefix(n, ws.r1, [&](int i) { return (c.lens[src[i]] & (c.bs - 1)) != 0 ? 1 : 0; });
-        if (threadIdx.x < kCluster)
+        if (threadIdx.x < w.ctas)
             *cl.map_shared_rank(&tails_all, threadIdx.x) = t;
     }
     cl.sync();
@@ -392,7 +414,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 // ---- copy: the pairs that may be copied -------------------------------------
 // A pair with a page outside the pool, a destination that an earlier pair
 // has, or a destination that is any pair's source is left out (-1).
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads)
     cache_copy_check_kernel(const Cache c, const int *src, const int *dst, int n, const CacheWs ws)
 {
     dependents_may_start();
@@ -403,16 +425,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
         *ws.err = NSA_OK;
         *ws.npairs = n;
     }
-    claim_clear(src, n, c.pages, ws.p2, w);
-    claim_clear(dst, n, c.pages, ws.p2, w);
-    cl.sync();
-    claim(dst, n, c.pages, ws.p2, w, false);
-    claim(src, n, c.pages, ws.p2, w, true);
+    __shared__ int marks[kMarks];
+    const Claims claims(cl, w, dst, src, n, c.pages, marks, ws.p2);
     cl.sync();
     bool bad = false;
-    for (int i = w.rank * kThreads + threadIdx.x; i < n; i += kCluster * kThreads) {
+    for (int i = w.thread; i < n; i += w.threads) {
         const int s = src[i], d = dst[i];
-        const bool ok = s >= 0 && s < c.pages && d >= 0 && d < c.pages && __ldcg(ws.p2 + d) == i;
+        const bool ok = s >= 0 && s < c.pages && d >= 0 && d < c.pages && claims.first(d) == i;
         ws.p0[i] = ok ? s : -1;
         ws.p1[i] = ok ? d : -1;
         bad |= !ok;
@@ -424,18 +443,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 // ---- compact: live pages to the front of the pool ---------------------------
 // With n live pages, the live pages at n and above move, in order, to the
 // free pages below n, in order.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cache_compact_kernel(const Cache c, const CacheWs ws)
+__global__ void __launch_bounds__(kThreads) cache_compact_kernel(const Cache c, const CacheWs ws)
 {
     dependents_may_start();
     dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
-    __shared__ int counts[kAllWarps];
+    __shared__ int counts[kMaxCluster * kWarps];
     __shared__ int low;  // live pages below n
     const Where w = where(cl);
     if (w.rank == 0 && threadIdx.x == 0)
         *ws.err = NSA_OK;
     cl.sync();  // every CTA of the cluster runs from here on: its shared memory may be written
-    const Runs run(c, w.warp);
+    const Runs run(c, w);
     share_count(cl, counts, w, run.count(w.lane, [&](int p) { return c.ref[p] > 0; }));
     cl.sync();
     int before, n;
@@ -452,7 +471,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cac
             const int p = p0 + w.lane;
             k += __popc(__ballot_sync(0xffffffffu, p < n && c.ref[p] > 0));
         }
-        if (w.lane < kCluster)
+        if (w.lane < w.ctas)
             *cl.map_shared_rank(&low, w.lane) = k;
     }
     cl.sync();
@@ -480,7 +499,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cac
     cl.sync();
     bool bad = false;
     const int64_t entries = (int64_t)c.rows * c.cols;
-    for (int64_t i = w.rank * kThreads + threadIdx.x; i < entries; i += kCluster * kThreads) {
+    for (int64_t i = w.thread; i < entries; i += w.threads) {
         const int p = c.table[i];
         if (p >= n && p < c.pages) {
             // p's place among the moved pages, if it is one of them (a free
@@ -493,7 +512,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads) cac
         } else if (p < -1 || p >= c.pages)
             bad = true;
     }
-    for (int k = w.rank * kThreads + threadIdx.x; k < moved; k += kCluster * kThreads) {
+    for (int k = w.thread; k < moved; k += w.threads) {
         const int s = __ldcg(ws.p0 + k), d = __ldcg(ws.p1 + k);
         c.ref[d] = c.ref[s];
         c.ref[s] = 0;
@@ -547,32 +566,54 @@ __global__ void __launch_bounds__(kCopyThreads) cache_move_kernel(const Cache c,
     }
 }
 
+// One cluster over `work` counts or entries: a CTA for each 512 of them.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t work, cudaStream_t st, Args... args)
+{
+    int ctas = 1;
+    while (ctas < kMaxCluster && work > 512 * (int64_t)ctas)
+        ctas *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, KArgs(args)...);
+}
+
 }  // namespace
 
 cudaError_t launch_cache_reserve(const Cache &c, const int *n_new, const CacheWs &ws, cudaStream_t st)
 {
-    return launch_dependent(cache_reserve_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, n_new, ws);
+    return launch_cluster(cache_reserve_kernel, c.pages, st, c, n_new, ws);
 }
 
 cudaError_t launch_cache_free(const Cache &c, const int *rows, int n, const CacheWs &ws, cudaStream_t st)
 {
-    return launch_dependent(cache_free_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, rows, n, ws);
+    return launch_cluster(cache_free_kernel, (int64_t)n * c.cols, st, c, rows, n, ws);
 }
 
 cudaError_t launch_cache_fork(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws, cudaStream_t st)
 {
-    return launch_dependent(cache_fork_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, src, dst, n, ws);
+    return launch_cluster(cache_fork_kernel, max((int64_t)c.pages, (int64_t)n * c.cols), st, c, src, dst, n, ws);
 }
 
 cudaError_t launch_cache_copy_check(const Cache &c, const int *src, const int *dst, int n, const CacheWs &ws,
                                     cudaStream_t st)
 {
-    return launch_dependent(cache_copy_check_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, src, dst, n, ws);
+    return launch_cluster(cache_copy_check_kernel, n, st, c, src, dst, n, ws);
 }
 
 cudaError_t launch_cache_compact(const Cache &c, const CacheWs &ws, cudaStream_t st)
 {
-    return launch_dependent(cache_compact_kernel, dim3(kCluster), dim3(kThreads), 0, st, c, ws);
+    return launch_cluster(cache_compact_kernel, max((int64_t)c.pages, (int64_t)c.rows * c.cols), st, c, ws);
 }
 
 cudaError_t launch_cache_move(const Cache &c, const CacheWs &ws, int max_pairs, cudaStream_t st)
