@@ -112,7 +112,7 @@ template <typename F> __device__ int64_t cta_prefix(int n, int *out, F need)
     return base;
 }
 
-constexpr int kBatch = 8;  // reads of a thread under way together
+constexpr int kBatch = 4;  // reads of a thread under way together
 
 // Takes the `total` lowest free pages: order[i] = the i-th, its count 1.
 __device__ __forceinline__ void take_free(const Cache &c, const Runs &r, int lane, int before, int total, int *order)
