@@ -254,6 +254,7 @@ template <int D, int NT, bool SPLIT> struct Smem {
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
     float2 ml[kWarps][R];       // each warp's maximum and sum
     float2 cta_ml[R];           // the CTA's, for its cluster
+    uint32_t nan[kWarps][R * D / 32];  // each warp's outputs that a NaN value reaches
     union {
         float o[kWarps][R][D + 4];                     // its part of O
         uint8_t ring[kWarps][attn_stages(NT)][32 * D];  // its steps under way: 16 tokens' keys, then values
@@ -262,7 +263,7 @@ template <int D, int NT, bool SPLIT> struct Smem {
 
 // Every length, index entry and page of a call, checked by one block, which
 // alone writes the error word (the clustered form's calls are small).
-__device__ void attn_check(const AttnArgs &a)
+__device__ __noinline__ void attn_check(const AttnArgs &a)
 {
     const Geo &g = a.g;
     const Cache &c = a.c;
@@ -510,6 +511,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         // ---- queries into fragments: element (k, n) of B is row n's element
         // k, in the order of the head dimension that the K loads give
         __syncthreads();  // the previous unit is done with shared memory
+        for (int i = lane; i < R * D / 32; i += 32)
+            sm.nan[warp][i] = 0;
+        bool nan_seen = false;
 #pragma unroll
         for (int i = 0; i < QR; ++i) {
             const int r = warp + i * kWarps;
@@ -730,71 +734,68 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                         }
                     }
                 }
+                auto load_v = [&]() {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    load_shared<VB>(at + (from_v ^ (i & 1) * D) + (i >> 1) * 8 * D, vw[i]);
-                // ---- values that a row does not attend must not reach it, whatever they hold
-                bool nan = false;
-                if (part) {
+                    for (int i = 0; i < 4; ++i)
+                        load_shared<VB>(at + (from_v ^ (i & 1) * D) + (i >> 1) * 8 * D, vw[i]);
+                    if (part)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int kk = key_now + tq * 2 + (i & 1) + (i >> 1) * 8;
-                        const bool out = kk > pmax || (g.window > 0 && kk <= pmin - g.window);
+                        for (int i = 0; i < 4; ++i) {
+                            const int kk = key_now + tq * 2 + (i & 1) + (i >> 1) * 8;
+                            const bool out = kk > pmax || (g.window > 0 && kk <= pmin - g.window);
 #pragma unroll
-                        for (int w = 0; w < VW; ++w) {
-                            if (out)
-                                vw[i][w] = 0u;
-                            const uint32_t x = vw[i][w] & 0x7f7f7f7fu;
-                            nan |= ((x + 0x01010101u) & 0x80808080u) != 0;
+                            for (int w = 0; w < VW; ++w)
+                                vw[i][w] = out ? 0u : vw[i][w];
                         }
+                };
+                load_v();
+                // ---- values that a row does not attend must not reach it,
+                // whatever they hold (0 * NaN would): tokens that no row
+                // attends are taken as zeros, and so is every NaN, which its
+                // rows get back when the warps' sums are joined
+                if (part) {
+                    bool nan = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int w = 0; w < VW; ++w)
+                            nan |= (((vw[i][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+                    if (__any_sync(0xffffffffu, nan)) {
+                        const uint8_t *vs = sm.ring[warp][stage == 0 ? kStages - 1 : stage - 1] + 16 * D;
+#pragma unroll 1
+                        for (int x = lane; x < 16 * D; x += 32) {
+                            const int tok = x / D, d = x % D, kk = key_now + tok;
+                            uint8_t *code = (uint8_t *)vs + v_at<D>(tok, d / 16) * 16 + d % 16;
+                            if ((*code & 0x7f) != 0x7f)
+                                continue;
+                            *code = 0;
+#pragma unroll 1
+                            for (int r = 0; r < u.nrows; ++r) {
+                                const int p = sm.pos[r];
+                                if (kk <= p && !(g.window > 0 && kk <= p - g.window))
+                                    atomicOr(&sm.nan[warp][r * (D / 32) + d / 32], 1u << (d % 32));
+                            }
+                        }
+                        nan_seen = true;
+                        __syncwarp();
+                        load_v();
                     }
                 }
                 // ---- O^T += V^T P^T
-                if (!(part && __any_sync(0xffffffffu, nan))) {
 #pragma unroll
-                    for (int w = 0; w < VW; ++w)
+                for (int w = 0; w < VW; ++w)
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            uint32_t af[4];
-                            e4m3x4_to_half(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), af[0], af[1]);
-                            e4m3x4_to_half(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), af[2], af[3]);
+                    for (int hf = 0; hf < 2; ++hf) {
+                        uint32_t af[4];
+                        e4m3x4_to_half(__byte_perm(vw[0][w], vw[1][w], hf ? 0x7362 : 0x5140), af[0], af[1]);
+                        e4m3x4_to_half(__byte_perm(vw[2][w], vw[3][w], hf ? 0x7362 : 0x5140), af[2], af[3]);
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                mma_f16(o[n][w * 2 + hf], af, pb[0][n][0], pb[0][n][1]);
-                                if constexpr (SPLIT)
-                                    mma_f16(o[n][w * 2 + hf], af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
-                            }
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16(o[n][w * 2 + hf], af, pb[0][n][0], pb[0][n][1]);
+                            if constexpr (SPLIT)
+                                mma_f16(o[n][w * 2 + hf], af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
                         }
-                } else {
-                    // a NaN among the values: token by token, and the rows
-                    // that do not attend the token keep their sums (0 * NaN
-                    // would reach them)
-#pragma unroll 1
-                    for (int tok = 0; tok < 16; ++tok) {
-                        const int mine = tok - tq * 2;  // 0, 1, 8, 9: token `tok` is this thread's i = 0, 1, 2, 3
-#pragma unroll
-                        for (int w = 0; w < VW; ++w)
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                uint32_t af[4];
-                                e4m3x4_to_half(__byte_perm(mine == 0 ? vw[0][w] : 0u, mine == 1 ? vw[1][w] : 0u, hf ? 0x7362 : 0x5140), af[0], af[1]);
-                                e4m3x4_to_half(__byte_perm(mine == 8 ? vw[2][w] : 0u, mine == 9 ? vw[3][w] : 0u, hf ? 0x7362 : 0x5140), af[2], af[3]);
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma_f16(d, af, pb[0][n][0], pb[0][n][1]);
-                                    if constexpr (SPLIT)
-                                        mma_f16(d, af, pb[SPLIT ? 1 : 0][n][0], pb[SPLIT ? 1 : 0][n][1]);
-#pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const int p = sm.pos[n * 8 + tq * 2 + (i & 1)], kk = key_now + tok;
-                                        if (kk <= p && !(g.window > 0 && kk <= p - g.window))
-                                            o[n][w * 2 + hf][i] += d[i];
-                                    }
-                                }
-                            }
                     }
-                }
             }
             tc::cp_async_wait<0>();
         }
@@ -818,6 +819,12 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                         *(float4 *)&sm.o[warp][r][gq * VB + 2 * j] = make_float4(o[n][j][i], o[n][j][i + 2], o[n][j + 1][i], o[n][j + 1][i + 2]);
                 }
             }
+        if (nan_seen) {  // (warp-uniform)
+            __syncwarp();
+            for (int x = lane; x < u.nrows * D; x += 32)
+                if (sm.nan[warp][x / 32] >> (x % 32) & 1u)
+                    sm.o[warp][x / D][x % D] = __int_as_float(0x7fffffff);
+        }
         __syncthreads();
         const bool whole = CLUSTER ? a.cs == 1 : at == u.begin && seg1 == u.begin + u.count;
         // a part: the first of the run in slot 0, its last in slot 1 (a run
@@ -1116,7 +1123,7 @@ int cluster_size(const Geo &g, const Cache &c, bool sel)
     while (cs < 16 && (units + 1) * cs * 2 <= slots && pages * c.bs > (int64_t)cs * 128)
         cs *= 2;
     const int64_t bytes = (pages + cs - 1) / cs * c.bs * 2 * g.D;
-    return sel || bytes <= (g.B == 1 ? 512 << 10 : 128 << 10) ? cs : 0;
+    return sel || bytes <= (g.B == 1 || g.window > 0 ? 640 << 10 : 128 << 10) ? cs : 0;
 }
 
 // shared memory above the default, and clusters of 16, allowed once per device

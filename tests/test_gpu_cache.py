@@ -597,10 +597,9 @@ def test_list_form(kw, dtype, Hq, Hkv, D, bs, T):
         takes("cache_attn", lens, [T] * B, Hq, Hkv, D, bs, dtype, cols=cols, **kw)
 
 
-@pytest.mark.parametrize("window", [600, 1500])
-def test_list_form_window(window):
+def test_list_form_window():
     g = np.random.default_rng(8)
-    takes("cache_attn", [int(n) for n in g.integers(0, 2000, 40)], [2] * 40, 16, 8, 128, 64, BF, window=window)
+    takes("cache_attn", [int(n) for n in g.integers(0, 5000, 40)], [2] * 40, 16, 8, 128, 64, BF, window=3500)
 
 
 @pytest.mark.parametrize("T", [1, 4])
