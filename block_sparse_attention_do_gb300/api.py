@@ -591,7 +591,8 @@ class KVCache:
     contiguous), k_scale, v_scale float32 [num_pages, Hkv], page_table int32
     [rows, max_pages], seq_lens int32 [rows], refcount int32 [num_pages]
     (None: the caller manages pages itself; no reserve, free, fork or
-    compact).  `ws` is the workspace of the calls that change the cache;
+    compact).  The cache keeps their addresses: they are written in place,
+    never replaced.  `ws` is the workspace of the calls that change the cache;
     get_error(cache.ws) reads what the last of them found."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table, seq_lens, refcount=None):
@@ -680,6 +681,8 @@ def _raw_stream(cache):
 def _there(cache, stream):
     """The caller's stream (else the device's current one) as the context of
     a call, so that what it allocates belongs to that stream."""
+    _need(cache.device.type == "cuda" and (stream is None or stream.device == cache.device),
+          "cache: a CUDA device's cache, and a stream of that device")
     return torch.cuda.stream(torch.cuda.current_stream(cache.device) if stream is None else stream)
 
 
@@ -785,6 +788,7 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
               sinks.device == dev, "cache_fwd: sinks are float32 [Hq]")
     if q.numel() == 0:
         return torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
+    _need(ws is None or ws.device == dev, "cache_fwd: ws is on the cache's device")
     _, p, n, stats, dense = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
     o = torch.empty_like(q) if dense else torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(stats, dtype=torch.float32, device=dev)

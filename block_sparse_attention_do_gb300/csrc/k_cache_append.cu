@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
 template <typename T> cudaError_t append_t(const Geo &g, const Cache &c, const void *k, const void *v, int *err, cudaStream_t st)
 {
     constexpr int N = Vec16<T>::N;
-    const int per_row = (g.T + c.bs - 2) / c.bs + 1;
+    const int longest = g.thd ? min(g.T, max(g.ntok, 1)) : g.T, per_row = (longest + c.bs - 2) / c.bs + 1;
     // few new tokens per row: a warp per head, its values in 4 (fp32: 8)
     // vectors per thread; else a block per head
     constexpr int FEW = sizeof(T) == 2 ? 4 : 8;
-    const int vecs = min(g.T, c.bs) * c.D / N;
+    const int vecs = min(longest, c.bs) * c.D / N;
     const bool few = vecs <= 32 * FEW;
     const dim3 grid((unsigned)((int64_t)c.rows * per_row + 1), (unsigned)(few ? (2 * c.Hkv + kCta / 32 - 1) / (kCta / 32) : 2 * c.Hkv));
     const T *kn = (const T *)k, *vn = (const T *)v;

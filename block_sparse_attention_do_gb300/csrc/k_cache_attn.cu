@@ -1112,12 +1112,13 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 int cluster_size(const Geo &g, const Cache &c, bool sel)
 {
     const int nt = row_tile(g, sel), R = nt * 8, slots = num_sms() * attn_ctas(nt);
-    const int64_t units = sel ? (int64_t)g.ntok * g.Hkv * ((g.G + R - 1) / R) : (int64_t)g.B * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
+    const int64_t rows = (int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G;  // of the longest sequence, at most
+    const int64_t units = sel ? (int64_t)g.ntok * g.Hkv * ((g.G + R - 1) / R) : (int64_t)g.B * g.Hkv * ((rows + R - 1) / R);
     const int64_t checks = sel ? (int64_t)g.ntok * g.Hkv * g.S : (int64_t)g.B * c.cols;
     int64_t pages = sel ? g.S : c.cols;
     if (g.window > 0)
         pages = min(pages, ((int64_t)g.window + g.T) / c.bs + 2);
-    if (units >= INT32_MAX / 16 || checks > 8192)
+    if (units > 8192 || checks > 8192)
         return 0;
     int cs = 1;
     while (cs < 16 && (units + 1) * cs * 2 <= slots && pages * c.bs > (int64_t)cs * 128)
@@ -1244,7 +1245,7 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     a.err = (int *)ws;
     if (a.cs > 0) {
         if (!sel)
-            a.row_tiles = (int)(((int64_t)g.T * g.G + nt * 8 - 1) / (nt * 8));
+            a.row_tiles = (int)(((int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G + nt * 8 - 1) / (nt * 8));
         a.units = (sel ? g.ntok : g.B) * g.Hkv * a.row_tiles;
     }
     // a run is cut at multiples of 128 tokens, a step of the CTA's warps; of

@@ -1184,6 +1184,12 @@ nsa_status cache_geo(const nsa_problem *p, const nsa_cache *pc, const int32_t *c
         return NSA_ERR_INVALID_ARG;
     if (p->B != pc->rows || p->Hkv != pc->Hkv || p->D != pc->D || p->block_size != pc->block_size)
         return NSA_ERR_INVALID_ARG;
+    // positions reach from -T to the table's last key, and their differences
+    // from a window are ints too: a window that covers every key is none
+    if ((int64_t)c.cols * c.bs + p->T + 64 >= INT32_MAX)
+        return NSA_ERR_UNSUPPORTED;
+    if (g.window >= c.cols * c.bs)
+        g.window = 0;
     return NSA_OK;
 }
 
@@ -1340,6 +1346,11 @@ nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t wind
     if ((ws || need > kAlign) && (s = check_ws(ws, ws_bytes, need)) != NSA_OK)
         return s;
     cudaStream_t st = (cudaStream_t)stream;
+    if (g.ntok == 0) {
+        if (ws)
+            NSA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));
+        return NSA_OK;
+    }
     if (chunk) {
         if (ws)
             NSA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));

@@ -456,6 +456,62 @@ def test_bad_index_entries_and_lengths_are_reported():
     assert with_errors(q, cache)[1] == api.NSA_OK
 
 
+def test_a_window_beyond_every_key_is_none():
+    cache = filled([300, 64], 2, 64, 32, 2)
+    for T in (1, 40):
+        q = torch.randn(2, 8, T, 64, device=DEV).to(BF)
+        want = api.cache_fwd(q, cache)
+        for window in (320, 5000, 2 ** 31 - 1):
+            assert all(torch.equal(a, b) for a, b in zip(want, api.cache_fwd(q, cache, window=window)))
+
+
+def test_loose_bounds_and_empty_calls():
+    """max_seqlen far above the longest run; no token at all."""
+    cache = filled([300, 64, 9], 2, 64, 32, 2)
+    cu = torch.tensor([0, 3, 3, 5], dtype=torch.int32, device=DEV)
+    q = torch.randn(5, 8, 64, device=DEV).to(BF)
+    want = api.cache_fwd(q, cache, cu_seqlens=cu, max_seqlen=3)
+    for bound in (4, 1000, 1 << 20):
+        o, lse = api.cache_fwd(q, cache, cu_seqlens=cu, max_seqlen=bound)
+        assert (o.float() - want[0].float()).abs().max() <= 2 ** -7 * want[0].float().abs().max() and (lse - want[1]).abs().max() < 1e-4
+    none = torch.zeros(4, dtype=torch.int32, device=DEV)
+    o, lse = api.cache_fwd(q[:0], cache, cu_seqlens=none, max_seqlen=1)
+    assert o.shape == (0, 8, 64) and lse.shape == (0, 8)
+    before = cache.k.view(torch.uint8).clone()
+    api.cache_append(cache, q[:0, :2], q[:0, :2], cu_seqlens=none, max_seqlen=1)
+    x = torch.randn(5, 2, 64, device=DEV).to(BF)
+    api.cache_append(cache, x, x, cu_seqlens=none, max_seqlen=7)  # rows that belong to no sequence
+    assert api.get_error(cache.ws) == 0 and torch.equal(before, cache.k.view(torch.uint8))
+    p = api.problem(3, 8, 2, 1, 64, 32, 1, BF, layout=api.LAYOUT_THD, total_tokens=0)
+    ws = torch.full((1 << 22,), 0xff, dtype=torch.uint8, device=DEV)
+    for idx in (None, cu.data_ptr()):
+        assert api.lib().nsa_cache_fwd(p, cache.ref, 0, none.data_ptr(), idx, None, q.data_ptr(), o.data_ptr() or q.data_ptr(),
+                                       lse.data_ptr() or q.data_ptr(), ws.data_ptr(), ws.numel(), api._stream()) == 0
+        assert api.get_error(ws) == 0
+
+
+def test_packed_offsets_that_are_none_are_reported():
+    """Runs longer than the bound, backward, or past the tensor: their rows are neither read nor written."""
+    cache = filled([300, 64], 2, 64, 32, 2)
+    q = torch.randn(6, 8, 64, device=DEV).to(BF)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device=DEV)
+    for offsets, bound in (([0, 4, 6], 3), ([0, 5, 3], 6), ([0, 2, 60], 60), ([-3, 2, 6], 6)):
+        cu = torch.tensor(offsets, dtype=torch.int32, device=DEV)
+        api.cache_fwd(q, cache, cu_seqlens=cu, max_seqlen=bound, ws=ws)
+        assert api.get_error(ws) == 3, offsets
+        before = cache.k.view(torch.uint8).clone()
+        bad = 0 if offsets[1] - offsets[0] > bound or offsets[0] < 0 else 1
+        api.cache_append(cache, q[:, :2].contiguous(), q[:, :2].contiguous(), cu_seqlens=cu, max_seqlen=bound)
+        assert api.get_error(cache.ws) == 3, offsets
+        held = cache.page_table[bad]
+        assert torch.equal(before[held[held >= 0].long()], cache.k.view(torch.uint8)[held[held >= 0].long()])
+    long = torch.tensor([0, 500, 400], dtype=torch.int32, device=DEV)  # a chunk's
+    many = torch.randn(600, 16, 64, device=DEV).to(BF)
+    wide = filled([500, 600], 8, 64, 32, 2)
+    assert form_of(lambda: api.cache_fwd(many, wide, cu_seqlens=long, max_seqlen=500, ws=ws)) == "cache_chunk"
+    assert api.get_error(ws) == 3
+
+
 def test_calls_on_two_streams_and_in_graphs():
     cache = filled([3000, 100, 0, 64], 2, 128, 64, 4)
     qs = [torch.randn(4, 8, T, 128, device=DEV).to(BF) for T in (1, 1, 3, 50)]
