@@ -621,7 +621,7 @@ class KVCache:
         n = int(lib().nsa_cache_workspace_size(self.ref))
         if n == 0:
             raise NsaError(1, "nsa_cache_workspace_size")
-        self.ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
         self._problems = {}
 
     def problem(self, x, S, scale, cu_seqlens, max_seqlen, selection, query):
@@ -757,6 +757,7 @@ def cache_append(cache, k, v, cu_seqlens=None, max_seqlen=None, stream=None):
           "cache_append: k and v alike, on the cache's device")
     _same_strides(k, v, "k and v")
     if k.numel() == 0:
+        cache.ws[:4].zero_()  # nothing to do, nothing found
         return
     p = cache.problem(k, 1, None, cu_seqlens, longest, False, False)[1]
     _check(lib().nsa_cache_append(p, cache.ref, cu_seqlens.data_ptr() if cu_seqlens is not None else None, k.data_ptr(),
@@ -776,7 +777,8 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
             return cache_fwd(q, cache, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)
     dev = cache.device
     longest = None if cu_seqlens is None else _cu(cache, cu_seqlens, max_seqlen)
-    _need(q.device == dev, "cache_fwd: q is on the cache's device")
+    _need(q.device == dev and (ws is None or ws.device == dev), "cache_fwd: q and ws are on the cache's device")
+    _need(q.dim() == (4 if cu_seqlens is None else 3), "cache_fwd: q is [rows, Hq, T, D], or packed [total, Hq, D] with cu_seqlens")
     S = 1
     if block_idx is not None:
         _need(window is None and sinks is None, "cache_fwd: a window or sinks go with the whole cache only")
@@ -787,8 +789,9 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
         _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and tuple(sinks.shape) == (q.shape[1],) and
               sinks.device == dev, "cache_fwd: sinks are float32 [Hq]")
     if q.numel() == 0:
+        if ws is not None:
+            ws[:4].zero_()
         return torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)
-    _need(ws is None or ws.device == dev, "cache_fwd: ws is on the cache's device")
     _, p, n, stats, dense = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True)
     o = torch.empty_like(q) if dense else torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(stats, dtype=torch.float32, device=dev)

@@ -31,6 +31,11 @@ struct CacheWs {
     int *r0, *r1;
 };
 
+// New tokens and query rows of a kv head of the longest sequence, as far as
+// the host knows: the caller's bound may be far above the packed tokens.
+inline int longest_tokens(const Geo &g) { return g.thd ? min(g.T, max(g.ntok, 1)) : g.T; }
+inline int64_t longest_rows(const Geo &g) { return (int64_t)longest_tokens(g) * g.G; }
+
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
 

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
 template <typename T> cudaError_t append_t(const Geo &g, const Cache &c, const void *k, const void *v, int *err, cudaStream_t st)
 {
     constexpr int N = Vec16<T>::N;
-    const int longest = g.thd ? min(g.T, max(g.ntok, 1)) : g.T, per_row = (longest + c.bs - 2) / c.bs + 1;
+    const int longest = longest_tokens(g), per_row = (longest + c.bs - 2) / c.bs + 1;
     // few new tokens per row: a warp per head, its values in 4 (fp32: 8)
     // vectors per thread; else a block per head
     constexpr int FEW = sizeof(T) == 2 ? 4 : 8;

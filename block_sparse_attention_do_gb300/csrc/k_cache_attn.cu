@@ -1106,14 +1106,14 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // GPU's CTAs and 128 tokens each go, and are whole where there are many.  The
 // cut goes by the table's width, not by lengths, so with several sequences
 // (which may be of any length) a CTA's share has to be short: 128 KB of codes;
-// one sequence alone 512 KB, or an index's equal rows any.  A token over 8192
+// one sequence alone, or keys that a window bounds, 640 KB; an index's equal
+// rows any.  A token over 8192
 // cached ones (8 kv heads): 14.6 us by the list, of which the join's launch
 // and the list's own reads were 5, and 22 us of host time; 13.2 and 15 here.
 int cluster_size(const Geo &g, const Cache &c, bool sel)
 {
     const int nt = row_tile(g, sel), R = nt * 8, slots = num_sms() * attn_ctas(nt);
-    const int64_t rows = (int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G;  // of the longest sequence, at most
-    const int64_t units = sel ? (int64_t)g.ntok * g.Hkv * ((g.G + R - 1) / R) : (int64_t)g.B * g.Hkv * ((rows + R - 1) / R);
+    const int64_t units = sel ? (int64_t)g.ntok * g.Hkv * ((g.G + R - 1) / R) : (int64_t)g.B * g.Hkv * ((longest_rows(g) + R - 1) / R);
     const int64_t checks = sel ? (int64_t)g.ntok * g.Hkv * g.S : (int64_t)g.B * c.cols;
     int64_t pages = sel ? g.S : c.cols;
     if (g.window > 0)
@@ -1220,7 +1220,7 @@ int64_t cache_attn_entries(const Geo &g, const Cache &c, bool sel)
 {
     const int R = row_tile(g, sel) * 8;
     return sel ? (int64_t)g.ntok * g.Hkv * g.S * ((g.G + R - 1) / R)
-               : (int64_t)g.B * (c.cols + start_cost(g)) * g.Hkv * (((int64_t)g.T * g.G + R - 1) / R);
+               : (int64_t)g.B * (c.cols + start_cost(g)) * g.Hkv * ((longest_rows(g) + R - 1) / R);
 }
 
 size_t cache_attn_ws_bytes(const Geo &g, const Cache &c, bool sel) { return cluster_size(g, c, sel) > 0 ? 256 : attn_layout(g, sel).total; }
@@ -1245,7 +1245,7 @@ cudaError_t launch_cache_attn(const Geo &g, const Cache &c, const void *q, const
     a.err = (int *)ws;
     if (a.cs > 0) {
         if (!sel)
-            a.row_tiles = (int)(((int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G + nt * 8 - 1) / (nt * 8));
+            a.row_tiles = (int)((longest_rows(g) + nt * 8 - 1) / (nt * 8));
         a.units = (sel ? g.ntok : g.B) * g.Hkv * a.row_tiles;
     }
     // a run is cut at multiples of 128 tokens, a step of the CTA's warps; of

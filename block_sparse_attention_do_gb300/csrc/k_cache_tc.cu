@@ -572,9 +572,6 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
 
 }  // namespace
 
-// Rows of the longest sequence, as far as the host knows.
-static int64_t longest_rows(const Geo &g) { return (int64_t)(g.thd ? min(g.T, g.ntok) : g.T) * g.G; }
-
 // Where this kernel takes over from the list's (k_cache_attn.cu), whose time
 // goes by 32-row tiles, all SMs together, while a CTA here takes 256 rows by
 // itself.  Measured over 4096 cached tokens, 8 kv heads of 4 query heads: 16

@@ -482,6 +482,10 @@ def test_loose_bounds_and_empty_calls():
     x = torch.randn(5, 2, 64, device=DEV).to(BF)
     api.cache_append(cache, x, x, cu_seqlens=none, max_seqlen=7)  # rows that belong to no sequence
     assert api.get_error(cache.ws) == 0 and torch.equal(before, cache.k.view(torch.uint8))
+    free = torch.tensor([9], dtype=torch.int32, device=DEV)
+    api.cache_free(cache, free)  # no such row; then a call that finds nothing
+    api.cache_append(cache, q[:0, :2], q[:0, :2], cu_seqlens=none, max_seqlen=1)
+    assert api.get_error(cache.ws) == 0
     p = api.problem(3, 8, 2, 1, 64, 32, 1, BF, layout=api.LAYOUT_THD, total_tokens=0)
     ws = torch.full((1 << 22,), 0xff, dtype=torch.uint8, device=DEV)
     for idx in (None, cu.data_ptr()):
