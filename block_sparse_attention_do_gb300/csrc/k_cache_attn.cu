@@ -9,11 +9,15 @@
 // codes and a page of small values costs no range.
 //
 // What bounds it: the cache's bytes, 2 D per key and kv head, each read once;
-// 4 G D operations on them are far below the tensor cores' rate (G = 4: 4
+// 4 G D operations on them are far below the tensor cores' rate (G = 4: 8
 // operations a byte).  So the layout is made for the loads: every warp keeps
 // its next steps of 16 tokens under way into a ring of its own in shared
-// memory, and no warp waits for another before the end.  The products are taken transposed, tokens (then head
-// dimensions) as the 16 rows of mma.m16n8k16 and query rows as its 8 columns:
+// memory, and no warp waits for another before the end.  Measured, D = 128, 8
+// kv heads of 4 query heads: 32 sequences of 128 .. 32768 tokens, 1.08 GB of
+// codes, 182 us, 5.9 TB/s (88% of a plain copy's rate); one sequence of 8192,
+// 17 MB, 13 us, of which 4 are any launch's.  The products are taken
+// transposed, tokens (then head dimensions) as the 16 rows of mma.m16n8k16
+// and query rows as its 8 columns:
 //   S^T[token, row] = K q^T     A: a thread's 16 code bytes of one token are
 //       the pairs of four k-steps, in an order of the head dimension that q's
 //       fragments share;
@@ -1106,9 +1110,11 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // GPU's CTAs and 128 tokens each go, and are whole where there are many.  The
 // cut goes by the table's width, not by lengths, so with several sequences
 // (which may be of any length) a CTA's share has to be short: 128 KB of codes;
-// one sequence alone, or keys that a window bounds, 640 KB; an index's equal
-// rows any.  A token over 8192
-// cached ones (8 kv heads): 14.6 us by the list, of which the join's launch
+// one sequence alone, or keys that a window bounds, 640 KB (16 sequences of 5
+// tokens behind a window of 4096: 40 us by the list, 35 here); an index's equal
+// rows any.  Units cut finer than one round of CTAs cost more (the same call in
+// two rounds 42 us, 128 index rows of 16 blocks 31 us for 21).  A token over
+// 8192 cached ones (8 kv heads): 14.6 us by the list, of which the join's launch
 // and the list's own reads were 5, and 22 us of host time; 13.2 and 15 here.
 int cluster_size(const Geo &g, const Cache &c, bool sel)
 {

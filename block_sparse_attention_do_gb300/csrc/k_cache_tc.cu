@@ -11,13 +11,22 @@
 //                       stored) to halves in shared memory, 128 keys x D,
 //                       128-byte swizzled
 //   2 issuing warps     S_q = Q_q K^T and O_q += P_q V for the tile q = 0, 1
-//                       of 128 rows: one tile's softmax runs under the
-//                       other's products
+//                       of 128 rows, in turns: one tile's softmax runs under
+//                       the other's products
 //   2 x 4 softmax warps a row per thread: maximum, exponentials, P as halves
 //                       over S's own columns of tensor memory
 // Halves hold e4m3 exactly, bf16 queries scaled by a power of two per row
 // exactly (but for elements 2^-29 below the row's largest), and P with 11
 // bits, three more than bf16.  Tensor memory is full: S 2 x 128 columns, O 2 x D.
+//
+// Measured: chunks of up to 2048 tokens of 6 sequences over 2048 .. 8192 keys
+// (32 query heads on 8, D = 128; 395 GFLOP, masked keys not counted) 341 us,
+// 1.16 PFLOP/s, 60% of the measured bf16 rate.  A tile of 128 keys takes 1.65
+// us, where its products take 1.0 and its softmax (256 x 128 exponentials, with
+// a maximum, a scaling, a sum and a rounding of each) about as long beside
+// them; beginning and ending a unit of 256 rows costs some 10 us.  CTAs that
+// keep their tensor memory and take several units in turn did not lower that,
+// and their inner loop no longer fitted its registers (1.75 us a tile).
 #include <math.h>
 
 #include "cache_common.cuh"
