@@ -10,7 +10,7 @@
 // written once; a page's earlier codes are touched only when its scale grew.
 //
 // What bounds it: prompts, the bytes (keys and values, 2 in and 1 out each:
-// 172 MB of 8 prompts of up to 8192 tokens in 32 us, 5.3 TB/s); single tokens,
+// 172 MB of 8 prompts of up to 8192 tokens in 31 us, 5.5 TB/s); single tokens,
 // the launch (64 rows: 5.5 us, of which 4 are any launch's).
 #include <math.h>
 
@@ -24,10 +24,31 @@ namespace {
 
 constexpr int kCta = 128;
 
-// a 16-byte vector of the element type as floats
+// A 16-byte vector of the element type: as floats; as floats times a power of
+// two (exact: bf16 has float's exponents, and what falls below its normal range
+// is far below the least code); and the running maximum of its magnitudes,
+// which order as their bits do.
 template <typename T> struct Vec16;
 template <> struct Vec16<__nv_bfloat16> {
     static constexpr int N = 8;
+    static __device__ __forceinline__ void scaled(const uint4 &w, float by, float (&x)[8])
+    {
+        const __nv_bfloat162 f = __float2bfloat162_rn(by);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        uint32_t y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 p = __hmul2(*(const __nv_bfloat162 *)&u[i], f);
+            y[i] = *(const uint32_t *)&p;
+        }
+        get(make_uint4(y[0], y[1], y[2], y[3]), x);
+    }
+    static __device__ __forceinline__ uint32_t top(uint32_t t, const uint4 &w)
+    {
+        t = __vmaxu2(__vmaxu2(t, w.x & 0x7fff7fffu), w.y & 0x7fff7fffu);
+        return __vmaxu2(__vmaxu2(t, w.z & 0x7fff7fffu), w.w & 0x7fff7fffu);
+    }
+    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return max(t << 16, t & 0xffff0000u); }  // a float's
     static __device__ __forceinline__ void get(const uint4 &w, float (&x)[8])
     {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -40,6 +61,18 @@ template <> struct Vec16<__nv_bfloat16> {
 };
 template <> struct Vec16<float> {
     static constexpr int N = 4;
+    static __device__ __forceinline__ void scaled(const uint4 &w, float by, float (&x)[4])
+    {
+        get(w, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] *= by;
+    }
+    static __device__ __forceinline__ uint32_t top(uint32_t t, const uint4 &w)
+    {
+        return max(max(max(t, w.x & 0x7fffffffu), max(w.y & 0x7fffffffu, w.z & 0x7fffffffu)), w.w & 0x7fffffffu);
+    }
+    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return t; }
     static __device__ __forceinline__ void get(const uint4 &w, float (&x)[4])
     {
         x[0] = __uint_as_float(w.x);
@@ -108,15 +141,21 @@ __device__ void append_check(const Geo &g, const Cache &c, int per_row, int *err
         *err = bad ? NSA_ERR_BAD_INDEX : NSA_OK;
 }
 
+// Blocks of an SM that the registers leave room for: as many as hold a
+// thread's vectors without spilling (8 prompts of up to 8192 tokens, 8 vectors
+// a thread: 31.0 us with 10 blocks, 34.8 with 6, 36.9 with 12; one vector: any
+// number serves).
+template <typename T, int VPT> constexpr int append_ctas() { return VPT == 1 ? 4 : VPT * sizeof(T) <= 16 ? 10 : 6; }
+
 // GROUP threads per head of k or v of a touched page; VPT vectors of the
 // page's new tokens per thread (VPT * GROUP * N elements cover a page, or
 // the call's few new tokens).
 template <typename T, int GROUP, int VPT>
-__global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const Cache c, const T *kn, const T *vn, int per_row,
+__global__ void __launch_bounds__(kCta, append_ctas<T, VPT>()) cache_append_kernel(const Geo g, const Cache c, const T *kn, const T *vn, int per_row,
                                                             int *err)
 {
     constexpr int N = Vec16<T>::N;
-    __shared__ float red[kCta / 32];
+    __shared__ uint32_t red[kCta / 32];
     dependents_may_start();
     dependency_wait();
     if (blockIdx.x == gridDim.x - 1) {
@@ -148,35 +187,45 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
     const int nvec = n << shift;
     const T *src = (which ? vn : kn) + (n > 0 ? kv_off(g, b, h, t0) : 0);
     const int st = (int)c.st;
+    // a thread's vectors lie at one place of tokens GROUP / vec_tok apart
+    const T *from = src + (lane >> shift) * g.skv.t + (lane & (vec_tok - 1)) * N;
     uint4 w[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-        const int x = lane + i * GROUP;
-        if (x < nvec)
-            w[i] = __ldg((const uint4 *)(src + (x >> shift) * g.skv.t + (x & (vec_tok - 1)) * N));
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (lane + i * GROUP < nvec)
+            w[i] = __ldg((const uint4 *)from);
+        from += (GROUP >> shift) * g.skv.t;
     }
     float *scales = (which ? c.vs : c.ks) + (int64_t)(n > 0 ? page : 0) * c.Hkv + h;
     const float old = lo > 0 && n > 0 ? *scales : 0.f;
-    float amax = 0.f;
+    auto of_group = [&](uint32_t bits) {  // their maximum
+        bits = __reduce_max_sync(0xffffffffu, bits);
+        if constexpr (GROUP > 32) {
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0)
+                red[threadIdx.x / 32] = bits;
+            __syncthreads();
+            bits = max(max(red[0], red[1]), max(red[2], red[3]));
+        }
+        return bits;
+    };
+    uint32_t top = 0;
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
-        if (lane + i * GROUP < nvec) {
+        top = Vec16<T>::top(top, w[i]);
+    float amax = __uint_as_float(of_group(Vec16<T>::top_bits(top)));
+    if (!(amax < INFINITY)) {  // infinities or NaN (the group's threads alike): of the others
+        float fin = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
             float x[N];
             Vec16<T>::get(w[i], x);
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float a = fabsf(x[e]);
-                amax = a < INFINITY ? fmaxf(amax, a) : amax;
-            }
+            for (int e = 0; e < N; ++e)
+                fin = fabsf(x[e]) < INFINITY ? fmaxf(fin, fabsf(x[e])) : fin;
         }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    if constexpr (GROUP > 32) {
-        if ((threadIdx.x & 31) == 0)
-            red[threadIdx.x / 32] = amax;
-        __syncthreads();
-        amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+        amax = __uint_as_float(of_group(__float_as_uint(fin)));
     }
     if (n == 0)
         return;
@@ -201,17 +250,15 @@ __global__ void __launch_bounds__(kCta) cache_append_kernel(const Geo g, const C
     }
     const float inv = pow2_inverse(scale);
     if (inv != 0.f) {
+        uint8_t *to = dst + (int64_t)(lo + (lane >> shift)) * st + (lane & (vec_tok - 1)) * N;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int x = lane + i * GROUP;
-            if (x < nvec) {
+            if (lane + i * GROUP < nvec) {
                 float f[N];
-                Vec16<T>::get(w[i], f);
-#pragma unroll
-                for (int e = 0; e < N; ++e)
-                    f[e] *= inv;
-                store_codes<N>(dst + (lo + (x >> shift)) * st + (x & (vec_tok - 1)) * N, f);
+                Vec16<T>::scaled(w[i], inv, f);
+                store_codes<N>(to, f);
             }
+            to += (GROUP >> shift) * st;
         }
     } else {  // a scale of the caller's, larger than the new tokens need: divided, off the common path
 #pragma unroll 1
