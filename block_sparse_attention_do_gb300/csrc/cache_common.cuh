@@ -41,7 +41,9 @@ constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a
 
 // The cache's kernels run one behind the other in steps of a few microseconds,
 // so each is launched as a programmatic dependent: it is set up while the one
-// before it ends, and waits here before it reads or writes anything.
+// before it ends, and waits here before it reads or writes anything.  What the
+// one before may have written is then read by plain loads: to a read-only load
+// nothing changes while its kernel runs, and this one runs already.
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

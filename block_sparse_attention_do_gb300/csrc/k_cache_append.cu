@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(kCta, append_ctas<T, VPT>()) cache_append_kern
     for (int i = 0; i < VPT; ++i) {
         w[i] = make_uint4(0, 0, 0, 0);
         if (lane + i * GROUP < nvec)
-            w[i] = __ldg((const uint4 *)from);
+            w[i] = *(const uint4 *)from;
         from += (GROUP >> shift) * g.skv.t;
     }
     float *scales = (which ? c.vs : c.ks) + (int64_t)(n > 0 ? page : 0) * c.Hkv + h;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kCta, append_ctas<T, VPT>()) cache_append_kern
 #pragma unroll 1
         for (int x = lane; x < nvec; x += GROUP) {
             float f[N];
-            Vec16<T>::get(__ldg((const uint4 *)(src + (x >> shift) * g.skv.t + (x & (vec_tok - 1)) * N)), f);
+            Vec16<T>::get(*(const uint4 *)(src + (x >> shift) * g.skv.t + (x & (vec_tok - 1)) * N), f);
 #pragma unroll
             for (int e = 0; e < N; ++e)
                 f[e] = __fdiv_rn(f[e], scale);

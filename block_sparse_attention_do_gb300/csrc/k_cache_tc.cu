@@ -192,7 +192,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
             uint4 x[D / 8];
 #pragma unroll
             for (int i = 0; i < D / 8; ++i)
-                x[i] = have ? __ldg((const uint4 *)src + i) : make_uint4(0, 0, 0, 0);
+                x[i] = have ? ((const uint4 *)src)[i] : make_uint4(0, 0, 0, 0);
             uint32_t top = 0;  // largest magnitude's bits
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
@@ -421,13 +421,13 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
             if (all) {
 #pragma unroll
                 for (int y = 0; y < LOADS; ++y)
-                    x[y] = __ldg((const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st));
+                    x[y] = *(const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st);
             } else {
 #pragma unroll
                 for (int y = 0; y < LOADS; ++y) {
                     const int key = first + y * PER_LOAD + key_in;
                     x[y] = there[y * PER_LOAD / 16] && key <= pmax && key >= key_first
-                               ? __ldg((const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st))
+                               ? *(const uint4 *)(at[y * PER_LOAD / 16] + y % (16 / PER_LOAD) * PER_LOAD * st)
                                : make_uint4(0, 0, 0, 0);
                 }
             }
