@@ -441,6 +441,8 @@ nsa_status nsa_select_topk(const nsa_problem *p, const int32_t *cu_seqlens, cons
  * is reported (NSA_ERR_BAD_INDEX through nsa_get_error(ws, ...), of the last
  * call that used ws) and left out; nothing is read or written outside the
  * pool.
+ * Positions and entries are counted in ints: num_pages * Hkv, rows * max_pages
+ * and max_pages * block_size + T near 2^31 are refused (NSA_ERR_UNSUPPORTED).
  */
 typedef struct nsa_cache {
     int32_t num_pages;

@@ -166,3 +166,13 @@ def test_tensors_are_checked():
                dict(k=k.transpose(2, 3), v=k.transpose(2, 3))):
         with pytest.raises(api.NsaError):
             api.KVCache(**{**good, **kw})
+
+
+def test_positions_stay_within_an_int(lib):
+    """Positions reach from -T to the table's last key."""
+    thd = dict(layout=api.LAYOUT_THD, total_tokens=5)
+    for T, code in ((2 ** 31 - 1, 0), (2 ** 31 - 640 - 64, 0), (2 ** 31 - 640 - 66, 1)):
+        assert (lib.nsa_cache_fwd_workspace_size(problem(T=T, **thd), cache(), 0) > 0) == bool(code), T
+    p = problem(T=2 ** 31 - 1, **thd)
+    assert lib.nsa_cache_fwd(p, cache(), 0, P, None, None, P, P, P, P, BIG, None) == UNSUPPORTED
+    assert lib.nsa_cache_append(p, cache(), P, P, P, P, BIG, None) == UNSUPPORTED
