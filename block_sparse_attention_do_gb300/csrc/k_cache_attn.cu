@@ -193,6 +193,17 @@ __device__ __forceinline__ int query_tokens(const Geo &g, int b)
     return g.thd && (n < 0 || n > g.T || g.cu[b] < 0 || g.cu[b + 1] > g.ntok) ? -1 : n;
 }
 
+// Whether packed token tok is a query of some sequence: then of sequence b,
+// its t-th.  Tokens in front of the first offset, or of a range that is none,
+// are nobody's.
+__device__ __forceinline__ bool query_of(const Geo &g, int tok, int &b, int &t)
+{
+    b = seq_of_token(g, tok);
+    const int n = query_tokens(g, b);
+    t = n > 0 ? tok - g.cu[b] : 0;
+    return t >= 0 && t < n;
+}
+
 // tokens of sequence b in the cache (a length that the table cannot hold is reported by the join)
 __device__ __forceinline__ int held_tokens(const AttnArgs &a, int b)
 {
@@ -297,9 +308,7 @@ __device__ __noinline__ void attn_check(const AttnArgs &a)
             const int row = a.by_S.divmod(i, s);
             if (g.thd) {
                 const int tok = a.by_Hkv.divmod(row, h);
-                b = seq_of_token(g, tok);
-                t = tok - g.cu[b];
-                if (t >= query_tokens(g, b))
+                if (!query_of(g, tok, b, t))
                     continue;  // a token of no sequence
             } else
                 b = a.by_Hkv.divmod(a.by_T.divmod(row, t), h);
@@ -409,15 +418,14 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             u.begin = CLUSTER ? 0 : unit * g.S;
             u.count = g.S;
             int rt, t;
+            bool query = true;
             const int row = a.by_tiles.divmod(unit, rt);  // of the index
-            if (g.thd) {
-                const int tok = a.by_Hkv.divmod(row, u.kvh);
-                u.b = seq_of_token(g, tok);
-                t = tok - g.cu[u.b];
-            } else
+            if (g.thd)
+                query = query_of(g, a.by_Hkv.divmod(row, u.kvh), u.b, t);
+            else
                 u.b = a.by_Hkv.divmod(a.by_T.divmod(row, t), u.kvh);
             u.row0 = t * g.G + rt * R;
-            u.nrows = t < query_tokens(g, u.b) ? min(R, g.G - rt * R) : 0;  // 0: a token of no sequence
+            u.nrows = query ? min(R, g.G - rt * R) : 0;  // 0: a token of no sequence
             u.page_lo = 0;
         } else if (CLUSTER) {
             int rt;
@@ -975,10 +983,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
         int h, b, t;
         const int tok = a.by_Hq.divmod(w, h);
         if (g.thd) {
-            b = seq_of_token(g, tok);
-            t = tok - g.cu[b];
-            if (t >= query_tokens(g, b))
-                continue;
+            if (!query_of(g, tok, b, t))
+                continue;  // a token of no sequence
         } else
             b = a.by_T.divmod(tok, t);
         int hh;

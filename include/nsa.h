@@ -521,8 +521,10 @@ nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *c, const int3
  * sinks (Hq floats or NULL): as for nsa_sink_fwd.  q, o: p's dtype, layout and
  * strides; lse as for the other forwards.  A row that attends nothing gets
  * O = 0 and LSE = -inf (with sinks: the sink).  Masked places may hold
- * anything, NaN included.  Rows of THD tensors that belong to no sequence are
- * left as they were.  p->B = rows, p->Hkv, D and block_size the cache's,
+ * anything, NaN included.  Rows of THD tensors that belong to no sequence
+ * (in front of the first offset, behind the last, or of a run that goes
+ * backward, past the tensor or beyond T tokens: that is reported) are left as
+ * they were.  p->B = rows, p->Hkv, D and block_size the cache's,
  * p->kv_stride unused.  `selection`: whether block_idx will be given.
  * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).  A call that
  * needs a workspace of 256 bytes needs it for the error word alone: its ws may

@@ -516,6 +516,61 @@ def test_packed_offsets_that_are_none_are_reported():
     assert api.get_error(ws) == 3
 
 
+def packed_call(q, cache, offsets, bound, idx=None, **kw):
+    """nsa_cache_fwd on packed queries, outputs set to 7 before: (o, lse, error, form)."""
+    total, Hq, D = q.shape
+    o, lse = torch.full_like(q, 7.0), torch.full((total, Hq), 7.0, device=DEV)
+    p = api.problem(len(offsets) - 1, Hq, cache.struct.Hkv, bound, D, cache.struct.block_size, 1 if idx is None else idx.shape[-1],
+                    q.dtype, layout=api.LAYOUT_THD, total_tokens=total)
+    n = api.lib().nsa_cache_fwd_workspace_size(p, cache.ref, int(idx is not None))
+    ws, cu = torch.empty(n, dtype=torch.uint8, device=DEV), i32(*offsets)
+    sinks = kw.get("sinks")
+    form = form_of(lambda: api._check(api.lib().nsa_cache_fwd(
+        p, cache.ref, kw.get("window", 0), cu.data_ptr(), None if idx is None else idx.data_ptr(),
+        None if sinks is None else sinks.data_ptr(), q.data_ptr(), o.data_ptr(), lse.data_ptr(), ws.data_ptr(), n, api._stream()), "fwd"))
+    return o, lse, api.get_error(ws), form
+
+
+def check_packed(q, cache, offsets, o, lse, idx=None):
+    """The runs that are one against the plain form; every other row untouched."""
+    total, Hq, D = q.shape
+    mine = np.zeros(total, bool)
+    for b, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        if 0 <= lo <= hi <= total:
+            mine[lo:hi] = True
+            want = Plain(cache).attend(b, q[lo:hi].double().cpu().numpy(), 1 / math.sqrt(D), None if idx is None else idx[lo:hi].cpu().numpy())
+            check_attend(o[lo:hi].double().cpu().numpy(), lse[lo:hi].double().cpu().numpy(), *want, q.dtype, D)
+    other = torch.tensor(~mine, device=DEV)
+    assert (o[other] == 7).all() and (lse[other] == 7).all()
+
+
+@pytest.mark.parametrize("front,error", [(True, 0), (False, 3)])
+@pytest.mark.parametrize("form,dtype,Hq,Hkv,D,bs,lens,runs,S,cols", [
+    ("cache_attn_cluster", BF, 8, 2, 64, 32, [100, 70], (5, 9, 14), 3, None),
+    ("cache_attn_cluster", F32, 8, 2, 64, 32, [100, 70], (5, 9, 14), 0, None),
+    ("cache_attn", BF, 8, 2, 64, 32, [300, 200], (37, 60, 165), 40, None),  # index rows cut, and joined
+    ("cache_attn", F32, 40, 2, 32, 16, [300, 200], (37, 60, 125), 40, None),
+    ("cache_attn", F32, 8, 2, 64, 32, [300, 200], (37, 60, 125), 0, 600),
+    ("cache_chunk", BF, 16, 8, 64, 32, [500, 400], (15, 300, 600), 0, None)])
+def test_tokens_in_front_of_the_first_offset_are_left(form, dtype, Hq, Hkv, D, bs, lens, runs, S, cols, front, error):
+    """Offsets that begin behind the first token ([5, 9, 14]), and a first run that goes backward ([9, 5, 14]):
+    the tokens before belong to no sequence, and none of their rows is read or written."""
+    a, b, c = runs
+    offsets, total = [a, b, c] if front else [b, a, c], c + 6
+    cache = filled(lens, Hkv, D, bs, 4, cols=cols)
+    g = np.random.default_rng(4)
+    q = torch.tensor(g.normal(size=(total, Hq, D)), dtype=torch.float32).to(dtype).to(DEV)
+    idx = None
+    if S:
+        idx = torch.zeros(total, Hkv, S, dtype=torch.int32, device=DEV)
+        new = [max(0, y - x) for x, y in zip(offsets, offsets[1:])]
+        at = a if front else offsets[1]
+        idx[at:at + sum(new)] = torch.tensor(index_rows(lens, new, Hkv, S, bs, g), device=DEV)
+    o, lse, e, took = packed_call(q, cache, offsets, c, idx)
+    assert took == form and e == error
+    check_packed(q, cache, offsets, o, lse, idx)
+
+
 def test_calls_on_two_streams_and_in_graphs():
     cache = filled([3000, 100, 0, 64], 2, 128, 64, 4)
     qs = [torch.randn(4, 8, T, 128, device=DEV).to(BF) for T in (1, 1, 3, 50)]
