@@ -36,6 +36,18 @@ struct CacheWs {
 inline int longest_tokens(const Geo &g) { return g.thd ? min(g.T, max(g.ntok, 1)) : g.T; }
 inline int64_t longest_rows(const Geo &g) { return (int64_t)longest_tokens(g) * g.G; }
 
+// The new tokens (queries; keys and values to append) of sequence b; -1 for a
+// packed range that is none or is longer than the problem says: none of its
+// rows is read or written.  The offsets may be any ints: they are compared
+// before they are subtracted.
+__device__ __forceinline__ int new_tokens(const Geo &g, int b)
+{
+    if (!g.thd)
+        return g.T;
+    const int from = g.cu[b], to = g.cu[b + 1];
+    return from < 0 || to < from || to > g.ntok || to - from > g.T ? -1 : to - from;
+}
+
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
 

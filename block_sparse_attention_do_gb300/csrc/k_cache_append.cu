@@ -105,13 +105,12 @@ template <int N> __device__ __forceinline__ void store_codes(uint8_t *p, const f
 
 // the new tokens of row b: their count and first position; false where the
 // row's length or packed range cannot hold them
-__device__ __forceinline__ bool new_tokens(const Geo &g, const Cache &c, int b, int &n, int &start)
+__device__ __forceinline__ bool places(const Geo &g, const Cache &c, int b, int &n, int &start)
 {
     const int len = c.lens[b];
-    n = seq_len(g, b);
-    start = len - n;
-    return n >= 0 && n <= g.T && start >= 0 && (int64_t)len <= (int64_t)c.cols * c.bs &&
-           (!g.thd || (g.cu[b] >= 0 && g.cu[b + 1] <= g.ntok));
+    n = new_tokens(g, b);
+    start = n >= 0 && len >= n ? len - n : -1;
+    return start >= 0 && (int64_t)len <= (int64_t)c.cols * c.bs;
 }
 
 // a page that new tokens may go into: in the pool, and no other row's
@@ -131,7 +130,7 @@ __device__ void append_check(const Geo &g, const Cache &c, int per_row, int *err
     for (int64_t i = threadIdx.x; i < (int64_t)c.rows * per_row; i += kCta) {
         const int b = (int)(i / per_row), j = (int)(i % per_row);
         int n, start;
-        if (!new_tokens(g, c, b, n, start))
+        if (!places(g, c, b, n, start))
             bad = 1;
         else if (n > 0 && (start >> c.bsh) + j <= (start + n - 1) >> c.bsh)
             bad |= !writable(c, c.table[(int64_t)b * c.cols + (start >> c.bsh) + j]);
@@ -170,7 +169,7 @@ __global__ void __launch_bounds__(kCta, append_ctas<T, VPT>()) cache_append_kern
     int lo = 0, n = 0, page = -1, t0 = 0;  // the page's slots [lo, lo + n) get tokens t0 ..
     if (live) {
         int nn, start;
-        if (new_tokens(g, c, b, nn, start)) {
+        if (places(g, c, b, nn, start)) {
             const int col = (start >> c.bsh) + j, first = max(start, col * c.bs), end = min(start + nn, (col + 1) * c.bs);
             if (first < end) {
                 page = c.table[(int64_t)b * c.cols + col];

@@ -185,21 +185,13 @@ template <int D> __device__ __forceinline__ int v_at(int t, int u)
     return (t * (D / 16) + u) ^ (D == 128 ? (t >> 1 & 3) << 1 : D == 64 ? (t >> 1 & 1) << 2 | (t >> 2 & 1) << 1 : (t >> 2 & 1) << 1);
 }
 
-// query tokens of sequence b; -1 for a packed range that is not one, or is
-// longer than the problem says (none of its rows is read or written)
-__device__ __forceinline__ int query_tokens(const Geo &g, int b)
-{
-    const int n = seq_len(g, b);
-    return g.thd && (n < 0 || n > g.T || g.cu[b] < 0 || g.cu[b + 1] > g.ntok) ? -1 : n;
-}
-
 // Whether packed token tok is a query of some sequence: then of sequence b,
 // its t-th.  Tokens in front of the first offset, or of a range that is none,
 // are nobody's.
 __device__ __forceinline__ bool query_of(const Geo &g, int tok, int &b, int &t)
 {
     b = seq_of_token(g, tok);
-    const int n = query_tokens(g, b);
+    const int n = new_tokens(g, b);
     t = n > 0 ? tok - g.cu[b] : 0;
     return t >= 0 && t < n;
 }
@@ -213,7 +205,7 @@ __device__ __forceinline__ int held_tokens(const AttnArgs &a, int b)
 // The pages of sequence b that any of its query rows attends: [lo, lo + n).
 __device__ __forceinline__ int attended_pages(const AttnArgs &a, int b, int &lo)
 {
-    const int nq = query_tokens(a.g, b), len = held_tokens(a, b);
+    const int nq = new_tokens(a.g, b), len = held_tokens(a, b);
     lo = 0;
     if (nq <= 0 || len <= 0)
         return 0;
@@ -227,7 +219,7 @@ __device__ __forceinline__ int attended_pages(const AttnArgs &a, int b, int &lo)
 // tiles of R query rows of sequence b (dense)
 template <int R> __device__ __forceinline__ int row_tiles_of(const Geo &g, int b)
 {
-    return (max(query_tokens(g, b), 0) * g.G + R - 1) / R;
+    return (max(new_tokens(g, b), 0) * g.G + R - 1) / R;
 }
 
 // A unit of the list: a tile of query rows and the run of list entries that
@@ -289,7 +281,7 @@ __device__ __noinline__ void attn_check(const AttnArgs &a)
         return page < 0 || page >= c.pages;
     };
     for (int b = tid; b < g.B; b += kThreads)
-        bad |= c.lens[b] < 0 || c.lens[b] > c.cols * c.bs || query_tokens(g, b) < 0;
+        bad |= c.lens[b] < 0 || c.lens[b] > c.cols * c.bs || new_tokens(g, b) < 0;
     if (!a.idx)
         for (int b = tid >> 5; b < g.B; b += kWarps) {
             int lo;
@@ -312,7 +304,7 @@ __device__ __noinline__ void attn_check(const AttnArgs &a)
                     continue;  // a token of no sequence
             } else
                 b = a.by_Hkv.divmod(a.by_T.divmod(row, t), h);
-            const int pos = held_tokens(a, b) - query_tokens(g, b) + t;
+            const int pos = held_tokens(a, b) - new_tokens(g, b) + t;
             if (j < 0 || j >= c.cols || j * c.bs > pos || bad_page(b, j))
                 bad = 1;
             for (int k = i - s; k < i; ++k)
@@ -433,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             u.begin = 0;
             u.count = attended_pages(a, u.b, u.page_lo);
             u.row0 = rt * R;
-            u.nrows = min(R, query_tokens(g, u.b) * g.G - u.row0);
+            u.nrows = min(R, new_tokens(g, u.b) * g.G - u.row0);
         } else {
             int lo = 0, hi = g.B - 1;  // the sequence: prefix[b] * Hkv <= at < prefix[b + 1] * Hkv
             while (lo < hi) {
@@ -450,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             u.count = n;
             u.kvh = tiles == 1 ? in : in / tiles;
             u.row0 = tiles == 1 ? 0 : in % tiles * R;
-            u.nrows = min(R, query_tokens(g, lo) * g.G - u.row0);
+            u.nrows = min(R, new_tokens(g, lo) * g.G - u.row0);
         }
         int seg1;
         if constexpr (CLUSTER) {
@@ -468,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
             }
         }
         const int len = held_tokens(a, u.b);
-        const int pos0 = len - query_tokens(g, u.b);  // position of the sequence's first query token
+        const int pos0 = len - new_tokens(g, u.b);  // position of the sequence's first query token
         const int t_first = a.by_G.div(u.row0), t_last = a.by_G.div(u.row0 + u.nrows - 1);
         const int pmin = pos0 + t_first, pmax = pos0 + t_last;  // of the tile's rows
         const int key_lo = g.window > 0 ? pmin - g.window - 14 : INT32_MIN;  // steps before it lie left of every window
@@ -967,7 +959,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
         int bad = 0;
         for (int b = tid; b < g.B; b += kJoinThreads) {
             const int len = a.c.lens[b];
-            bad |= len < 0 || len > a.c.cols * a.c.bs || query_tokens(g, b) < 0;
+            bad |= len < 0 || len > a.c.cols * a.c.bs || new_tokens(g, b) < 0;
         }
         dependency_wait();
         for (int i = tid; i < a.ncta; i += kJoinThreads)
@@ -995,7 +987,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
             count = g.S;
         } else {
             int lo;
-            const int row = t * g.G + hh, tiles = (query_tokens(g, b) * g.G + R - 1) / R;
+            const int row = t * g.G + hh, tiles = (new_tokens(g, b) * g.G + R - 1) / R;
             r = row % R;
             count = attended_pages(a, b, lo);
             in = (kvh * tiles + row / R) * (count + a.start_cost) + a.start_cost;

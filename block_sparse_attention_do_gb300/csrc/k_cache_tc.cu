@@ -129,12 +129,11 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
     // sequence's last rows, which attend the most keys, come first
     const int nbg = g.B * g.Hkv, bg = blockIdx.x % nbg, from_end = blockIdx.x / nbg;
     const int b = bg / g.Hkv, kvh = bg % g.Hkv;
-    const int nq = seq_len(g, b), cap = c.cols * c.bs, lens = c.lens[b];
+    const int nq = new_tokens(g, b), cap = c.cols * c.bs, lens = c.lens[b];
     const int len = min(max(lens, 0), cap);
-    const bool packed_ok = !g.thd || (nq >= 0 && nq <= g.T && g.cu[b] >= 0 && g.cu[b + 1] <= g.ntok);
-    if (from_end == 0 && kvh == 0 && threadIdx.x == 0 && (lens != len || !packed_ok))
+    if (from_end == 0 && kvh == 0 && threadIdx.x == 0 && (lens != len || nq < 0))
         set_error(p.err, NSA_ERR_BAD_INDEX);
-    const int tile = packed_ok ? (nq * g.G + kTileRows - 1) / kTileRows - 1 - from_end : -1;
+    const int tile = nq > 0 ? (nq * g.G + kTileRows - 1) / kTileRows - 1 - from_end : -1;
     if (tile < 0)
         return;
     const int row0 = tile * kTileRows, nrows = min(kTileRows, nq * g.G - row0);

@@ -571,6 +571,24 @@ def test_tokens_in_front_of_the_first_offset_are_left(form, dtype, Hq, Hkv, D, b
     check_packed(q, cache, offsets, o, lse, idx)
 
 
+@pytest.mark.parametrize("offsets", [[2 ** 31 - 1, -2 ** 31, 4], [2 ** 31 - 1, -2 ** 31 + 300, 400], [-2 ** 31, 2 ** 31 - 1, 5],
+                                     [2, 2 ** 31 - 1, 2 ** 31 - 1]])
+@pytest.mark.parametrize("total,Hq,Hkv,S", [(12, 8, 2, 0), (12, 8, 2, 3), (600, 16, 8, 0)])
+def test_offsets_whose_difference_leaves_the_ints_are_reported(offsets, total, Hq, Hkv, S):
+    """Runs from one end of the ints to the other, some of them 1 or 300 tokens long by a difference that wraps round."""
+    cache = filled([400, 300], Hkv, 64, 32, 4)
+    q = torch.randn(total, Hq, 64, device=DEV).to(BF)
+    idx = torch.zeros(total, Hkv, S, dtype=torch.int32, device=DEV) if S else None
+    o, lse, e, _ = packed_call(q, cache, offsets, total, idx)
+    assert e == 3 and (o == 7).all() and (lse == 7).all()
+    before = [x.clone() for x in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale)]
+    new = torch.randn(total, Hkv, 64, device=DEV).to(BF)
+    api.cache_append(cache, new, new, cu_seqlens=i32(*offsets), max_seqlen=total)
+    assert api.get_error(cache.ws) == 3
+    for a, b in zip(before, (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale)):
+        assert torch.equal(a, b)
+
+
 def test_calls_on_two_streams_and_in_graphs():
     cache = filled([3000, 100, 0, 64], 2, 128, 64, 4)
     qs = [torch.randn(4, 8, T, 128, device=DEV).to(BF) for T in (1, 1, 3, 50)]
