@@ -941,8 +941,9 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
 // parts' maxima and sums, a thread each, then their vectors, the warps taking
 // the parts in turn with several loads in flight; the order of the sums is
 // that of CTAs and warps, whatever order they ran in.  The kernel is a
-// programmatic dependent of the main one: it is set up while that runs and
-// waits before it reads what that wrote.
+// programmatic dependent of the main one, which lets it start before the
+// kernels in front of both may have ended: it waits before it reads anything,
+// the lengths and offsets too (a reserve two launches back may still write them).
 // kJoinWarps: 8 for few rows of many parts, 2 where the rows alone fill the
 // GPU (1920 rows of 2 or 3 parts: 64 threads each have them all under way).
 template <typename T, int D, int kJoinWarps>
@@ -953,6 +954,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
     const Geo &g = a.g;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     dependents_may_start();
+    dependency_wait();
     __shared__ float part[kJoinWarps][D];
     __shared__ float factor[kJoinThreads], red[2][kJoinWarps];
     if (blockIdx.x == 0) {  // the call's error word
@@ -961,7 +963,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
             const int len = a.c.lens[b];
             bad |= len < 0 || len > a.c.cols * a.c.bs || new_tokens(g, b) < 0;
         }
-        dependency_wait();
         for (int i = tid; i < a.ncta; i += kJoinThreads)
             bad |= a.status[i] != NSA_OK;
         bad = __syncthreads_or(bad);
@@ -992,7 +993,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const AttnA
             count = attended_pages(a, b, lo);
             in = (kvh * tiles + row / R) * (count + a.start_cost) + a.start_cost;
         }
-        dependency_wait();
         int first = 0, last = -1, begin = 0;  // the CTAs with a part of the row
         if (count > 0) {
             int total;

@@ -1,6 +1,9 @@
 """The paged 8-bit cache's entry points refuse bad calls on the host, before
 any launch (no GPU needed)."""
 import ctypes as C
+import glob
+import os
+import re
 
 import pytest
 import torch
@@ -176,3 +179,21 @@ def test_positions_stay_within_an_int(lib):
     p = problem(T=2 ** 31 - 1, **thd)
     assert lib.nsa_cache_fwd(p, cache(), 0, P, None, None, P, P, P, P, BIG, None) == UNSUPPORTED
     assert lib.nsa_cache_append(p, cache(), P, P, P, P, BIG, None) == UNSUPPORTED
+
+
+def test_kernels_wait_before_they_read():
+    """Every kernel of the cache may start while the launches before it still run (a reserve that writes lengths, an
+    append that writes pages): nothing of a call's arguments is read in front of its wait for them."""
+    csrc = os.path.join(os.path.dirname(api.__file__), "csrc")
+    seen = 0
+    for path in glob.glob(os.path.join(csrc, "k_cache_*.cu")):
+        text = re.sub(r"//[^\n]*", "", open(path).read())
+        for part in text.split("__global__")[1:]:
+            name = re.search(r"\b(cache_\w+)\(", part).group(1)
+            body = part[part.index("\n{"):part.index("\n}")]
+            assert "dependency_wait();" in body, name
+            before = body[:body.index("dependency_wait();")]
+            assert not re.search(r"\b(lens|cu|table|ref|ks|vs|status|idx|sinks|n_new|rows|src|dst|part_\w+|p[012]|npairs|err)\b|"
+                                 r"\b\w+(_tokens|_pages|_of|_off|_len)\(", before), (name, before)
+            seen += 1
+    assert seen == 10

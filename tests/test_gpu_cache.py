@@ -1041,3 +1041,69 @@ def test_serving_steps(dtype, Hq, Hkv, D, bs, graph):
             prompts([7, 0, 0, 0, bs + 1, 0])
             same_pool(cache, plain)
     same_pool(cache, plain)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_serving_steps_of_the_list_form(graph):
+    """Page operations that write lengths, append, and the attention's two kernels directly behind them: rows leave, are
+    forked and grow in one step after another, with nothing between the launches."""
+    g = np.random.default_rng(12)
+    rows, cols, Hq, Hkv, D, bs, dtype = 40, 40, 8, 2, 128, 64, BF
+    cache = api.make_cache(300, Hkv, D, bs, rows, cols)
+    plain = Plain(cache)
+    new = [int(n) for n in g.integers(0, 200, rows)]
+    api.cache_reserve(cache, i32(*new))
+    assert plain.reserve(new) == 0
+    k, v = (torch.tensor(g.normal(size=(sum(new), Hkv, D)), dtype=torch.float32).to(dtype) for _ in range(2))
+    cu = np.concatenate([[0], np.cumsum(new)])
+    api.cache_append(cache, k.to(DEV), v.to(DEV), cu_seqlens=i32(*cu), max_seqlen=max(new))
+    for b in range(rows):
+        plain.append(b, *(x[cu[b]:cu[b + 1]].double().numpy() for x in (k, v)))
+    free, src, dst = i32(3, 20, 39), i32(0, 1, 5), i32(10, 11, 3)
+    grow = i32(*[int(n) for n in g.integers(0, 2, rows)])
+    q, kn, vn = (torch.tensor(g.normal(size=(rows, H, 1, D)), dtype=torch.float32).to(dtype).to(DEV) for H in (Hq, Hkv, Hkv))
+    turn = i32(*[1] * rows)
+
+    def step():
+        api.cache_reserve(cache, grow)
+        api.cache_free(cache, free)
+        api.cache_fork(cache, src, dst)
+        a = api.cache_fwd(q, cache)
+        api.cache_reserve(cache, turn)
+        api.cache_append(cache, kn, vn)
+        return a, api.cache_fwd(q, cache)
+
+    assert form_of(lambda: api.cache_fwd(q, cache)) == "cache_attn"
+    run = step
+    if graph:
+        saved = [x.clone() for x in (cache.page_table, cache.seq_lens, cache.refcount)]
+        captured = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(captured):
+            got = step()
+        for a, b in zip((cache.page_table, cache.seq_lens, cache.refcount), saved):
+            a.copy_(b)
+
+        def run():
+            captured.replay()
+            return got
+    # the rows that grow here attend values that no append wrote: the same on both sides
+    for i in range(12):
+        outs = run()
+        assert plain.reserve(grow.tolist()) == 0
+        for r in free.tolist():
+            plain.release(r)
+        assert plain.fork(src.tolist(), dst.tolist()) == 0
+        before = [x.copy() for x in (plain.lens, plain.table)]
+        pool = [x.copy() for x in (plain.k, plain.v, plain.ks, plain.vs)]
+        assert plain.reserve(turn.tolist()) == 0
+        for b in range(rows):
+            plain.append(b, kn[b, :, 0].double().cpu().numpy()[None], vn[b, :, 0].double().cpu().numpy()[None])
+        same_meta(cache, plain)
+        same_pool(cache, plain)
+        after = [plain.lens, plain.table, plain.k, plain.v, plain.ks, plain.vs]
+        for (o, lse), state in ((outs[0], before + pool), (outs[1], after)):
+            plain.lens, plain.table, plain.k, plain.v, plain.ks, plain.vs = state
+            for b in range(0, rows, 1 if i in (0, 11) else 7):
+                want = plain.attend(b, q[b].transpose(0, 1).double().cpu().numpy(), 1 / math.sqrt(D))
+                check_attend(o[b].transpose(0, 1).double().cpu().numpy(), lse[b].transpose(0, 1).double().cpu().numpy(), *want, dtype, D)
+        plain.lens, plain.table, plain.k, plain.v, plain.ks, plain.vs = after
