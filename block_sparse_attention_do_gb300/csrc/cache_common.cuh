@@ -51,6 +51,12 @@ __device__ __forceinline__ int new_tokens(const Geo &g, int b)
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100: the scale of a block of zeros
 
+// The attention's weights carry their page's value scale, w = p vs; with scales
+// within 2^-kNearScale .. 2^kNearScale the sum of p can be had from them, as
+// w / vs: a w that has left float's range belongs to a p below 2^-46 of the
+// row's largest.  A page outside has its p summed by an exponential of their own.
+constexpr float kNearScale = 40.f;
+
 // The cache's kernels run one behind the other in steps of a few microseconds,
 // so each is launched as a programmatic dependent: it is set up while the one
 // before it ends, and waits here before it reads or writes anything.  What the

@@ -6,7 +6,12 @@
 //   x_j = scale * log2(e) * ks_j * <q_r, ck_j>,  w_j = 2^(x_j + log2(vs_j) - M)
 //   O = sum w_j cv_j / sum (w_j / vs_j),  LSE = ln 2 * (M + log2 sum (w_j / vs_j))
 // The value scale rides in the exponent, so the second product runs on plain
-// codes and a page of small values costs no range.
+// codes and a page of small values costs O no range.  For the sum it may: where
+// a page's scale lies outside 2^-40 .. 2^40 a weight w can underflow although
+// w / vs counts (64 values of zero, scale 2^-100, beside others of scale 2^27:
+// half the sum).  From a list with such a page on the sum is taken from the
+// scores alone, 2^(x_j - log2(vs_j) - N) with a maximum N of their own, in a pass
+// over the keys of its own; at the unit's end O is turned to units of 2^N.
 //
 // What bounds it: the cache's bytes, 2 D per key and kv head, each read once;
 // 4 G D operations on them are far below the tensor cores' rate (G = 4: 8
@@ -260,6 +265,7 @@ template <int D, int NT, bool SPLIT> struct Smem {
     int key0[kList];     // first key (kNoKey: left out)
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
     float2 ml[kWarps][R];       // each warp's maximum and sum
+    float2 alone[kWarps][R];    // those of the scores alone, once the sum is kept apart
     float2 cta_ml[R];           // the CTA's, for its cluster
     uint32_t nan[kWarps][R * D / 32];  // each warp's outputs that a NaN value reaches
     union {
@@ -555,8 +561,38 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         }
         my_page = in_pool(my_block, my_page);
 
+        // S^T = K q^T of a thread's 16 codes of two tokens
+        auto scores = [&](const uint32_t (&kw)[2][KL * KB / 4], float (&x)[NT][4]) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[n][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                uint32_t af[4];
+                e4m3x4_to_half(kw[0][k], af[0], af[2]);
+                e4m3x4_to_half(kw[1][k], af[1], af[3]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const uint2 bf = sm.qf[0][k][n][lane];
+                    mma_f16(x[n], af, bf.x, bf.y);
+                    if constexpr (SPLIT) {
+                        const uint2 bl = sm.qf[SPLIT ? 1 : 0][k][n][lane];
+                        mma_f16(x[n], af, bl.x, bl.y);
+                    }
+                }
+            }
+        };
+        // over the lanes that share a query row
+        auto sum_of_rows = [](float x) {
+            x += __shfl_xor_sync(0xffffffffu, x, 4);
+            x += __shfl_xor_sync(0xffffffffu, x, 8);
+            return x + __shfl_xor_sync(0xffffffffu, x, 16);
+        };
         float o[NT][MT][4];
         float m[NT][2], l[NT][2];
+        bool apart = false;  // (uniform over the CTA) the sums are in sm.alone
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -610,13 +646,16 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
 #pragma unroll
             for (int i = 0; i < kStages - 1; ++i)
                 fetch(warp + i * kWarps, i);
+            bool far = apart;  // a scale of values outside the common range
             if (tid < ne) {
                 float ks = 0.f, vs = 1.f;
                 if (my_page >= 0) {
                     ks = c.ks[(int64_t)my_page * c.Hkv + u.kvh];
                     vs = fmaxf(c.vs[(int64_t)my_page * c.Hkv + u.kvh], kScaleFloor);
                 }
-                sm.sc[tid] = make_float4(ks, log2f(vs), 1.f / vs, 0.f);
+                const float lvs = log2f(vs);
+                far = far || fabsf(lvs) > kNearScale;
+                sm.sc[tid] = make_float4(ks, lvs, 1.f / vs, 0.f);
             }
             if (sel && warp * 32 < ne) {  // an entry that its row has before is left out: no row attends its keys
                 bool twice = false;
@@ -633,7 +672,23 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                     sm.key0[tid] = kNoKey;
                 }
             }
-            __syncthreads();
+            far = __syncthreads_or(far);
+            if (far) {
+                if (!apart)  // the warp's sums so far
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = sum_of_rows(l[n][i]);
+                            if (gq == 0)
+                                sm.alone[warp][n * 8 + tq * 2 + i] = make_float2(m[n][i], x);
+                            l[n][i] = 0.f;
+                        }
+                apart = true;
+                if (tid < ne)
+                    sm.sc[tid].z = 0.f;  // its weights add nothing to the sum
+                __syncthreads();
+            }
             for (int s = warp; s < steps; s += kWarps) {
                 __syncwarp();  // the stage that is filled now has been read
                 fetch(s + (kStages - 1) * kWarps, stage == 0 ? kStages - 1 : stage - 1);
@@ -650,28 +705,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
 #pragma unroll
                     for (int i = 0; i < KL; ++i)
                         load_shared<KB>(at + (from_k ^ i * 64) + r * 8 * D, &kw[r][i * (KB / 4)]);
-                // ---- S^T = K q^T
                 float x[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        x[n][i] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    uint32_t af[4];
-                    e4m3x4_to_half(kw[0][k], af[0], af[2]);
-                    e4m3x4_to_half(kw[1][k], af[1], af[3]);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const uint2 bf = sm.qf[0][k][n][lane];
-                        mma_f16(x[n], af, bf.x, bf.y);
-                        if constexpr (SPLIT) {
-                            const uint2 bl = sm.qf[SPLIT ? 1 : 0][k][n][lane];
-                            mma_f16(x[n], af, bl.x, bl.y);
-                        }
-                    }
-                }
+                scores(kw, x);
                 // ---- w = 2^(x + log2 vs - M)
                 const float4 sc = sm.sc[s >> per_sh];
 #pragma unroll
@@ -802,6 +837,50 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                     }
             }
             tc::cp_async_wait<0>();
+            if (far) {  // the list's keys once more, for the sum of the scores alone
+#pragma unroll 1
+                for (int s = warp; s < steps; s += kWarps) {
+                    const int key_now = step_key(s);
+                    if (!attended(key_now))
+                        continue;
+                    const uint8_t *from = c.k + sm.off[s >> per_sh] + (int64_t)((s & per_mask) * 16 + gq) * st + tq * KB;
+                    uint32_t kw[2][KL * KB / 4];
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+#pragma unroll
+                        for (int i = 0; i < KL * KB / 4; i += 2)
+                            *(uint2 *)&kw[r][i] = *(const uint2 *)(from + r * 8 * st + i / (KB / 4) * 4 * KB + i % (KB / 4) * 4);
+                    float x[NT][4];
+                    scores(kw, x);
+                    const float ks = sm.sc[s >> per_sh].x;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int r = n * 8 + tq * 2 + i, p = sm.pos[r];
+                            const float f = ks * sm.qmul[r];
+                            const float2 old = sm.alone[warp][r];
+                            float y[2], top = old.x, sum = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int kk = key_now + gq + e * 8;
+                                y[e] = kk > p || (g.window > 0 && kk <= p - g.window) ? -INFINITY : x[n][i + 2 * e] * f;
+                                top = fmaxf(top, y[e]);
+                            }
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                sum += tc::ex2(y[e] - top);
+                            sum = sum_of_rows(sum);
+                            __syncwarp();  // (every lane has read the old ones)
+                            if (gq == 0)
+                                sm.alone[warp][r] = make_float2(top, old.y * exp2f(old.x - top) + sum);
+                        }
+                    __syncwarp();
+                }
+            }
         }
 
         // ---- the warps' sums joined in shared memory (over the rings)
@@ -810,10 +889,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                float x = l[n][i];
-                x += __shfl_xor_sync(0xffffffffu, x, 4);
-                x += __shfl_xor_sync(0xffffffffu, x, 8);
-                x += __shfl_xor_sync(0xffffffffu, x, 16);
+                float x = sum_of_rows(l[n][i]);
                 const int r = n * 8 + tq * 2 + i;
                 if (gq == 0)
                     sm.ml[warp][r] = make_float2(m[n][i], x);
@@ -823,6 +899,20 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                         *(float4 *)&sm.o[warp][r][gq * VB + 2 * j] = make_float4(o[n][j][i], o[n][j][i + 2], o[n][j + 1][i], o[n][j + 1][i + 2]);
                 }
             }
+        if (apart) {  // O to units of 2^N, N raised by the sum's exponent: O is then a mean of values
+            __syncwarp();
+            for (int r = 0; r < u.nrows; ++r) {
+                const float2 alone = sm.alone[warp][r], ml = sm.ml[warp][r];
+                const int e = alone.y > 0.f && alone.y < INFINITY ? (int)(__float_as_uint(alone.y) >> 23) - 127 : 0;
+                const float top = alone.x + (float)e, f = exp2f(fminf(ml.x - top, 127.f));
+                __syncwarp();
+                for (int d = lane; d < D; d += 32)
+                    sm.o[warp][r][d] *= f;
+                if (lane == 0)  // (the other sum is 0, or a NaN that its row keeps)
+                    sm.ml[warp][r] = make_float2(top, ml.y + alone.y * __uint_as_float((uint32_t)(127 - e) << 23));
+            }
+            __syncwarp();
+        }
         if (nan_seen) {  // (warp-uniform)
             __syncwarp();
             for (int x = lane; x < u.nrows * D; x += 32)

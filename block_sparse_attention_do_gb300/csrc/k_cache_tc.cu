@@ -2,7 +2,8 @@
 // paged 8-bit cache on the tcgen05 tensor cores; bf16 queries, D = 64 or 128.
 //
 // The formulas are those of k_cache_attn.cu (scales of a page's values in the
-// exponent, running maximum raised only when a weight would pass 2^10).  Here
+// exponent, running maximum raised only when a weight would pass 2^10, the sum
+// taken from the scores alone from a page of far values on).  Here
 // the products bound the time: 4 D operations per query row and key, so each
 // code is converted once for 256 rows and the conversion leaves the critical
 // path to warps of its own:
@@ -71,7 +72,7 @@ template <int D> struct Layout {
     static constexpr int kHalf = 128 * 128;                // one half of 128 rows
     static constexpr int kTile = kHalves * kHalf;          // 128 rows x D halves
     static constexpr int q = 0, k = 2 * kTile, v = k + kStages * kTile;
-    static constexpr int scales = v + kStages * kTile;     // float4 [kScaleRing][8]
+    static constexpr int scales = v + kStages * kTile;     // float4 [kScaleRing][8]: k scale, log2 and reciprocal of the v scale, 1 if the tile has one far from 1
     static constexpr int bars = scales + kScaleRing * 8 * 16;
     static constexpr int misc = bars + B_COUNT * 8;        // wait context, tensor memory address, NaN flag
     static constexpr int total = misc + 32 + 1024;         // and room to align
@@ -220,7 +221,8 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
             fence_async_smem();
             mbar_arrive(&bars[B_Q]);
         }
-        float m = kNoMax, l = 0.f;
+        float m = kNoMax, l = 0.f, N = 0.f;
+        bool apart = false;  // (uniform over the CTA) l is in units of 2^N, else of 2^m
         bool ok = true;
         for (int i = 0; i < ntiles; ++i) {
             const int j = j0 + i;
@@ -261,10 +263,40 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
                 top = fmaxf(top, fmaf(fmaxf(max3(y[0], y[1], y[2]), y[3]), f[n].x, f[n].y));
             }
             const bool raise = top > m + kLazy;  // (no column attended: top is -infinity)
-            if (__any_sync(0xffffffffu, raise)) {
+            if (__any_sync(0xffffffffu, raise || apart || f[0].w != 0.f)) {
+                if (apart || f[0].w != 0.f) {  // the sum by the scores alone, here and from here on
+                    if (!apart)
+                        N = m;
+                    apart = true;
+#pragma unroll 1
+                    for (int pass = 0; pass < 2; ++pass) {  // their maximum, then their sum
+                        float y = N;
+#pragma unroll 1
+                        for (int cc = 0; cc < kTileKeys; cc += 16) {  // (of one page)
+                            uint32_t a[16];
+                            tmem_ld16(s_at + cc, a);
+                            tmem_wait_ld();
+                            const float4 page = sc[cc / BS];
+                            const float mul = fmaxf(page.x * qmul, kTiny);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float x = fmaf(__uint_as_float(a[e]), mul, pass ? -N : 0.f);
+                                // (a page that is not in the pool has no keys)
+                                if (page.z != 0.f && cc + e <= cmax && cc + e >= cmin) {
+                                    if (pass)
+                                        l += ex2(x);
+                                    else
+                                        y = fmaxf(y, x);
+                                }
+                            }
+                        }
+                        l *= pass ? 1.f : ex2(N - y);
+                        N = y;
+                    }
+                }
                 const float mn = raise ? top : m, f = ex2(m - mn);
                 m = mn;
-                l *= f;
+                l *= apart ? 1.f : f;
                 if (i > 0) {  // (S_q of this tile follows P_q V of the last one: O_q is at rest)
 #pragma unroll 1
                     for (int cc = 0; cc < D; cc += 16) {
@@ -286,7 +318,11 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
 #pragma unroll
                 for (int n = 0; n < (PAGES + 1) / 2; ++n) {
                     constexpr int COLS = BS < 64 ? BS : 64;
-                    const float4 fn = f[hf * (PAGES / 2) + n];
+                    float4 fn = f[hf * (PAGES / 2) + n];
+                    if (PAGES > 4) {  // (eight pages' scales would not fit the registers beside S)
+                        fn = sc[hf * (PAGES / 2) + n];
+                        fn.x = fmaxf(fn.x * qmul, kTiny);
+                    }
                     const float add = fn.y - m;
                     const uint64_t mul2 = f2(fn.x, fn.x), add2 = f2(add, add);
                     uint64_t sum[2];
@@ -302,7 +338,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
                     }
                     float a0, a1;
                     f2_split(f2_add(sum[0], sum[1]), a0, a1);
-                    l = fmaf(a0 + a1, fn.z, l);
+                    l = fmaf(a0 + a1, apart ? 0.f : fn.z, l);
                 }
                 tmem_st32(s_at + hf * 32, w);
                 tmem_wait_st();
@@ -316,10 +352,18 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
         if (ok) {
             tc_fence_after();
             float f = 1.f;
+            if (apart) {  // O from units of 2^m to those of 2^N, N raised by the sum's exponent: O is then a mean of values
+                const int e = l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0;
+                N += (float)e;
+                l *= __uint_as_float((uint32_t)(127 - e) << 23);
+                f = exp2f(fminf(m - N, 127.f));
+                m = N;
+            }
             if (p.sinks && have) {
                 const float sk = p.sinks[h] * 1.4426950408889634f, mn = fmaxf(m, sk);
-                f = ex2(m - mn);
-                l = l * f + ex2(sk - mn);
+                const float down = ex2(m - mn);
+                f *= down;
+                l = l * down + ex2(sk - mn);
                 m = mn;
             }
             const bool some = l > 0.f || l != l;
@@ -446,9 +490,11 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
         for (int i = 0; i < ntiles; ++i) {
             const int j = j0 + i, s = i % kStages;
             // (a page that is not in the pool gets weight 0)
-            if (cw == 0 && lane < npages) {
-                const float vsc = fmaxf(vs, kScaleFloor);
-                scales[(i & (kScaleRing - 1)) * 8 + lane] = id >= 0 ? make_float4(ks, log2f(vsc), 1.f / vsc, 0.f) : make_float4(1.f, -INFINITY, 0.f, 0.f);
+            if (cw == 0) {
+                const float vsc = fmaxf(vs, kScaleFloor), lvs = log2f(vsc);
+                const bool far = __any_sync(0xffffffffu, id >= 0 && fabsf(lvs) > kNearScale);
+                if (lane < npages)
+                    scales[(i & (kScaleRing - 1)) * 8 + lane] = id >= 0 ? make_float4(ks, lvs, 1.f / vsc, far ? 1.f : 0.f) : make_float4(1.f, -INFINITY, 0.f, far ? 1.f : 0.f);
             }
             if (values && masked(j)) {
                 // a NaN value must not meet the weight 0 of a row that does

@@ -705,6 +705,45 @@ def test_chunk_form_scales_and_bad_pages():
     assert api.get_error(ws) == 0
 
 
+def far_values(*scales):
+    """Pages in turn: zeros (the scale that append gives them), then values of each scale."""
+    def edit(cache):
+        n = len(scales) + 1
+        cache.v_scale[::n] = 2.0 ** -100
+        cache.v.view(torch.uint8)[::n] = 0
+        for i, s in enumerate(scales):
+            cache.v_scale[i + 1::n] = s
+    return edit
+
+
+SPREAD = (2.0 ** 27, 2.0 ** 60, 1.0, 2.0 ** -60, 2.0 ** 100, 2.0 ** -90)
+
+
+@pytest.mark.parametrize("scales,kw", [((2.0 ** 27,), dict()), ((2.0 ** 60,), dict(sinks=True)), ((2.0 ** 41, 2.0 ** -41), dict(window=200)),
+                                       ((1.0,), dict()), (SPREAD, dict(S=9)), (SPREAD, dict())])
+@pytest.mark.parametrize("form,dtype,G,D,bs", [
+    ("cache_attn_cluster", BF, 4, 128, 64), ("cache_attn_cluster", F32, 12, 64, 32), ("cache_attn_cluster", BF, 20, 32, 16),
+    ("cache_attn", BF, 4, 128, 16), ("cache_attn", F32, 3, 128, 64), ("cache_attn", BF, 12, 128, 64), ("cache_attn", F32, 20, 64, 32)])
+def test_values_of_zero_beside_large_ones(scales, kw, form, dtype, G, D, bs):
+    """Every page counts in the denominator, however far apart its values' scale lies (a page of zeros beside one of
+    large values, ordinary scores): O and LSE by each form of the attention."""
+    if form == "cache_attn_cluster":
+        lens, cols = [900, 65, 300], None
+    else:
+        g = np.random.default_rng(3)
+        lens = [int(n) for n in g.integers(1, 250, 110 if "S" not in kw else 460)]
+        cols = 9000 * 128 // (bs * D) if "window" not in kw else 4000 * 128 // (bs * D)
+    kw = dict(kw, window=3500) if form == "cache_attn" and "window" in kw else kw  # (many keys in reach: the list form)
+    takes(form, lens, [1] * len(lens), 2 * G, 2, D, bs, dtype, cols=cols, edit=far_values(*scales), **kw)
+
+
+@pytest.mark.parametrize("scales,kw", [((2.0 ** 27,), dict()), ((2.0 ** 60,), dict(window=70, sinks=True)), (SPREAD, dict()),
+                                       (SPREAD, dict(window=150))])
+@pytest.mark.parametrize("D,bs", [(128, 64), (128, 16), (64, 32)])
+def test_chunk_form_values_of_zero_beside_large_ones(scales, kw, D, bs):
+    takes("cache_chunk", [700, 300, 40], [260, 300, 40], 16, 8, D, bs, BF, ragged=True, edit=far_values(*scales), **kw)
+
+
 def test_chunk_form_leaves_rows_behind_the_last_sequence():
     cache = filled([400, 300], 8, 64, 32, 1)
     cu = torch.tensor([0, 300, 600], dtype=torch.int32, device=DEV)
