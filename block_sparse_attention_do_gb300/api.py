@@ -593,7 +593,8 @@ class KVCache:
     (None: the caller manages pages itself; no reserve, free, fork or
     compact).  The cache keeps their addresses: they are written in place,
     never replaced.  `ws` is the workspace of the calls that change the cache;
-    get_error(cache.ws) reads what the last of them found."""
+    get_error(cache.ws) reads what the last of them found.  `fwd_ws` is the
+    last cache_fwd's workspace (None: it had none), for get_error too."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table, seq_lens, refcount=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.float8_e4m3fn,
@@ -622,6 +623,7 @@ class KVCache:
         if n == 0:
             raise NsaError(1, "nsa_cache_workspace_size")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+        self.fwd_ws = None
         self._problems = {}
 
     def problem(self, x, S, scale, cu_seqlens, max_seqlen, selection, query):
@@ -771,7 +773,9 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     each token's latest keys, with `block_idx` the selected blocks; `sinks` as
     for sel_fwd.  Returns (o, lse).  A ws of the caller's
     (nsa_cache_fwd_workspace_size) holds the error word that get_error reads;
-    without one each call has its own, and bad entries are left out unreported."""
+    without one each call has its own, cache.fwd_ws, except a few short rows'
+    (the clustered form): that checks its entries only with a ws of the
+    caller's, and else leaves bad ones out unreported."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_fwd(q, cache, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)
@@ -797,6 +801,7 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
     lse = torch.empty(stats, dtype=torch.float32, device=dev)
     if ws is None and n > 256:
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    cache.fwd_ws = ws
     at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check(lib().nsa_cache_fwd(p, cache.ref, int(window or 0), None if cu_seqlens is None else cu_seqlens.data_ptr(),
                                None if block_idx is None else block_idx.data_ptr(), None if sinks is None else sinks.data_ptr(),

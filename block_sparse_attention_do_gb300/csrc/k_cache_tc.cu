@@ -65,6 +65,7 @@ struct Params {
     int *err;
     int tiles;    // row tiles of the longest sequence
     int wait_us;  // bounded-wait limit in microseconds (0: the default)
+    int stall;    // self-test: the S-product issuers stay idle (see wait_test)
 };
 
 template <int D> struct Layout {
@@ -349,73 +350,73 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
         // ---- O / l
         if (ok && ntiles > 0)
             ok = mbar_wait_warp(&bars[B_O], 0, ctx);
-        if (ok) {
-            tc_fence_after();
-            float f = 1.f;
-            if (apart) {  // O from units of 2^m to those of 2^N, N raised by the sum's exponent: O is then a mean of values
-                const int e = l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0;
-                N += (float)e;
-                l *= __uint_as_float((uint32_t)(127 - e) << 23);
-                f = exp2f(fminf(m - N, 127.f));
-                m = N;
-            }
-            if (p.sinks && have) {
-                const float sk = p.sinks[h] * 1.4426950408889634f, mn = fmaxf(m, sk);
-                const float down = ex2(m - mn);
-                f *= down;
-                l = l * down + ex2(sk - mn);
-                m = mn;
-            }
-            const bool some = l > 0.f || l != l;
-            f = some ? f / l : 0.f;
-            // values that were NaN in tiles that some rows attend in part
-            // were taken as 0 there: put them back for the rows that attend them
-            uint32_t nan_dim[D / 32];
+        if (!ok)  // a wait gave up: NaN in the rows, which are not finished, whether it is reported or not
+            l = __int_as_float(0x7fffffff);
+        tc_fence_after();
+        float f = 1.f;
+        if (apart) {  // O from units of 2^m to those of 2^N, N raised by the sum's exponent: O is then a mean of values
+            const int e = l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0;
+            N += (float)e;
+            l *= __uint_as_float((uint32_t)(127 - e) << 23);
+            f = exp2f(fminf(m - N, 127.f));
+            m = N;
+        }
+        if (p.sinks && have) {
+            const float sk = p.sinks[h] * 1.4426950408889634f, mn = fmaxf(m, sk);
+            const float down = ex2(m - mn);
+            f *= down;
+            l = l * down + ex2(sk - mn);
+            m = mn;
+        }
+        const bool some = l > 0.f || l != l;
+        f = some ? f / l : 0.f;
+        // values that were NaN in tiles that some rows attend in part
+        // were taken as 0 there: put them back for the rows that attend them
+        uint32_t nan_dim[D / 32];
 #pragma unroll
-            for (int x = 0; x < D / 32; ++x)
-                nan_dim[x] = 0;
-            if (*nan_seen && have) {
+        for (int x = 0; x < D / 32; ++x)
+            nan_dim[x] = 0;
+        if (*nan_seen && have) {
 #pragma unroll 1
-                for (int key = max(key_first, g.window > 0 ? pos - g.window + 1 : 0); key <= pos; ++key) {
-                    if (!masked(key / kTileKeys)) {
-                        key |= kTileKeys - 1;
-                        continue;
-                    }
-                    const int page = c.table[(int64_t)b * c.cols + (key / BS)];
-                    if (page < 0 || page >= c.pages)
-                        continue;
-                    const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (BS - 1)) * c.st;
+            for (int key = max(key_first, g.window > 0 ? pos - g.window + 1 : 0); key <= pos; ++key) {
+                if (!masked(key / kTileKeys)) {
+                    key |= kTileKeys - 1;
+                    continue;
+                }
+                const int page = c.table[(int64_t)b * c.cols + (key / BS)];
+                if (page < 0 || page >= c.pages)
+                    continue;
+                const uint8_t *v = c.v + (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (BS - 1)) * c.st;
 #pragma unroll
-                    for (int x = 0; x < D / 4; ++x) {
-                        const uint32_t u = ((const uint32_t *)v)[x] & 0x7f7f7f7fu, hit = (u + 0x01010101u) & 0x80808080u;
-                        // bits 7, 15, 23, 31 to dimensions 4 x ..
-                        nan_dim[x / 8] |= ((hit >> 7 & 1u) | (hit >> 14 & 2u) | (hit >> 21 & 4u) | (hit >> 28 & 8u)) << (x % 8 * 4);
-                    }
+                for (int x = 0; x < D / 4; ++x) {
+                    const uint32_t u = ((const uint32_t *)v)[x] & 0x7f7f7f7fu, hit = (u + 0x01010101u) & 0x80808080u;
+                    // bits 7, 15, 23, 31 to dimensions 4 x ..
+                    nan_dim[x / 8] |= ((hit >> 7 & 1u) | (hit >> 14 & 2u) | (hit >> 21 & 4u) | (hit >> 28 & 8u)) << (x % 8 * 4);
                 }
             }
-            __nv_bfloat16 *dst = p.o + (have ? o_off(g, b, h, t) : 0);
+        }
+        __nv_bfloat16 *dst = p.o + (have ? o_off(g, b, h, t) : 0);
 #pragma unroll
-            for (int cc = 0; cc < D; cc += 32) {
-                uint32_t a[32];
-                if (ntiles > 0) {
-                    tmem_ld32(lanes + TM_O + q * 128 + cc, a);
-                    tmem_wait_ld();
-                }
-                uint32_t w[16];
+        for (int cc = 0; cc < D; cc += 32) {
+            uint32_t a[32];
+            if (ntiles > 0) {
+                tmem_ld32(lanes + TM_O + q * 128 + cc, a);
+                tmem_wait_ld();
+            }
+            uint32_t w[16];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float y0 = nan_dim[cc / 32] >> (2 * e) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e]) * f;
-                    const float y1 = nan_dim[cc / 32] >> (2 * e + 1) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e + 1]) * f;
-                    w[e] = some && ntiles > 0 ? pack_bf16(y0, y1) : 0u;
-                }
-                if (have)
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *(uint4 *)(dst + cc + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+            for (int e = 0; e < 16; ++e) {
+                const float y0 = nan_dim[cc / 32] >> (2 * e) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e]) * f;
+                const float y1 = nan_dim[cc / 32] >> (2 * e + 1) & 1u ? __uint_as_float(0x7fffffffu) : __uint_as_float(a[2 * e + 1]) * f;
+                w[e] = some && ntiles > 0 ? pack_bf16(y0, y1) : 0u;
             }
             if (have)
-                p.lse[stat_off(g, b, h, t)] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 16; e += 4)
+                    *(uint4 *)(dst + cc + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
         }
+        if (have)
+            p.lse[stat_off(g, b, h, t)] = some ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
     } else if (warp < kSoftmaxWarps + kConvWarps) {
         // ------------------------------------------------------- converters
         // Two warps take a tile's keys, two its values: a warp half of the
@@ -567,7 +568,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
             // The warps take turns: a turn is P_q V and the next S_q, so that
             // one tile's softmax lies under the other's products (left to
             // themselves the two fall into step: 449 us for 389).
-            bool ok = ntiles > 0 && mbar_wait_warp(&bars[B_Q], 0, ctx) && mbar_wait_warp(&bars[B_KF], 0, ctx);
+            bool ok = !p.stall && ntiles > 0 && mbar_wait_warp(&bars[B_Q], 0, ctx) && mbar_wait_warp(&bars[B_KF], 0, ctx);
             if (ok) {
                 fence_async_smem();  // the converters' writes, for the tensor cores
                 tc_fence_after();
@@ -654,6 +655,7 @@ cudaError_t launch_cache_chunk(const Geo &g, const Cache &c, const void *q, cons
     p.err = err;
     p.tiles = (int)((longest_rows(g) + kTileRows - 1) / kTileRows);
     p.wait_us = wait_test().wait_us;
+    p.stall = wait_test().kernel == WAIT_TEST_FWD;
     void (*const kernels[2][3])(const Params) = {{cache_chunk_kernel<64, 16>, cache_chunk_kernel<64, 32>, cache_chunk_kernel<64, 64>},
                                                  {cache_chunk_kernel<128, 16>, cache_chunk_kernel<128, 32>, cache_chunk_kernel<128, 64>}};
     auto kernel = kernels[g.D == 128][c.bsh - 4];

@@ -10,7 +10,8 @@ namespace nsa {
 
 // Self-test of the tensor-core kernels' bounded waits (nsa_debug_stall): the
 // kernel whose S-product issuer stays idle, so that its first wait on S runs
-// out, and the wait limit of every tensor-core kernel in microseconds
+// out (FWD: nsa_cache_fwd's chunk form too), and the wait limit of every
+// tensor-core kernel in microseconds
 // (0: the default).  Both 0 in normal operation.
 enum { WAIT_TEST_NONE = 0, WAIT_TEST_FWD = 1, WAIT_TEST_DKDV = 2, WAIT_TEST_DQ = 3 };
 struct WaitTest {

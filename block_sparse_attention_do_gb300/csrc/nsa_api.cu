@@ -1323,7 +1323,8 @@ size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *pc, i
     const bool thd = p->layout == NSA_LAYOUT_THD;
     if (cache_geo(p, &shape, thd ? kFakeCuQ : nullptr, selection != 0, 0, g, c) != NSA_OK)
         return 0;
-    return cache_chunk_supported(g, p->dtype, selection != 0) ? kAlign : cache_attn_ws_bytes(g, c, selection != 0);
+    // (the chunk form needs no more than the error word, 256 bytes: a size of its own tells its callers that waits may give up)
+    return cache_chunk_supported(g, p->dtype, selection != 0) ? 2 * kAlign : cache_attn_ws_bytes(g, c, selection != 0);
 }
 
 nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *pc, int32_t window, const int32_t *cu_seqlens,

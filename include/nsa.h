@@ -362,7 +362,7 @@ nsa_status nsa_build_inverse_index_noalloc(const nsa_problem *p, const int32_t *
  * memory, and report NSA_ERR_DEVICE_TIMEOUT through the workspace error word,
  * leaving the CUDA context usable.  nsa_debug_stall(kernel, wait_limit_us)
  * lets a test run that path without any fault: while `kernel` is 1 (the
- * forward), 2 (the dK/dV kernel) or 3 (the dQ kernel), that kernel is
+ * forward, and the chunk form of nsa_cache_fwd), 2 (the dK/dV kernel) or 3 (the dQ kernel), that kernel is
  * launched with the thread that issues its S = Q K^T products idle, so the
  * first wait on S runs out; `wait_limit_us` (1 .. 2000000; 0 = the default
  * of 2 s) replaces the limit of every tensor-core kernel's waits.
@@ -526,9 +526,12 @@ nsa_status nsa_cache_append(const nsa_problem *p, const nsa_cache *c, const int3
  * backward, past the tensor or beyond T tokens: that is reported) are left as
  * they were.  p->B = rows, p->Hkv, D and block_size the cache's,
  * p->kv_stride unused.  `selection`: whether block_idx will be given.
- * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).  A call that
- * needs a workspace of 256 bytes needs it for the error word alone: its ws may
- * be NULL, and errors are then not reported.
+ * Without an index B is at most 8192 (else NSA_ERR_UNSUPPORTED).  A call whose
+ * workspace size is 256 or 512 bytes uses 256 of them, for the error word
+ * alone: its ws may be NULL, and errors are then not reported.  512: a call on
+ * the tensor cores (chunks of prompts), whose bounded waits may give up
+ * (NSA_ERR_DEVICE_TIMEOUT); rows that were not finished then hold NaN, with or
+ * without a ws.
  */
 size_t nsa_cache_fwd_workspace_size(const nsa_problem *p, const nsa_cache *c, int32_t selection);
 nsa_status nsa_cache_fwd(const nsa_problem *p, const nsa_cache *c, int32_t window, const int32_t *cu_seqlens,

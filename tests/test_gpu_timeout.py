@@ -78,3 +78,41 @@ def test_wait_runs_out_reports_timeout_and_recovers(kernel):
     assert api.get_error(ws) == 0  # reading clears it
     # the same stream and context, normal operation: parity with the oracle
     _check_normal(cpu, g, bs, ws_f, ws_b)
+
+
+def _chunks(seed):
+    g = np.random.default_rng(seed)
+    cache = api.make_cache(64, 8, 128, 64, 2, 20, device=DEV)
+    new = torch.tensor([500, 300], dtype=torch.int32, device=DEV)
+    api.cache_reserve(cache, new)
+    mk = lambda H: torch.tensor(g.normal(size=(800, H, 128)), dtype=torch.float32).to(torch.bfloat16).to(DEV)  # noqa: E731
+    cu = torch.tensor([0, 500, 800], dtype=torch.int32, device=DEV)
+    api.cache_append(cache, mk(8), mk(8), cu_seqlens=cu, max_seqlen=500)
+    return mk(16), cache, dict(cu_seqlens=cu, max_seqlen=500)
+
+
+def test_a_chunk_over_the_cache_reports_its_timeout():
+    """nsa_cache_fwd's tensor-core form, called without a workspace: the unfinished rows hold NaN, the call's own error
+    word tells, and the next call is right."""
+    q, cache, kw = _chunks(5)
+    want = api.cache_fwd(q, cache, **kw)
+    torch.cuda.synchronize()
+    assert api.get_error(cache.fwd_ws) == 0 and not torch.isnan(want[0]).any()
+    api.debug_stall(1, 5000)  # 5 ms waits
+    try:
+        api.trace_enable(8)
+        got = api.cache_fwd(q, cache, **kw)
+        torch.cuda.synchronize()  # the launch returned: every wait ended
+        assert [name for name, _ in api.trace_records()] == ["cache_chunk"]
+    finally:
+        api.trace_enable(0)
+        api.debug_stall(0, 0)
+    assert torch.isnan(got[0]).all() and torch.isnan(got[1]).all()
+    assert api.get_error(cache.fwd_ws) == TIMEOUT
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    again = api.cache_fwd(q, cache, ws=ws, **kw)
+    assert all(torch.equal(a, b) for a, b in zip(want, again))
+    assert api.get_error(ws) == 0 and cache.fwd_ws is ws
+    # a single token takes the form that has no wait, and no word of its own
+    api.cache_fwd(q[:2].view(2, 16, 1, 128), cache)
+    assert cache.fwd_ws is None
