@@ -161,9 +161,9 @@ __device__ __forceinline__ void load_piece(const Cache &c, int r, int col0, int 
     }
 }
 
-// Gives back a piece of the pages of row r: true if an entry names no page or
-// a page that nobody holds.
-__device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, int lane, bool clear)
+// Gives back a piece of the pages of row r and empties it: true if an entry
+// names no page or a page that nobody holds.
+__device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, int lane)
 {
     int p[kBatch], was[kBatch];
     load_piece(c, r, col0, lane, p);
@@ -179,7 +179,7 @@ __device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, i
                 atomicAdd(c.ref + p[u], 1);
         }
         const int col = col0 + u * 32 + lane;
-        if (clear && col < c.cols)
+        if (col < c.cols)
             c.table[(int64_t)r * c.cols + col] = -1;
     }
     return bad;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads)
             bad = true;
             return;
         }
-        bad |= release_piece(c, r, col0, w.lane, true);
+        bad |= release_piece(c, r, col0, w.lane);
         if (col0 == 0 && w.lane == 0)
             c.lens[r] = 0;
     });
@@ -357,7 +357,14 @@ __global__ void __launch_bounds__(kThreads)
         return;  // the same in every CTA: nothing has changed
     // the destinations' own pages come back first: a tail may reuse them (an
     // error here: more table entries name a page than its count says)
-    for_pieces(c, w, n, [&](int i, int col0) { bad |= release_piece(c, dst[i], col0, w.lane, false); });
+    for_pieces(c, w, n, [&](int i, int col0) {
+        int p[kBatch];
+        load_piece(c, dst[i], col0, w.lane, p);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u)
+            if (p[u] >= 0)
+                bad |= atomicSub(c.ref + p[u], 1) <= 0;
+    });
     cl.sync();  // every thread has read ws.err: it may be written again
     if (bad)
         set_error(ws.err, NSA_ERR_BAD_INDEX);
@@ -372,7 +379,8 @@ __global__ void __launch_bounds__(kThreads)
     const int64_t tails = tails_all;
     int before, free;
     scan_counts(counts, w, before, free);
-    if (tails > free) {  // undo: nothing has changed
+    // (a thread that reads the word late may find CACHE_FULL there: the same)
+    if (tails > free || __ldcg(ws.err) != NSA_OK) {  // undo: nothing has changed
         for_pieces(c, w, n, [&](int i, int col0) {
             int p[kBatch];
             load_piece(c, dst[i], col0, w.lane, p);
@@ -382,7 +390,7 @@ __global__ void __launch_bounds__(kThreads)
                     atomicAdd(c.ref + p[u], 1);
         });
         if (w.rank == 0 && threadIdx.x == 0)
-            *ws.err = NSA_ERR_CACHE_FULL;
+            set_error(ws.err, NSA_ERR_CACHE_FULL);
         return;
     }
     take_free(c, run, w.lane, before, (int)tails, ws.p2);

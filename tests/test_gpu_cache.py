@@ -990,6 +990,22 @@ def test_page_lists_are_checked():
     same_meta(cache, plain)
 
 
+@pytest.mark.parametrize("spare", [0, 5])
+def test_a_fork_over_miscounted_pages_changes_nothing(spare):
+    """The destinations' entries name a page more often than its count says: found only when they are given back."""
+    for entries, count in (((0, 0), 1), ((0, 1, 0), 2), ((2, 2, 2), 2)):
+        cache = filled([40, 48, 48, 48], 1, 32, 16, 3, spare=spare, garbage=False)
+        for row in (2, 3):
+            for col, e in enumerate(entries):
+                cache.page_table[row, col] = cache.page_table[2, e].clone()
+        cache.refcount[cache.page_table[2, entries[0]].long()] = count
+        plain = Plain(cache)
+        api.cache_fork(cache, i32(0, 1), i32(2, 3))
+        assert api.get_error(cache.ws) == 3
+        same_meta(cache, plain)
+        same_pool(cache, plain)
+
+
 def test_a_full_pool_changes_nothing():
     cache = filled([40, 20, 0, 33], 1, 32, 16, 3, spare=1, cols=8, garbage=False)
     plain = Plain(cache)
