@@ -696,8 +696,9 @@ def _cu(cache, cu_seqlens, max_seqlen):
 
 def cache_reserve(cache, n_new, stream=None):
     """Row b of the cache grows by n_new[b] tokens (int32 [rows]): pages from
-    the pool, lowest ids first, and seq_lens.  All rows or, with too few free
-    pages (NSA_ERR_CACHE_FULL in cache.ws), none."""
+    the pool, lowest ids first, and seq_lens; pages that it holds there already
+    (its length was lowered: rejected drafts) are used again.  All rows or, with
+    too few free pages (NSA_ERR_CACHE_FULL in cache.ws), none."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_reserve(cache, n_new)

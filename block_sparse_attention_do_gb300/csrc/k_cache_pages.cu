@@ -86,8 +86,8 @@ __device__ __forceinline__ void scan_counts(const int *counts, const Where &w, i
     total = __reduce_add_sync(0xffffffffu, t);
 }
 
-// Exclusive prefix over i < n of need(i), by one CTA: out[i], the sum
-// returned to every thread.
+// Exclusive prefix over i < n of need(i), by one CTA: out[i] (if given), the
+// sum returned to every thread.
 template <typename F> __device__ int64_t cta_prefix(int n, int *out, F need)
 {
     __shared__ int64_t part[kWarps];
@@ -109,7 +109,7 @@ template <typename F> __device__ int64_t cta_prefix(int n, int *out, F need)
             before += k < warp ? part[k] : 0;
             all += part[k];
         }
-        if (i < n)
+        if (out && i < n)
             out[i] = (int)min(before + incl - x, (int64_t)INT32_MAX);
         base = all;
         __syncthreads();
@@ -186,6 +186,34 @@ __device__ __forceinline__ bool release_piece(const Cache &c, int r, int col0, i
 }
 
 // ---- reserve: row b grows by n_new[b] tokens; all rows or none ------------
+// The columns that row b grows into; false where it cannot.
+__device__ __forceinline__ bool grown_columns(const Cache &c, const int *n_new, int b, int &have, int &want)
+{
+    const int len = c.lens[b], n = n_new[b];
+    const bool ok = n >= 0 && len >= 0 && (int64_t)len + n <= (int64_t)c.cols * c.bs;
+    have = ok ? blocks_of(len, c) : 0;
+    want = ok ? blocks_of(len + n, c) : 0;
+    return ok;
+}
+
+// How many of columns [have, want) of row b hold a page already; -1 where one
+// holds what is no page in use.  (The whole warp.)
+__device__ __forceinline__ int held_columns(const Cache &c, int b, int have, int want, int lane)
+{
+    int held = 0;
+    bool none = false;
+#pragma unroll 4
+    for (int col = have + lane; col < want; col += 32) {
+        const int p = c.table[(int64_t)b * c.cols + col];
+        held += p != -1;
+        if (p != -1)
+            none |= p < 0 || p >= c.pages || c.ref[p] <= 0;
+    }
+    none = __any_sync(0xffffffffu, none);
+    held = __reduce_add_sync(0xffffffffu, held);
+    return none ? -1 : held;
+}
+
 __global__ void __launch_bounds__(kThreads)
     cache_reserve_kernel(const Cache c, const int *n_new, const CacheWs ws)
 {
@@ -193,29 +221,37 @@ __global__ void __launch_bounds__(kThreads)
     dependency_wait();
     cg::cluster_group cl = cg::this_cluster();
     __shared__ int counts[kMaxCluster * kWarps];
-    __shared__ int bad;
+    __shared__ int bad, kept;
     __shared__ int64_t need_all;
     const Where w = where(cl);
     if (threadIdx.x == 0)
-        bad = 0;
+        bad = kept = 0;
     cl.sync();  // every CTA of the cluster runs from here on: its shared memory may be written
-    auto ok = [&](int b) {
-        const int len = c.lens[b], n = n_new[b];
-        return n >= 0 && len >= 0 && (int64_t)len + n <= (int64_t)c.cols * c.bs;
-    };
-    auto need = [&](int b) {
-        const int len = c.lens[b], n = n_new[b];
-        return ok(b) ? blocks_of(len + n, c) - blocks_of(len, c) : 0;
-    };
-    // every CTA checks every row and knows the sum; CTA 0 writes the offsets
-    for (int b = threadIdx.x; b < c.rows; b += kThreads)
-        if (!ok(b))
-            bad = 1;
+    // every CTA checks every row and knows the sum; CTA 0 writes the offsets.
+    // A row whose length was lowered holds a page in the first column that it
+    // grows into (the read of a thread's first row is under way with the counts)
+    int in_first = -1;
+    bool none = false, held = false;
+#pragma unroll 4
+    for (int b = threadIdx.x; b < c.rows; b += kThreads) {
+        int have, want;
+        held |= in_first != -1;
+        none |= !grown_columns(c, n_new, b, have, want);
+        in_first = want > have ? c.table[(int64_t)b * c.cols + have] : -1;
+    }
+    if (none)
+        bad = 1;
     const Runs run(c, w);
     share_count(cl, counts, w, run.count(w.lane, [&](int p) { return c.ref[p] <= 0; }));
+    if (held || in_first != -1)
+        kept = 1;
     int64_t total;
     if (w.rank == 0) {
-        total = cta_prefix(c.rows, ws.r1, need);
+        total = cta_prefix(c.rows, ws.r1, [&](int b) {
+            int have, want;
+            grown_columns(c, n_new, b, have, want);
+            return want - have;
+        });
         if (threadIdx.x < w.ctas)
             *cl.map_shared_rank(&need_all, threadIdx.x) = total;
     }
@@ -223,6 +259,22 @@ __global__ void __launch_bounds__(kThreads)
     total = need_all;
     int before, free;
     scan_counts(counts, w, before, free);
+    if (kept && !bad) {  // off the common path: what each row lacks (-1: it cannot grow)
+        for (int b = w.warp; b < c.rows; b += w.warps) {
+            int have, want;
+            grown_columns(c, n_new, b, have, want);
+            const int held = held_columns(c, b, have, want, w.lane);
+            if (w.lane == 0)
+                ws.r0[b] = held < 0 ? -1 : want - have - held;
+        }
+        cl.sync();
+        total = cta_prefix(c.rows, w.rank == 0 ? ws.r1 : nullptr, [&](int b) {
+            const int lacks = __ldcg(ws.r0 + b);
+            if (lacks < 0)
+                bad = 1;
+            return max(lacks, 0);
+        });
+    }
     const bool full = total > free;
     if (w.rank == 0 && threadIdx.x == 0)
         *ws.err = bad ? NSA_ERR_BAD_INDEX : full ? NSA_ERR_CACHE_FULL : NSA_OK;
@@ -233,9 +285,20 @@ __global__ void __launch_bounds__(kThreads)
     for (int b = w.warp; b < c.rows; b += w.warps) {
         const int len = c.lens[b], n = n_new[b];
         const int have = blocks_of(len, c), want = blocks_of(len + n, c), off = __ldcg(ws.r1 + b);
+        int *row = c.table + (int64_t)b * c.cols;
+        if (!kept) {
 #pragma unroll 4
-        for (int col = have + w.lane; col < want; col += 32)
-            c.table[(int64_t)b * c.cols + col] = __ldcg(ws.p2 + off + col - have);
+            for (int col = have + w.lane; col < want; col += 32)
+                row[col] = __ldcg(ws.p2 + off + col - have);
+        } else
+            for (int col0 = have, nth = off; col0 < want; col0 += 32) {  // the empty columns
+                const int col = col0 + w.lane;
+                const bool empty = col < want && row[col] == -1;
+                const unsigned m = __ballot_sync(0xffffffffu, empty);
+                if (empty)
+                    row[col] = __ldcg(ws.p2 + nth + __popc(m & ((1u << w.lane) - 1u)));
+                nth += __popc(m);
+            }
         __syncwarp();
         if (w.lane == 0)
             c.lens[b] = len + n;

@@ -429,7 +429,9 @@ nsa_status nsa_select_topk(const nsa_problem *p, const int32_t *cu_seqlens, cons
  *   page_table [rows, max_pages] int32: row b's blocks in order, -1 behind
  *              them.  A row is one sequence (a batch entry of the calls below)
  *   seq_lens   [rows] int32: tokens of each row, NEW TOKENS INCLUDED: reserve
- *              first, then append, then attend
+ *              first, then append, then attend.  The caller may lower a length
+ *              (tokens that were drafted and rejected): the row keeps the pages
+ *              behind it until it grows into them again or is freed
  *   refcount   [num_pages] int32: table entries that name each page; 0: free
  *
  * All of it is the caller's device memory; the calls change it on `stream`,
@@ -465,9 +467,10 @@ typedef struct nsa_cache {
  * (256-byte aligned, any contents; 0: invalid cache), and choose the lowest
  * free page ids first, so that their results depend on the cache's state alone.
  *  - reserve: row b grows by n_new[b] >= 0 tokens (device int32 [rows]): pages
- *    for them, in the order of rows and columns, and seq_lens.  All rows or
- *    none: NSA_ERR_CACHE_FULL (too few free pages) or NSA_ERR_BAD_INDEX (a
- *    negative count, a row beyond max_pages) changes nothing.
+ *    for them, in the order of rows and columns, and seq_lens.  A column that
+ *    holds a page already keeps it.  All rows or none: NSA_ERR_CACHE_FULL (too
+ *    few free pages) or NSA_ERR_BAD_INDEX (a negative count, a row beyond
+ *    max_pages, a column that holds no page in use) changes nothing.
  *  - free: the n listed rows (device int32) give up their pages and have
  *    length 0.  A row outside the table or listed twice is reported, and
  *    freed once.

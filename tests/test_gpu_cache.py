@@ -990,6 +990,57 @@ def test_page_lists_are_checked():
     same_meta(cache, plain)
 
 
+@pytest.mark.parametrize("pool,rows,cols,bs", [(60, 6, 9, 16), (3000, 300, 9, 32), (9000, 70, 110, 16)])
+def test_lowered_lengths_keep_their_pages(pool, rows, cols, bs):
+    """Drafted tokens that were rejected: the caller lowers a row's length, and the row grows into the pages that it
+    holds.  No page is lost: a page is in use exactly as often as the table names it."""
+    g = np.random.default_rng(pool)
+    cache = api.make_cache(pool, 1, 32, bs, rows, cols)
+    table, lens = np.full((rows, cols), -1, np.int64), np.zeros(rows, np.int64)
+    for step in range(25):
+        grow = np.minimum(g.integers(0, 4 * bs if step % 3 else 9, rows), cols * bs - lens)
+        api.cache_reserve(cache, i32(*grow))
+        used = set(table[table >= 0].tolist())
+        free = iter([p for p in range(pool) if p not in used])
+        missing = [(b, c) for b in range(rows) for c in range(-(-lens[b] // bs), -(-(lens[b] + grow[b]) // bs)) if table[b, c] < 0]
+        if len(missing) > pool - len(used):
+            assert api.get_error(cache.ws) == 7
+        else:
+            assert api.get_error(cache.ws) == 0
+            for b, c in missing:
+                table[b, c] = next(free)
+            lens += grow
+        if step == 12:
+            src, dst = int(lens.argmax()), int(lens.argmin())
+            api.cache_fork(cache, i32(src), i32(dst))
+            assert api.get_error(cache.ws) == 0
+            full, tail = lens[src] // bs, int(lens[src] % bs > 0)
+            table[dst] = -1
+            table[dst, :full] = table[src, :full]
+            if tail:
+                table[dst, full] = min(set(range(pool)) - set(table[table >= 0].tolist()))
+            lens[dst] = lens[src]
+        if step % 8 == 7:
+            gone = g.permutation(rows)[:rows // 3]
+            api.cache_free(cache, i32(*gone))
+            table[gone], lens[gone] = -1, 0
+        assert np.array_equal(cache.page_table.cpu().numpy(), table) and np.array_equal(cache.seq_lens.cpu().numpy(), lens)
+        assert np.array_equal(cache.refcount.cpu().numpy(), np.bincount(table[table >= 0], minlength=pool))
+        lens = np.maximum(lens - g.integers(0, 2 * bs, rows) * (g.random(rows) < 0.7), 0)
+        cache.seq_lens.copy_(torch.tensor(lens, dtype=torch.int32))
+    row = int(lens.argmin())
+    held = cache.page_table[row].clone()
+    col = int(-(-lens[row] // bs))
+    for entry in (-2, pool, 2 ** 31 - 1, next(p for p in range(pool) if p not in set(table[table >= 0].tolist()))):
+        cache.page_table[row, col] = entry
+        before = [x.clone() for x in (cache.page_table, cache.seq_lens, cache.refcount)]
+        api.cache_reserve(cache, i32(*[bs if b == row else 0 for b in range(rows)]))
+        assert api.get_error(cache.ws) == 3
+        for a, b in zip(before, (cache.page_table, cache.seq_lens, cache.refcount)):
+            assert torch.equal(a, b)
+    cache.page_table[row] = held
+
+
 @pytest.mark.parametrize("spare", [0, 5])
 def test_a_fork_over_miscounted_pages_changes_nothing(spare):
     """The destinations' entries name a page more often than its count says: found only when they are given back."""
