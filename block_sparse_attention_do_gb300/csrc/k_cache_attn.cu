@@ -32,7 +32,10 @@
 // e4m3 is a subset of half, so codes convert exactly; q is scaled to half's
 // range by a power of two per row (bf16: exact but for elements 2^-29 below
 // the row's largest; fp32: two halves, 22 bits) and P is rounded to half, 11
-// bits (fp32: two halves).  Sums are fp32.  A CTA's work is a run of pages of
+// bits (fp32: two halves, 22).  A half is exact to 2^-24 and holds 2^15: the row's
+// largest weight is brought to 2^5 .. 2^15 (fp32: 2^13 .. 2^15), so that weights
+// down to 2^-19 (fp32, 22 bits: 2^-16, 2^-38 absolute) of it keep their bits.
+// Sums are fp32.  A CTA's work is a run of pages of
 // the whole call's list of (sequence, kv head, page), cut into equal runs so
 // that long and short sequences load every SM alike; rows whose pages fall to
 // several CTAs are joined by a second kernel, in a fixed order.
@@ -67,7 +70,10 @@ __host__ __device__ constexpr int attn_stages(int nt) { return nt >= 4 ? 4 : 3; 
 constexpr float kNoMax = -1e30f; // running maximum of a row that has seen no key
 constexpr int kMaxRows = 8192;   // sequences of a call without an index (their prefix sits in shared memory)
 constexpr int kNoKey = 0x7f000000; // position of the keys of an entry that is left out
-constexpr float kLazy = 10.f;    // w may reach 2^10 before its row's maximum is raised (half holds 2^15)
+// a row's unit M: its weights may grow from 2^up to 2^kTop (half holds 2^16) before
+// it is raised; fp32 keeps more small ones, and is raised more often
+constexpr float kTop = 15.f;
+__host__ __device__ constexpr float attn_up(bool split) { return split ? 13.f : 5.f; }
 
 // Division of 0 <= n < 2^31 by a number that the host knows: with 2^(l-1) < d
 // <= 2^l and m = floor(2^(31+l) / d) + 1, m d exceeds 2^(31+l) by at most 2^l,
@@ -734,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        raise |= fmaxf(x[n][i], x[n][i + 2]) > m[n][i] + kLazy;
+                        raise |= fmaxf(x[n][i], x[n][i + 2]) > m[n][i] + kTop;
                 if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
@@ -744,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
                             y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
-                            y = fmaxf(y, m[n][i]);
+                            y = fmaxf(y - attn_up(SPLIT), m[n][i]);
                             const float f = exp2f(m[n][i] - y);
                             m[n][i] = y;
                             l[n][i] *= f;

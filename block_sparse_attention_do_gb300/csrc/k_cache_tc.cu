@@ -2,7 +2,7 @@
 // paged 8-bit cache on the tcgen05 tensor cores; bf16 queries, D = 64 or 128.
 //
 // The formulas are those of k_cache_attn.cu (scales of a page's values in the
-// exponent, running maximum raised only when a weight would pass 2^10, the sum
+// exponent, a row's unit raised only when a weight would pass 2^15, the sum
 // taken from the scores alone from a page of far values on).  Here
 // the products bound the time: 4 D operations per query row and key, so each
 // code is converted once for 256 rows and the conversion leaves the critical
@@ -49,7 +49,7 @@ constexpr int kThreads = (kSoftmaxWarps + kConvWarps + 4) * 32;  // whole warpgr
 constexpr int kRegsSoftmax = 176, kRegsConv = 104, kRegsMma = 56;
 constexpr int kStages = 2;      // K and V tiles in shared memory
 constexpr int kScaleRing = 4;   // tiles whose page scales are kept: softmax lags the converters by up to 3
-constexpr float kNoMax = -1e30f, kLazy = 10.f;
+constexpr float kNoMax = -1e30f, kTop = 15.f, kUp = 5.f;  // a row's weights grow from 2^kUp to 2^kTop before its unit is raised
 constexpr float kTiny = 1.17549435e-38f;    // keeps kNoScore * scale from being a NaN
 constexpr uint32_t kNoScore = 0xff800000u;  // -infinity
 
@@ -263,7 +263,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
                 f[n].x = fmaxf(f[n].x * qmul, kTiny);
                 top = fmaxf(top, fmaf(fmaxf(max3(y[0], y[1], y[2]), y[3]), f[n].x, f[n].y));
             }
-            const bool raise = top > m + kLazy;  // (no column attended: top is -infinity)
+            const bool raise = top > m + kTop;  // (no column attended: top is -infinity)
             if (__any_sync(0xffffffffu, raise || apart || f[0].w != 0.f)) {
                 if (apart || f[0].w != 0.f) {  // the sum by the scores alone, here and from here on
                     if (!apart)
@@ -295,7 +295,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
                         N = y;
                     }
                 }
-                const float mn = raise ? top : m, f = ex2(m - mn);
+                const float mn = raise ? top - kUp : m, f = ex2(m - mn);
                 m = mn;
                 l *= apart ? 1.f : f;
                 if (i > 0) {  // (S_q of this tile follows P_q V of the last one: O_q is at rest)

@@ -744,6 +744,44 @@ def test_chunk_form_values_of_zero_beside_large_ones(scales, kw, D, bs):
     takes("cache_chunk", [700, 300, 40], [260, 300, 40], 16, 8, D, bs, BF, ragged=True, edit=far_values(*scales), **kw)
 
 
+@pytest.mark.parametrize("form,dtype,D,bs,lens,T", [
+    ("cache_attn_cluster", BF, 32, 16, [16, 15], 1), ("cache_attn_cluster", F32, 32, 16, [16, 15], 1),
+    ("cache_attn_cluster", F32, 64, 32, [16, 9], 1), ("cache_attn", F32, 32, 16, [16] * 90, 1), ("cache_attn", BF, 32, 16, [16] * 90, 1),
+    ("cache_chunk", BF, 64, 32, [300, 300], 300)])
+def test_small_weights_beside_a_large_one_keep_their_bits(form, dtype, D, bs, lens, T):
+    """One key takes nearly the whole weight and has a value of zero (a sink among the keys); what is left is the others,
+    all of one weight: the output is held to their relative roundings.  (The weight's place between two halves of step
+    2^-24 is the worst: 45.5 of them, or in 32 bits 1420.5.)"""
+    gap = 24 - math.log2(45.5 if dtype == BF else 1420.5)
+    Hkv, G = (8, 2) if form == "cache_chunk" else (2, 4)
+    cache = filled(lens, Hkv, D, bs, 5, garbage=False, cols=1000 * 64 // bs if form == "cache_attn" else None)
+    cache.k.view(torch.uint8).zero_()
+    cache.v.view(torch.uint8).fill_(0x38)  # 1.0
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    for b in range(len(lens)):
+        p = int(cache.page_table[b, 0])
+        cache.k.view(torch.uint8)[p, :, 0, 0] = 0x38
+        cache.v.view(torch.uint8)[p, :, 0] = 0
+    B = len(lens)
+    q = torch.zeros(B, Hkv * G, T, D)
+    q[..., 0] = 16.0
+    scale = gap * math.log(2) / 16
+    out = []
+    assert form_of(lambda: out.append(api.cache_fwd(q.to(dtype).to(DEV), cache, scale=scale))) == form
+    o, lse = (x.double().cpu().numpy() for x in out[0])
+    s32 = float(torch.tensor(scale, dtype=torch.float32).double())
+    keys = np.maximum(np.array(lens)[:, None] - T + 1 + np.arange(T)[None], 0)  # [B, T]
+    small = (keys - 1) * math.exp(-16 * s32)
+    want = (small / (1 + small))[:, None, :, None]
+    # the score: two roundings of the scale and one of the product; the exponential 2^-21; the weight's 11 or 22 bits;
+    # the sums' roundings; the output's own
+    rel = 2 * (3 * U32 * gap + 2.0 ** -21) + (2.0 ** -11 if dtype == BF else 2.0 ** -21) + 2 * (max(lens) + 16) * U32
+    rel += torch.finfo(dtype).eps / 2
+    assert (np.abs(o - want) <= rel * (1 + 2.0 ** -7) * want).all(), np.abs(o / np.maximum(want, 1e-30) - 1).max()
+    assert (np.abs(lse - (16 * s32 + np.log1p(small))[:, None]) <= (gap + 4) * 8 * U32).all()
+
+
 def test_chunk_form_leaves_rows_behind_the_last_sequence():
     cache = filled([400, 300], 8, 64, 32, 1)
     cu = torch.tensor([0, 300, 600], dtype=torch.int32, device=DEV)
