@@ -812,6 +812,24 @@ def test_list_form_window():
     takes("cache_attn", [int(n) for n in g.integers(0, 5000, 40)], [2] * 40, 16, 8, 128, 64, BF, window=3500)
 
 
+@pytest.mark.parametrize("kw", [dict(window=1), dict(window=37), dict(window=200), dict(window=70, sinks=True)])
+@pytest.mark.parametrize("dtype,Hq,Hkv,D,bs,T", [(BF, 8, 2, 128, 64, 1), (F32, 6, 2, 64, 32, 2), (BF, 32, 2, 128, 16, 1),
+                                                 (F32, 2, 1, 32, 16, 7), (BF, 20, 1, 64, 64, 1), (F32, 16, 1, 128, 64, 1)])
+def test_list_form_short_windows(kw, dtype, Hq, Hkv, D, bs, T):
+    """Windows of any length take the list where the table has many entries."""
+    g = np.random.default_rng(5)
+    B = 320 // Hkv
+    takes("cache_attn", [int(n) for n in g.integers(0, 300, B)], [T] * B, Hq, Hkv, D, bs, dtype, cols=8200 // B + 1, **kw)
+
+
+@pytest.mark.parametrize("S,rows", [(27, 320), (130, 320), (28, 304), (130, 304)])
+@pytest.mark.parametrize("dtype,G,D,bs", [(BF, 4, 128, 64), (F32, 3, 64, 32), (BF, 16, 128, 16), (BF, 20, 64, 64), (F32, 2, 32, 16)])
+def test_list_form_index(S, rows, dtype, G, D, bs):
+    """Index rows cut at 128 tokens and joined (320 of them over 304 or 152 CTAs), and whole ones, with nothing to join (304)."""
+    g = np.random.default_rng(6)
+    takes("cache_attn", [int(n) for n in g.integers(0, 300, rows // 2)], [1] * (rows // 2), 2 * G, 2, D, bs, dtype, S=S)
+
+
 @pytest.mark.parametrize("T", [1, 4])
 def test_list_form_nan_values(T):
     def edit(cache):
