@@ -696,8 +696,8 @@ def _cu(cache, cu_seqlens, max_seqlen):
 
 def cache_reserve(cache, n_new, stream=None):
     """Row b of the cache grows by n_new[b] tokens (int32 [rows]): pages from
-    the pool, lowest ids first, and seq_lens; pages that it holds there already
-    (its length was lowered: rejected drafts) are used again.  All rows or, with
+    the pool, lowest ids first, and seq_lens; pages of its own that it holds
+    there already (its length was lowered: rejected drafts) are used again.  All rows or, with
     too few free pages (NSA_ERR_CACHE_FULL in cache.ws), none."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
@@ -794,6 +794,7 @@ def cache_fwd(q, cache, block_idx=None, scale=None, cu_seqlens=None, max_seqlen=
         _need(sinks.dtype == torch.float32 and sinks.is_contiguous() and tuple(sinks.shape) == (q.shape[1],) and
               sinks.device == dev, "cache_fwd: sinks are float32 [Hq]")
     if q.numel() == 0:
+        cache.fwd_ws = ws
         if ws is not None:
             ws[:4].zero_()
         return torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(q.shape[:-1], dtype=torch.float32, device=dev)

@@ -196,8 +196,8 @@ __device__ __forceinline__ bool grown_columns(const Cache &c, const int *n_new, 
     return ok;
 }
 
-// How many of columns [have, want) of row b hold a page already; -1 where one
-// holds what is no page in use.  (The whole warp.)
+// How many of columns [have, want) of row b hold a page of the row's alone; -1
+// where one holds what is no page in use.  (The whole warp.)
 __device__ __forceinline__ int held_columns(const Cache &c, int b, int have, int want, int lane)
 {
     int held = 0;
@@ -205,9 +205,11 @@ __device__ __forceinline__ int held_columns(const Cache &c, int b, int have, int
 #pragma unroll 4
     for (int col = have + lane; col < want; col += 32) {
         const int p = c.table[(int64_t)b * c.cols + col];
-        held += p != -1;
-        if (p != -1)
-            none |= p < 0 || p >= c.pages || c.ref[p] <= 0;
+        if (p != -1) {
+            const int count = p >= 0 && p < c.pages ? c.ref[p] : 0;
+            held += count == 1;
+            none |= count <= 0;
+        }
     }
     none = __any_sync(0xffffffffu, none);
     held = __reduce_add_sync(0xffffffffu, held);
@@ -229,7 +231,8 @@ __global__ void __launch_bounds__(kThreads)
     cl.sync();  // every CTA of the cluster runs from here on: its shared memory may be written
     // every CTA checks every row and knows the sum; CTA 0 writes the offsets.
     // A row whose length was lowered holds a page in the first column that it
-    // grows into (the read of a thread's first row is under way with the counts)
+    // grows into: its own is kept, one that it shares is given back for another
+    // (the read of a thread's first row is under way with the counts)
     int in_first = -1;
     bool none = false, held = false;
 #pragma unroll 4
@@ -291,17 +294,28 @@ __global__ void __launch_bounds__(kThreads)
             for (int col = have + w.lane; col < want; col += 32)
                 row[col] = __ldcg(ws.p2 + off + col - have);
         } else
-            for (int col0 = have, nth = off; col0 < want; col0 += 32) {  // the empty columns
-                const int col = col0 + w.lane;
-                const bool empty = col < want && row[col] == -1;
-                const unsigned m = __ballot_sync(0xffffffffu, empty);
-                if (empty)
-                    row[col] = __ldcg(ws.p2 + nth + __popc(m & ((1u << w.lane) - 1u)));
+            for (int col0 = have, nth = off; col0 < want; col0 += 32) {  // the empty columns, and those of shared pages
+                const int col = col0 + w.lane, old = col < want ? row[col] : -1;
+                const bool lacks = col < want && (old == -1 || c.ref[old] > 1);
+                const unsigned m = __ballot_sync(0xffffffffu, lacks);
+                const int i = nth + __popc(m & ((1u << w.lane) - 1u));
+                if (lacks) {
+                    row[col] = __ldcg(ws.p2 + i);
+                    ws.p0[i] = old;
+                }
                 nth += __popc(m);
             }
         __syncwarp();
         if (w.lane == 0)
             c.lens[b] = len + n;
+    }
+    if (!kept)
+        return;
+    cl.sync();  // (every row has read the counts)
+    for (int i = w.thread; i < (int)total; i += w.threads) {
+        const int old = __ldcg(ws.p0 + i);
+        if (old >= 0)
+            atomicSub(c.ref + old, 1);
     }
 }
 

@@ -362,10 +362,11 @@ nsa_status nsa_build_inverse_index_noalloc(const nsa_problem *p, const int32_t *
  * memory, and report NSA_ERR_DEVICE_TIMEOUT through the workspace error word,
  * leaving the CUDA context usable.  nsa_debug_stall(kernel, wait_limit_us)
  * lets a test run that path without any fault: while `kernel` is 1 (the
- * forward, and the chunk form of nsa_cache_fwd), 2 (the dK/dV kernel) or 3 (the dQ kernel), that kernel is
- * launched with the thread that issues its S = Q K^T products idle, so the
- * first wait on S runs out; `wait_limit_us` (1 .. 2000000; 0 = the default
- * of 2 s) replaces the limit of every tensor-core kernel's waits.
+ * forward; the tensor-core form of nsa_cache_fwd too), 2 (the dK/dV kernel)
+ * or 3 (the dQ kernel), that kernel is launched with the thread that issues
+ * its S = Q K^T products idle, so the first wait on S runs out;
+ * `wait_limit_us` (1 .. 2000000; 0 = the default of 2 s) replaces the limit
+ * of every tensor-core kernel's waits.
  * nsa_debug_stall(0, 0) restores normal operation.  Returns
  * NSA_ERR_INVALID_ARG for values out of range.  The CUDA-core kernels (fp32,
  * other head dims and block sizes) have no waits and ignore it.
@@ -431,7 +432,8 @@ nsa_status nsa_select_topk(const nsa_problem *p, const int32_t *cu_seqlens, cons
  *   seq_lens   [rows] int32: tokens of each row, NEW TOKENS INCLUDED: reserve
  *              first, then append, then attend.  The caller may lower a length
  *              (tokens that were drafted and rejected): the row keeps the pages
- *              behind it until it grows into them again or is freed
+ *              behind it until it grows into them again or is freed.  Within a
+ *              block that other rows share, nothing can be appended
  *   refcount   [num_pages] int32: table entries that name each page; 0: free
  *
  * All of it is the caller's device memory; the calls change it on `stream`,
@@ -468,9 +470,11 @@ typedef struct nsa_cache {
  * free page ids first, so that their results depend on the cache's state alone.
  *  - reserve: row b grows by n_new[b] >= 0 tokens (device int32 [rows]): pages
  *    for them, in the order of rows and columns, and seq_lens.  A column that
- *    holds a page already keeps it.  All rows or none: NSA_ERR_CACHE_FULL (too
- *    few free pages) or NSA_ERR_BAD_INDEX (a negative count, a row beyond
- *    max_pages, a column that holds no page in use) changes nothing.
+ *    holds a page already (its row's length was lowered) keeps it, or, where
+ *    other rows share it, gives it back for one of its own.  All rows or none:
+ *    NSA_ERR_CACHE_FULL (too few free pages) or NSA_ERR_BAD_INDEX (a negative
+ *    count, a row beyond max_pages, a column that holds no page in use) changes
+ *    nothing.
  *  - free: the n listed rows (device int32) give up their pages and have
  *    length 0.  A row outside the table or listed twice is reported, and
  *    freed once.

@@ -1056,26 +1056,38 @@ def test_lowered_lengths_keep_their_pages(pool, rows, cols, bs):
     for step in range(25):
         grow = np.minimum(g.integers(0, 4 * bs if step % 3 else 9, rows), cols * bs - lens)
         api.cache_reserve(cache, i32(*grow))
-        used = set(table[table >= 0].tolist())
-        free = iter([p for p in range(pool) if p not in used])
-        missing = [(b, c) for b in range(rows) for c in range(-(-lens[b] // bs), -(-(lens[b] + grow[b]) // bs)) if table[b, c] < 0]
-        if len(missing) > pool - len(used):
+        count = np.bincount(table[table >= 0], minlength=pool)
+        free = iter(np.flatnonzero(count == 0))
+        # a page that several rows hold is no row's to grow into
+        missing = [(b, c) for b in range(rows) for c in range(-(-lens[b] // bs), -(-(lens[b] + grow[b]) // bs))
+                   if table[b, c] < 0 or count[table[b, c]] > 1]
+        if len(missing) > (count == 0).sum():
             assert api.get_error(cache.ws) == 7
         else:
             assert api.get_error(cache.ws) == 0
             for b, c in missing:
                 table[b, c] = next(free)
             lens += grow
-        if step == 12:
-            src, dst = int(lens.argmax()), int(lens.argmin())
-            api.cache_fork(cache, i32(src), i32(dst))
-            assert api.get_error(cache.ws) == 0
-            full, tail = lens[src] // bs, int(lens[src] % bs > 0)
-            table[dst] = -1
-            table[dst, :full] = table[src, :full]
-            if tail:
-                table[dst, full] = min(set(range(pool)) - set(table[table >= 0].tolist()))
-            lens[dst] = lens[src]
+        if step % 6 == 2:
+            order = np.argsort(lens)
+            src, dst = order[-3:], order[:3]
+            api.cache_fork(cache, i32(*src), i32(*dst))
+            tails = sum(int(n % bs > 0) for n in lens[src])
+            held = table.copy()
+            held[dst] = -1
+            free = iter(np.flatnonzero(np.bincount(held[held >= 0], minlength=pool) == 0).tolist() + [-1] * 3)
+            ids = [next(free) if lens[s] % bs else -1 for s in src]
+            if tails and min(i for s, i in zip(src, ids) if lens[s] % bs) < 0:
+                assert api.get_error(cache.ws) == 7
+            else:
+                assert api.get_error(cache.ws) == 0
+                table = held
+                for s, d, i in zip(src, dst, ids):
+                    full = lens[s] // bs
+                    table[d, :full] = table[s, :full]
+                    if lens[s] % bs:
+                        table[d, full] = i
+                    lens[d] = lens[s]
         if step % 8 == 7:
             gone = g.permutation(rows)[:rows // 3]
             api.cache_free(cache, i32(*gone))
