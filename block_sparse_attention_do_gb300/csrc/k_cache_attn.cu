@@ -270,8 +270,7 @@ template <int D, int NT, bool SPLIT> struct Smem {
     int64_t off[kList];  // of the listed entries: byte offset of the page and head
     int key0[kList];     // first key (kNoKey: left out)
     float4 sc[kList];    // k scale, log2 and reciprocal of the v scale
-    float2 ml[kWarps][R];       // each warp's maximum and sum
-    float2 alone[kWarps][R];    // those of the scores alone, once the sum is kept apart
+    float2 ml[kWarps][R];       // each warp's maximum and sum (before the end: of the scores alone, once those are kept apart)
     float2 cta_ml[R];           // the CTA's, for its cluster
     uint32_t nan[kWarps][R * D / 32];  // each warp's outputs that a NaN value reaches
     union {
@@ -598,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         };
         float o[NT][MT][4];
         float m[NT][2], l[NT][2];
-        bool apart = false;  // (uniform over the CTA) the sums are in sm.alone
+        bool apart = false;  // (uniform over the CTA) the sums are in sm.ml
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                         for (int i = 0; i < 2; ++i) {
                             const float x = sum_of_rows(l[n][i]);
                             if (gq == 0)
-                                sm.alone[warp][n * 8 + tq * 2 + i] = make_float2(m[n][i], x);
+                                sm.ml[warp][n * 8 + tq * 2 + i] = make_float2(m[n][i], x);
                             l[n][i] = 0.f;
                         }
                 apart = true;
@@ -865,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                         for (int i = 0; i < 2; ++i) {
                             const int r = n * 8 + tq * 2 + i, p = sm.pos[r];
                             const float f = ks * sm.qmul[r];
-                            const float2 old = sm.alone[warp][r];
+                            const float2 old = sm.ml[warp][r];
                             float y[2], top = old.x, sum = 0.f;
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {
@@ -882,7 +881,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                             sum = sum_of_rows(sum);
                             __syncwarp();  // (every lane has read the old ones)
                             if (gq == 0)
-                                sm.alone[warp][r] = make_float2(top, old.y * exp2f(old.x - top) + sum);
+                                sm.ml[warp][r] = make_float2(top, old.y * exp2f(old.x - top) + sum);
                         }
                     __syncwarp();
                 }
@@ -891,6 +890,8 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
 
         // ---- the warps' sums joined in shared memory (over the rings)
         __syncthreads();
+        float2 *end_ml = apart ? (float2 *)sm.sc + warp * R : sm.ml[warp];  // (the lists' scales are used up)
+        static_assert(sizeof(sm.sc) >= sizeof(sm.ml), "");
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -898,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
                 float x = sum_of_rows(l[n][i]);
                 const int r = n * 8 + tq * 2 + i;
                 if (gq == 0)
-                    sm.ml[warp][r] = make_float2(m[n][i], x);
+                    end_ml[r] = make_float2(m[n][i], x);
                 if (r < u.nrows) {
 #pragma unroll
                     for (int j = 0; j < MT; j += 2)  // dimensions gq * VB + 2 j ..
@@ -908,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, attn_ctas(NT)) cache_attn_kernel(con
         if (apart) {  // O to units of 2^N, N raised by the sum's exponent: O is then a mean of values
             __syncwarp();
             for (int r = 0; r < u.nrows; ++r) {
-                const float2 alone = sm.alone[warp][r], ml = sm.ml[warp][r];
+                const float2 alone = sm.ml[warp][r], ml = end_ml[r];
                 const int e = alone.y > 0.f && alone.y < INFINITY ? (int)(__float_as_uint(alone.y) >> 23) - 127 : 0;
                 const float top = alone.x + (float)e, f = exp2f(fminf(ml.x - top, 127.f));
                 __syncwarp();
