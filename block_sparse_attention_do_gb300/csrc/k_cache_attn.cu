@@ -19,7 +19,7 @@
 // its next steps of 16 tokens under way into a ring of its own in shared
 // memory, and no warp waits for another before the end.  Measured, D = 128, 8
 // kv heads of 4 query heads: 32 sequences of 128 .. 32768 tokens, 1.08 GB of
-// codes, 182 us, 5.9 TB/s (88% of a plain copy's rate); one sequence of 8192,
+// codes, 183 us, 5.9 TB/s (87% of a plain copy's rate); one sequence of 8192,
 // 17 MB, 13 us, of which 4 are any launch's.  The products are taken
 // transposed, tokens (then head dimensions) as the 16 rows of mma.m16n8k16
 // and query rows as its 8 columns:

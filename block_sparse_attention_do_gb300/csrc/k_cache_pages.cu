@@ -10,12 +10,13 @@
 // it is the chain of those steps (a few dependent reads each, about 0.6 us, and
 // as much for a barrier of several CTAs), not the bytes: 0.26 MB of counts for
 // 65,536 pages.  The pages' contents move in a wide launch that is bound by
-// memory bandwidth: 300 pages of 131 KB, 79 MB read and written, in 11.6 us,
-// 6.8 TB/s (18 for the call).  Calls measured (of each, 4 us are any launch's):
-// 64 of 72 rows forked in a pool of 4096 pages 14 us, 64 rows freed and reserved
-// again in one of 65,536 15 us, a pool of 4096 compacted 23 us, 10 of them the
-// bytes.  Lists, counts and contents in one launch of all SMs, with barriers
-// between them, was slower (copy 39 us).
+// memory bandwidth: 300 pages of 131 KB, 79 MB read and written, in 14.3 us
+// (profiled), 5.5 TB/s; 11.6 at a plain copy's rate; 18 for the call.  Calls
+// measured (of each, 4 us are any launch's): 64 of 72 rows forked in a pool of
+// 4096 pages 14 us, 64 rows freed and reserved again in one of 65,536 15 us, a
+// pool of 4096 compacted 23 us, whose bytes would take 9.9 at a copy's rate.
+// Lists, counts and contents in one launch of all SMs, with barriers between
+// them, was slower (copy 39 us).
 #include <cooperative_groups.h>
 
 #include "cache_common.cuh"

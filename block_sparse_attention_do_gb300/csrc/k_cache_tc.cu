@@ -21,13 +21,16 @@
 // bits, three more than bf16.  Tensor memory is full: S 2 x 128 columns, O 2 x D.
 //
 // Measured: chunks of up to 2048 tokens of 6 sequences over 2048 .. 8192 keys
-// (32 query heads on 8, D = 128; 395 GFLOP, masked keys not counted) 341 us,
-// 1.16 PFLOP/s, 60% of the measured bf16 rate.  A tile of 128 keys takes 1.65
+// (32 query heads on 8, D = 128; 395 GFLOP, masked keys not counted) 321 us,
+// 1.23 PFLOP/s, 64% of the measured bf16 rate.  A tile of 128 keys takes 1.5
 // us, where its products take 1.0 and its softmax (256 x 128 exponentials, with
 // a maximum, a scaling, a sum and a rounding of each) about as long beside
 // them; beginning and ending a unit of 256 rows costs some 10 us.  CTAs that
-// keep their tensor memory and take several units in turn did not lower that,
-// and their inner loop no longer fitted its registers (1.75 us a tile).
+// keep their tensor memory and take several units in turn did not lower that
+// (at 1.65 us a tile), and their inner loop no longer fitted its registers
+// (1.75).  The sum of the scores alone reads S from tensor memory once more:
+// held in registers for it, S cost every tile (345 us), as did a second copy of
+// the loop (350) and the same reads ahead of the maximum (368).
 #include <math.h>
 
 #include "cache_common.cuh"
@@ -630,10 +633,10 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) cache_ch
 // Where this kernel takes over from the list's (k_cache_attn.cu), whose time
 // goes by 32-row tiles, all SMs together, while a CTA here takes 256 rows by
 // itself.  Measured over 4096 cached tokens, 8 kv heads of 4 query heads: 16
-// sequences of 5, 8, 16 and 32 tokens (128 .. 512 tiles of 32 rows) 57, 62, 105
-// and 192 us by the list, 69, 69, 69 and 70 here; one of 64, 128 and 256 tokens
-// 32, 58 and 99 us there, 67, 67 and 68 here; 64 sequences of 8 and 16 (2048
-// cached, four rounds of CTAs) 127 and 237 us there, 145 and 146 here.
+// sequences of 5, 8, 16 and 32 tokens (128 .. 512 tiles of 32 rows) 57, 62, 103
+// and 184 us by the list, 66, 66, 66 and 67 here; one of 64, 128 and 256 tokens
+// 31, 57 and 95 us there, 62 here; 64 sequences of 8 and 16 (2048 cached, four
+// rounds of CTAs) 125 and 230 us there, 139 and 140 here.
 bool cache_chunk_supported(const Geo &g, int dtype, bool sel)
 {
     const int64_t rows = longest_rows(g), seqs = (int64_t)g.B * g.Hkv;
