@@ -589,6 +589,67 @@ def test_offsets_whose_difference_leaves_the_ints_are_reported(offsets, total, H
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("form,dtype,Hq,Hkv,D,T,cols", [("cache_attn_cluster", BF, 8, 2, 128, 1, None), ("cache_attn_cluster", F32, 6, 2, 64, 5, None),
+                                                        ("cache_attn", BF, 8, 2, 128, 3, 900), ("cache_attn", F32, 24, 2, 32, 2, 2000),
+                                                        ("cache_chunk", BF, 16, 8, 64, 150, None), ("cache_chunk", BF, 16, 8, 128, 150, None)])
+def test_strided_queries_give_the_same(form, dtype, Hq, Hkv, D, T, cols):
+    """Queries as a model's projection leaves them: token before head, a slice of one tensor of queries, keys and values."""
+    cache = filled([400, 170, 0, 151], Hkv, D, 32, 7, cols=cols)
+    wide = torch.randn(4, T, Hq + 2 * Hkv, D, device=DEV).to(dtype)
+    q = wide[:, :, :Hq].transpose(1, 2)
+    sinks = torch.randn(Hq, device=DEV)
+    for kw in (dict(), dict(window=60, sinks=sinks)):
+        got = []
+        assert form_of(lambda: got.append(api.cache_fwd(q, cache, **kw))) == form or kw
+        want = api.cache_fwd(q.contiguous(), cache, **kw)
+        assert all(torch.equal(a, b) for a, b in zip(got[0], want))
+    if T < 40:
+        idx = torch.zeros(4, Hkv, T, 2, dtype=torch.int32, device=DEV)
+        idx[..., 1] = -1
+        assert all(torch.equal(a, b) for a, b in zip(api.cache_fwd(q, cache, block_idx=idx), api.cache_fwd(q.contiguous(), cache, block_idx=idx)))
+    packed = wide.view(4 * T, Hq + 2 * Hkv, D)[:, :Hq]
+    cu = i32(*[T * i for i in range(5)])
+    a, b = (api.cache_fwd(x, cache, cu_seqlens=cu, max_seqlen=T) for x in (packed, packed.contiguous()))
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_captured_calls_keep_their_own_word():
+    """A chunk's and a list's call in graphs, replayed on two streams at once: each graph has its workspace."""
+    cache = filled([700, 300, 40], 8, 64, 32, 6, cols=900)
+    q = torch.randn(3, 16, 150, 64, device=DEV).to(BF)
+    one = q[:, :, :1].contiguous()
+    want = [api.cache_fwd(x, cache) for x in (q, one)]
+    torch.cuda.synchronize()
+    graphs, outs, words = [], [], []
+    for x, form in ((q, "cache_chunk"), (one, "cache_attn")):
+        assert form_of(lambda: api.cache_fwd(x, cache)) == form
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(api.cache_fwd(x, cache))
+        graphs.append(g)
+        words.append(cache.fwd_ws)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(4):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert [api.get_error(w) for w in words] == [0, 0]
+        for a, b in zip(want, outs):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+    page = cache.page_table[0, 2].clone()
+    cache.page_table[0, 2] = -5
+    for g in graphs:
+        g.replay()
+    assert [api.get_error(w) for w in words] == [3, 3]
+    cache.page_table[0, 2] = page
+
+
+def test_the_most_rows_of_a_call():
+    g = np.random.default_rng(9)
+    takes("cache_attn", [int(n) for n in g.integers(0, 40, 8192)], [1] * 8192, 2, 1, 32, 16, F32)
+
+
 def test_calls_on_two_streams_and_in_graphs():
     cache = filled([3000, 100, 0, 64], 2, 128, 64, 4)
     qs = [torch.randn(4, 8, T, 128, device=DEV).to(BF) for T in (1, 1, 3, 50)]
@@ -911,6 +972,22 @@ def test_append_packed_and_strided(dtype):
     same_pool(cache, plain)
 
 
+@pytest.mark.parametrize("offsets,error", [([5, 9, 9, 150], 0), ([9, 5, 40, 60], 3)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_from_behind_the_first_token(dtype, offsets, error):
+    """Packed offsets that begin behind the first token, and a first run that goes backward: no row of nobody's is taken."""
+    cache = filled([60, 50, 200], 2, 64, 32, 3, garbage=False)
+    plain = Plain(cache)
+    g = np.random.default_rng(3)
+    k, v = (torch.tensor(g.normal(size=(156, 2, 64)), dtype=torch.float32).to(dtype) for _ in range(2))
+    api.cache_append(cache, k.to(DEV), v.to(DEV), cu_seqlens=i32(*offsets), max_seqlen=150)
+    assert api.get_error(cache.ws) == error
+    for b, (lo, hi) in enumerate(zip(offsets, offsets[1:])):
+        if lo < hi:
+            plain.append(b, k[lo:hi].double().numpy(), v[lo:hi].double().numpy())
+    same_pool(cache, plain)
+
+
 def test_append_special_values():
     cache = filled([66, 64], 1, 32, 64, 1, garbage=False)
     cache.k_scale.fill_(2.0 ** -7)
@@ -1046,7 +1123,7 @@ def test_page_lists_are_checked():
     same_meta(cache, plain)
 
 
-@pytest.mark.parametrize("pool,rows,cols,bs", [(60, 6, 9, 16), (3000, 300, 9, 32), (9000, 70, 110, 16)])
+@pytest.mark.parametrize("pool,rows,cols,bs", [(60, 6, 9, 16), (3000, 300, 9, 32), (9000, 70, 110, 16), (9000, 1300, 8, 16)])
 def test_lowered_lengths_keep_their_pages(pool, rows, cols, bs):
     """Drafted tokens that were rejected: the caller lowers a row's length, and the row grows into the pages that it
     holds.  No page is lost: a page is in use exactly as often as the table names it."""
