@@ -71,9 +71,11 @@ def _bht_strides(t, thd):
     [total, H, D]) tensor whose last dimension is contiguous."""
     if t.stride(-1) != 1:
         raise ValueError("the head dimension must be contiguous")
-    if thd:
-        return (0, t.stride(1), t.stride(0))
-    return (t.stride(0), t.stride(1), t.stride(2))
+    s = (0, t.stride(1), t.stride(0)) if thd else (t.stride(0), t.stride(1), t.stride(2))
+    # (all 0 declares a dense tensor: of one row that is expanded, its rows would be read behind it)
+    if not any(s) and t.numel() > t.shape[-1]:
+        raise ValueError("expanded tensors have no rows of their own: make them contiguous")
+    return s
 
 
 def declare_strides(p: Problem, thd: bool, q=None, k=None, o=None, dq=None, dk=None) -> Problem:
@@ -602,6 +604,7 @@ def _row_strides(t, thd):
     of size 1 (never stepped) replaced by valid ones."""
     _need(t.stride(-1) == 1, "norm_rope: the head dimension must be contiguous")
     s = [(t.stride(i) if t.shape[i] > 1 else t.shape[-1]) for i in range(t.dim() - 1)]
+    _need(any(s), "norm_rope: expanded tensors have no rows of their own (all strides 0 declare a dense one): make them contiguous")
     return (t.shape[-1], s[1], s[0]) if thd else tuple(s)
 
 
@@ -741,7 +744,8 @@ class KVCache:
     def __init__(self, k, v, k_scale, v_scale, page_table, seq_lens, refcount=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.float8_e4m3fn,
               "KVCache: k and v are float8_e4m3fn [num_pages, Hkv, block_size, D]")
-        _need(k.stride(3) == 1 and k.stride() == v.stride(), "KVCache: k and v have the same strides, D contiguous")
+        _need(k.stride(3) == 1 and k.stride() == v.stride() and any(k.stride()[:3]),
+              "KVCache: k and v have the same strides, D contiguous, and are not expanded")
         dev = k.device
         for s in (k_scale, v_scale):
             _need(s.dtype == torch.float32 and s.is_contiguous() and tuple(s.shape) == tuple(k.shape[:2]) and s.device == dev,

@@ -83,3 +83,31 @@ def test_tensors_are_checked():
     q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 2, 8, 64)
     with pytest.raises(api.NsaError):
         api._norm_rope(q, k, q, k, None, None, True, None, None, None, None, 1e-6, False, None)
+
+
+def test_expanded_tensors_are_refused():
+    """All strides 0 declare a dense tensor: one row expanded to many (a gradient that is the same for every token) would be
+    read far behind its end."""
+    row = torch.zeros(32)
+    with pytest.raises(api.NsaError):
+        api._row_strides(row.expand(2, 3, 4, 32), False)
+    with pytest.raises(ValueError):
+        api._bht_strides(row.expand(2, 3, 4, 32), False)
+    with pytest.raises(ValueError):
+        api._bht_strides(row.expand(5, 3, 32), True)
+    # of one dimension alone: a stride of 0 beside others that are not, refused by the call
+    p = api.problem(2, 3, 3, 4, 32, 64, 1, torch.float32)
+    for x in (torch.zeros(2, 3, 1, 32).expand(2, 3, 4, 32), torch.zeros(1, 3, 4, 32).expand(2, 3, 4, 32)):
+        p.q_stride[:] = api._row_strides(x, False)
+        assert api.lib().nsa_norm_rope_bwd_workspace_size(p) == 0
+    # tensors of one row, and dense ones, as before
+    assert any(api._row_strides(row.expand(1, 1, 1, 32), False)) and api._row_strides(torch.zeros(2, 3, 4, 32), False) == (384, 128, 32)
+    api._bht_strides(row.expand(1, 1, 1, 32), False)
+    assert api._bht_strides(torch.zeros(5, 3, 32), True) == (0, 32, 96)
+
+
+def test_an_expanded_cache_is_refused():
+    k = torch.zeros(32, dtype=torch.uint8).view(torch.float8_e4m3fn).expand(8, 2, 16, 32)
+    sc, (table, lens, refs) = torch.ones(8, 2), (torch.zeros(s, dtype=torch.int32) for s in ((3, 4), (3,), (8,)))
+    with pytest.raises(api.NsaError):
+        api.KVCache(k, k, sc, sc.clone(), table, lens, refs)
