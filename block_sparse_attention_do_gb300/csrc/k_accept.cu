@@ -137,7 +137,20 @@ template <int D> __global__ void __launch_bounds__(kMoveWarps * 32) accept_move_
             uint32_t lo, hi;
             e4m3x4_to_half(top, lo, hi);
             const float x = __half22float2(*(const __half2 *)&lo).x * ss[v];
-            amax = x < INFINITY ? fmaxf(amax, x) : amax;
+            if (x < INFINITY) {
+                amax = fmaxf(amax, x);
+                continue;
+            }
+            // a product beyond float's range counts in no maximum: the largest of the others (as in append)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                e4m3x4_to_half(u[i], lo, hi);
+                const float2 f = __half22float2(*(const __half2 *)&lo), g = __half22float2(*(const __half2 *)&hi);
+                for (float y : {f.x, f.y, g.x, g.y}) {
+                    y = fabsf(y * ss[v]);
+                    amax = y < INFINITY ? fmaxf(amax, y) : amax;
+                }
+            }
         }
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
         const float scale = fmaxf(e4m3_scale(amax), old);

@@ -414,6 +414,25 @@ def test_accept_nan_and_zero_codes():
     accept_case([100, 90], [40, 50], [(3, 9, 30, 35), (0, 7, 8, 9, 40)], 2, 64, 16, edit=edit)
 
 
+@pytest.mark.parametrize("D,bs", [(32, 16), (64, 32), (128, 64)])
+@pytest.mark.parametrize("slot", [0, 4])
+def test_accept_values_beyond_floats_range(D, bs, slot):
+    """A code times its scale that passes float's range counts in no maximum, as in append, where an infinity counts in none;
+    the finite values beside it in the same 16 codes do, and what they are divided by is theirs."""
+    head = bs + slot
+
+    def edit(cache):
+        for at in (head + bs + 3, head + bs + 6):  # 256 * 2^120, 3 * 2^120 and smaller ones in every 16 codes
+            page, i = int(cache.page_table[0, at // bs]), at % bs
+            cache.k_scale[page] = 2.0 ** 120
+            code = cache.k.view(torch.uint8)[page, :, i]
+            code.fill_(0x20)
+            code[:, ::16], code[:, 5::16], code[:, 7::16] = 0x78, 0x44, 0xf8
+        cache.v.view(torch.uint8)[page, :, i, :16] = 0x7f  # NaN alone
+    with np.errstate(over="ignore"):
+        accept_case([head + bs + 9, 40], [bs + 9, 5], [(bs + 3, bs + 6), (1,)], 2, D, bs, edit=edit)
+
+
 def test_accept_takes_what_an_append_of_the_values_gives():
     """The rule itself, through the library's append: the accepted drafts' values, appended to a row that never had the
     others, give the same codes and scales."""
