@@ -81,8 +81,8 @@ template <int D> __device__ __forceinline__ int k_at(int t, int u) { return (t *
 template <int D, bool SPLIT> struct Smem {
     uint2 qf[SPLIT ? 2 : 1][D / 16][kTiles][32];
     uint8_t ring[kWarps][kStages][16 * D];
-    int64_t off[kList * 4];  // of the listed steps: byte offset of the page, head and first key
-    float ks[kList * 4];     // their keys' scale (-1: no keys)
+    int64_t off[kList * 4];  // of the listed steps: byte offset of the page, head and first key (-1: no keys)
+    float ks[kList * 4];     // their keys' scale, whatever it is
     float sum[kList * 4];    // a block's sum, at its first step
     float mul[kRows];        // scale * log2(e) * 2^-e of each row
     float lse[kRows];        // its LSE in units of log 2 (no such row, or one that attends nothing: infinity)
@@ -196,8 +196,8 @@ template <typename T, int D, bool ONE> __global__ void __launch_bounds__(kThread
                 }
             }
             __syncthreads();  // the list before, and the unit before, are done with shared memory
-            sm.off[tid] = page >= 0 ? (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (c.bs - 1)) * st : 0;
-            sm.ks[tid] = page >= 0 ? c.ks[(int64_t)page * c.Hkv + kvh] : -1.f;
+            sm.off[tid] = page >= 0 ? (int64_t)page * c.sp + (int64_t)kvh * c.sh + (int64_t)(key & (c.bs - 1)) * st : -1;
+            sm.ks[tid] = page >= 0 ? c.ks[(int64_t)page * c.Hkv + kvh] : 0.f;
             sm.sum[tid] = 0.f;
             if (chunks == 1 && e0 == at)
                 stage(0);
@@ -233,7 +233,7 @@ template <typename T, int D, bool ONE> __global__ void __launch_bounds__(kThread
                 }
                 // steps that no row attends, or that have no page, are not read
                 auto attended = [&](int slot, int k0) {
-                    return sm.ks[slot] >= 0.f && k0 <= pmax && !(g.window > 0 && k0 + 15 <= pmin - g.window);
+                    return sm.off[slot] >= 0 && k0 <= pmax && !(g.window > 0 && k0 + 15 <= pmin - g.window);
                 };
                 auto fetch = [&](int j, int sub) {
                     const int slot = (j * kWarps + warp) * 4 + sub;

@@ -310,6 +310,21 @@ def test_weigh_waits_that_give_up():
     assert api.get_error(word) == 0 and torch.equal(weight, good)
 
 
+@pytest.mark.parametrize("dtype,D,T", [(BF, 128, 1), (BF, 64, 12), (F32, 64, 30), (BF, 32, 40), (BF, 128, 40), (BF, 64, 100)])
+def test_weigh_a_scale_that_is_nan_is_a_key_that_is(dtype, D, T):
+    """NaN in the weights of the page's head, in each form, and in no other."""
+    cache = filled([300, 200], 2, D, 32, 1)
+    q = torch.randn(2, 8, T, D, device=DEV).to(dtype)
+    _, lse = api.cache_fwd(q, cache)
+    want, got = (torch.zeros(2, 2, cache.page_table.shape[1], device=DEV) for _ in range(2))
+    api.cache_weigh(q, lse, cache, want)
+    cache.k_scale[int(cache.page_table[0, 2]), 1] = math.nan
+    api.cache_weigh(q, lse, cache, got)
+    assert torch.isnan(got[0, 1, 2]) and torch.isfinite(want).all()
+    got[0, 1, 2] = want[0, 1, 2]
+    assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------- evict
 
 def plain_evict(cache, weight, keep, first, recent):
