@@ -739,7 +739,8 @@ class KVCache:
     compact).  The cache keeps their addresses: they are written in place,
     never replaced.  `ws` is the workspace of the calls that change the cache;
     get_error(cache.ws) reads what the last of them found.  `fwd_ws` is the
-    last cache_fwd's workspace (None: it had none), for get_error too."""
+    last cache_fwd's workspace (None: it had none), `weigh_ws` the last
+    cache_weigh's, for get_error too."""
 
     def __init__(self, k, v, k_scale, v_scale, page_table, seq_lens, refcount=None):
         _need(k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype == torch.float8_e4m3fn,
@@ -769,7 +770,7 @@ class KVCache:
         if n == 0:
             raise NsaError(1, "nsa_cache_workspace_size")
         self.ws = torch.zeros(n, dtype=torch.uint8, device=dev)
-        self.fwd_ws = None
+        self.fwd_ws = self.weigh_ws = None
         self._problems = {}
 
     def problem(self, x, S, scale, cu_seqlens, max_seqlen, selection, query, tree=False):
@@ -1007,8 +1008,8 @@ def cache_weigh(q, lse, cache, weight, decay=1.0, scale=None, cu_seqlens=None, m
     """What the queries of a cache_fwd call (q, its lse, scale, window and
     offsets) gave each block of their rows, summed over tokens and a kv
     head's query heads, is added to weight (float32 [rows, Hkv, max_pages],
-    in place) times decay.  A ws of the caller's (256 bytes) holds the error
-    word that get_error reads; without one errors are not reported."""
+    in place) times decay.  The error word that get_error reads is
+    cache.weigh_ws: ws, the caller's 256 bytes, or the call's own."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_weigh(q, lse, cache, weight, decay, scale, cu_seqlens, max_seqlen, window, ws)
@@ -1019,14 +1020,16 @@ def cache_weigh(q, lse, cache, weight, decay=1.0, scale=None, cu_seqlens=None, m
     _need(lse.dtype == torch.float32 and lse.is_contiguous() and lse.device == dev and lse.shape == q.shape[:-1],
           "cache_weigh: lse is a dense float32 of q's rows")
     _weights(cache, weight)
+    if ws is None:  # (a page that is none, a wait that gave up: eviction would drop the blocks and nobody hear of it)
+        ws = torch.empty(256, dtype=torch.uint8, device=dev)
+    cache.weigh_ws = ws
     if q.numel() == 0:
-        if ws is not None:
-            ws[:4].zero_()
+        ws[:4].zero_()
         return
     p = cache.problem(q, 1, scale, cu_seqlens, longest, False, True)[1]
-    at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
     _check(lib().nsa_cache_weigh(p, cache.ref, int(window or 0), None if cu_seqlens is None else cu_seqlens.data_ptr(), q.data_ptr(),
-                                 lse.data_ptr(), float(decay), weight.data_ptr(), at, size, _raw_stream(cache)), "nsa_cache_weigh")
+                                 lse.data_ptr(), float(decay), weight.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream(cache)),
+           "nsa_cache_weigh")
 
 
 def cache_evict(cache, weight, keep, first=0, recent=1, kept=None, stream=None):

@@ -343,6 +343,16 @@ template <typename T, int D, bool ONE> __global__ void __launch_bounds__(kThread
     }
 }
 
+// The error word, cleared by a launch that overlaps its neighbours' (a memset begins behind the
+// end of what is in front of it, and what follows behind its own): 32 rows of 128 .. 32768
+// tokens 95.2 us, with a memset 97.4, without a word 93.6.
+__global__ void weigh_word_kernel(int *err)
+{
+    dependents_may_start();
+    dependency_wait();
+    *err = NSA_OK;
+}
+
 template <typename T, int D> cudaError_t weigh_t(const WeighArgs &a, cudaStream_t st)
 {
     auto kernel = longest_rows(a.g) <= 8 ? weigh_kernel<T, D, true> : weigh_kernel<T, D, false>;
@@ -359,6 +369,8 @@ template <typename T, int D> cudaError_t weigh_t(const WeighArgs &a, cudaStream_
 int64_t cache_weigh_entries(const Geo &g, const Cache &c) { return (int64_t)g.B * (((int64_t)c.cols * c.bs + kGroup - 1) / kGroup + kStartCost) * g.Hkv; }
 
 int cache_weigh_max_rows() { return kWeighMaxRows; }
+
+cudaError_t launch_weigh_word(int *err, cudaStream_t st) { return err ? launch_dependent(weigh_word_kernel, dim3(1), dim3(1), 0, st, err) : cudaSuccess; }
 
 cudaError_t launch_cache_weigh(const Geo &g, const Cache &c, const void *q, const float *lse, float decay, float *weight, int dtype, int *err,
                                cudaStream_t st)

@@ -184,7 +184,8 @@ cudaError_t launch_tree_chunk(const Geo &g, const Cache &c, const void *q, const
                               char *ws, cudaStream_t st);
 // drafts that were accepted (k_accept.cu): path [rows, A]
 cudaError_t launch_cache_accept(const Cache &c, const int *n_new, const int *path, int A, const CacheWs &ws, cudaStream_t st);
-// blocks' attention weight (k_weigh.cu): weight [rows, Hkv, cols]; err (may be null) is zero at launch
+// blocks' attention weight (k_weigh.cu): weight [rows, Hkv, cols]; err (may be null) is cleared by launch_weigh_word
+cudaError_t launch_weigh_word(int *err, cudaStream_t st);
 cudaError_t launch_cache_weigh(const Geo &g, const Cache &c, const void *q, const float *lse, float decay, float *weight, int dtype, int *err,
                                cudaStream_t st);
 int64_t cache_weigh_entries(const Geo &g, const Cache &c);  // upper bound on the call's list (counted in int)

@@ -1547,8 +1547,7 @@ nsa_status nsa_cache_weigh(const nsa_problem *p, const nsa_cache *pc, int32_t wi
     if (ws && (s = check_ws(ws, ws_bytes, kAlign)) != NSA_OK)
         return s;
     cudaStream_t st = (cudaStream_t)stream;
-    if (ws)
-        NSA_TRY(cudaMemsetAsync(ws, 0, sizeof(int), st));
+    NSA_TRY(launch_weigh_word((int *)ws, st));
     if (g.ntok == 0)
         return NSA_OK;
     if (cache_weigh_tc_supported(g, p->dtype))

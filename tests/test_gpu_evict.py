@@ -325,6 +325,46 @@ def test_weigh_a_scale_that_is_nan_is_a_key_that_is(dtype, D, T):
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("T", [1, 100])
+def test_weigh_reports_without_a_word_of_the_callers(T):
+    """Pages that are none, and bounded waits that gave up, through the handle's word; each call has its own."""
+    cache = filled([300, 200], 2, 128, 64, 1)
+    q = torch.randn(2, 8, T, 128, device=DEV).to(BF)
+    _, lse = api.cache_fwd(q, cache)
+    weight = torch.zeros(2, 2, cache.page_table.shape[1], device=DEV)
+    api.cache_weigh(q, lse, cache, weight)
+    first = cache.weigh_ws
+    assert api.get_error(first) == 0
+    page = int(cache.page_table[1, 0])
+    cache.page_table[1, 0] = 4096
+    api.cache_weigh(q, lse, cache, weight)
+    second = cache.weigh_ws
+    cache.page_table[1, 0] = page
+    api.cache_weigh(q, lse, cache, weight)
+    assert api.get_error(cache.weigh_ws) == 0 and api.get_error(second) == 3 and api.get_error(first) == 0
+    word = torch.full((256,), 255, dtype=torch.uint8, device=DEV)
+    api.cache_weigh(q, lse, cache, weight, ws=word)
+    assert cache.weigh_ws is word and api.get_error(word) == 0
+    api.cache_weigh(q[:, :, :0], lse[:, :, :0], cache, weight)
+    assert cache.weigh_ws is not word and api.get_error(cache.weigh_ws) == 0
+    if T > 16:
+        api.debug_stall(1, 20000)
+        try:
+            api.cache_weigh(q, lse, cache, weight)
+            assert api.get_error(cache.weigh_ws) == 4
+        finally:
+            api.debug_stall(0, 0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.cache_weigh(q, lse, cache, weight)
+    held = cache.weigh_ws
+    for bad in (True, False, True):
+        cache.page_table[1, 0] = 4096 if bad else page
+        graph.replay()
+        torch.cuda.synchronize()
+        assert api.get_error(held) == (3 if bad else 0)
+
+
 # ------------------------------------------------------------------- evict
 
 def plain_evict(cache, weight, keep, first, recent):
