@@ -161,10 +161,11 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a)
         }
         return __shfl_sync(0xffffffffu, incl, 31);
     };
+    bool low = false;       // a page was dropped more often than its count said
     int equal = 0, to = 0;  // candidates equal to `top`, and columns that stay, before the batch
     for (int j0 = 0; j0 < cols; j0 += kThreads * kCols) {
         uint32_t k[kCols], votes[kCols];
-        int nth[kCols], dst[kCols], page[kCols];
+        int nth[kCols], dst[kCols], page[kCols], was[kCols];
         bool stays[kCols];
 #pragma unroll
         for (int v = 0; v < kCols; ++v) {
@@ -187,8 +188,7 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a)
         for (int v = 0; v < kCols; ++v) {
             const int j = j0 + v * kThreads + tid;
             dst[v] += to;
-            if (j < cols && !stays[v])
-                atomicSub(c.ref + page[v], 1);  // (a page of the pool: checked)
+            was[v] = j < cols && !stays[v] ? atomicSub(c.ref + page[v], 1) : 1;  // (a page of the pool: checked)
             stays[v] = stays[v] && dst[v] != j;  // (from here on: moves)
             if (kept && j < cols && dst[v] == j)
                 kept[j] = j;
@@ -218,6 +218,12 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a)
                 if (kept)
                     kept[dst[v]] = j0 + v * kThreads + tid;
             }
+#pragma unroll
+        for (int v = 0; v < kCols; ++v)
+            if (was[v] <= 0) {
+                atomicAdd(c.ref + page[v], 1);
+                low = true;
+            }
     }
     __syncthreads();
     for (int j = to + tid; j < cols; j += kThreads) {
@@ -227,6 +233,8 @@ __global__ void __launch_bounds__(kThreads) evict_kernel(const EvictArgs a)
         for (int h = 0; h < c.Hkv; ++h)
             weight[(int64_t)h * cols + j] = 0.f;
     }
+    if (low)
+        set_error(a.err, NSA_ERR_BAD_INDEX);
     if (tid == 0)
         c.lens[b] = len - (cols - to) * c.bs;
 }

@@ -655,7 +655,9 @@ nsa_status nsa_cache_accept(const nsa_cache *c, const int32_t *n_new, const int3
  * are placed behind the shorter row.  kept ([rows, max_pages] int32, or
  * NULL): the column that each column was before.  A row whose length the table
  * cannot hold, or one of whose blocks has no page in use, is reported
- * (NSA_ERR_BAD_INDEX) and left.  Needs page_table, seq_lens and refcount; ws: 256 bytes.
+ * (NSA_ERR_BAD_INDEX) and left; a page that is dropped more often than its count
+ * says is reported too, and its count ends at 0.  Needs page_table, seq_lens and
+ * refcount; ws: 256 bytes.
  */
 nsa_status nsa_cache_weigh(const nsa_problem *p, const nsa_cache *c, int32_t window, const int32_t *cu_seqlens,
                            const void *q, const float *lse, float decay, float *weight, void *ws, size_t ws_bytes,

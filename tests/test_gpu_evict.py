@@ -484,6 +484,28 @@ def test_evict_bad_rows_are_left_and_reported():
         assert kept[0].tolist() == list(range(9)) and cache.seq_lens[1] == 64
 
 
+def test_evict_counts_too_low_are_reported():
+    """A page that two rows name and whose count is 1: both rows close up, the count ends at 0, not below, and that is
+    reported; counts that are right are not."""
+    for count in (1, 2):
+        cache = filled([16 * 9, 16 * 9], 2, 32, 16, 1)
+        page = int(cache.page_table[0, 3])
+        spare = int(cache.page_table[1, 3])
+        cache.page_table[1, 3] = page
+        cache.refcount[spare] = 0
+        cache.refcount[page] = count
+        weight = torch.rand(2, 2, 9, device=DEV)
+        weight[:, :, 3] = 0.0
+        api.cache_evict(cache, weight, 8)
+        # (one row may meet the count that the other has taken: it is then left, and the page is its own again in no table)
+        left = [b for b in range(2) if int(cache.seq_lens[b]) == 16 * 9]
+        assert api.get_error(cache.ws) == (3 if count == 1 else 0)
+        assert len(left) == 0 if count == 2 else len(left) <= 1
+        assert int(cache.refcount[page]) == 0 and int(cache.refcount.min()) == 0
+        for b in range(2):
+            assert (page in cache.page_table[b].tolist()) == (b in left)
+
+
 def test_evict_in_a_graph_and_repeats():
     cache = filled([16 * 40, 16 * 30], 2, 32, 16, 1)
     table, lens, ref = cache.page_table.clone(), cache.seq_lens.clone(), cache.refcount.clone()
