@@ -246,7 +246,7 @@ cudaError_t launch_cache_evict(const Cache &c, float *weight, int keep, int firs
     EvictArgs a = {c, weight, kept, keep, first, recent, err, c.cols <= kMaxKeys};
     const size_t smem = a.in_smem ? sizeof(uint32_t) * (size_t)c.cols : 0;
     if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaError_t e = allow_shared((const void *)evict_kernel);
         if (e != cudaSuccess)
             return e;
     }

@@ -32,6 +32,34 @@ int num_sms()
     return cached[dev];
 }
 
+cudaError_t allow_shared(const void *kernel)
+{
+    struct Allowed {
+        const void *kernel;
+        int dev;
+    };
+    constexpr int kMost = 1024;  // (kernels times devices; beyond, each call allows the same once more)
+    static Allowed list[kMost];
+    static int n = 0;
+    static std::mutex mu;
+    int dev = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    std::lock_guard<std::mutex> lk(mu);
+    for (int i = 0; i < n; ++i)
+        if (list[i].kernel == kernel && list[i].dev == dev)
+            return cudaSuccess;
+    cudaFuncAttributes attr;
+    if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess ||
+        (e = cudaFuncGetAttributes(&attr, kernel)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)attr.sharedSizeBytes)) != cudaSuccess)
+        return e;
+    if (n < kMost)
+        list[n++] = {kernel, dev};
+    return cudaSuccess;
+}
+
 namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn()

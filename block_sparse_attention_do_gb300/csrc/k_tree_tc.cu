@@ -981,7 +981,7 @@ template <int D> cudaError_t tree_chunk_t(const Params &p, cudaStream_t st)
 {
     void (*const kernels[3])(const Params) = {tree_chunk_kernel<D, 16>, tree_chunk_kernel<D, 32>, tree_chunk_kernel<D, 64>};
     auto kernel = kernels[p.c.bsh - 4];
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
+    cudaError_t e = allow_shared((const void *)kernel);
     if (e != cudaSuccess || (e = launch_dependent(kernel, dim3((unsigned)p.ctas), dim3(kThreads), Layout<D>::total, st, p)) != cudaSuccess)
         return e;
     return launch_dependent(tree_join_kernel<D>, dim3((unsigned)p.ctas, kTileRows / kJoinWarps), dim3(kJoinWarps * 32), 0, st, p);

@@ -357,7 +357,7 @@ template <typename T, int D> cudaError_t weigh_t(const WeighArgs &a, cudaStream_
 {
     auto kernel = longest_rows(a.g) <= 8 ? weigh_kernel<T, D, true> : weigh_kernel<T, D, false>;
     const size_t smem = sizeof(Smem<D, sizeof(T) == 4>) + sizeof(int) * (size_t)(a.g.B + 1);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_shared((const void *)kernel);
     if (e != cudaSuccess)
         return e;
     return launch_dependent(kernel, dim3((unsigned)(num_sms() * kCtas)), dim3(kThreads), smem, st, a);

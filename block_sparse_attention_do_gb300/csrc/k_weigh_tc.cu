@@ -414,7 +414,7 @@ template <int D> __global__ void __launch_bounds__(kThreads, kCtas) weigh_tc_ker
 
 template <int D> cudaError_t weigh_tc_t(const CUtensorMap &tm, const Params &p, cudaStream_t st)
 {
-    cudaError_t e = cudaFuncSetAttribute(weigh_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout<D>::total);
+    cudaError_t e = allow_shared((const void *)weigh_tc_kernel<D>);
     if (e != cudaSuccess)
         return e;
     return launch_dependent(weigh_tc_kernel<D>, dim3((unsigned)(num_sms() * kCtas)), dim3(kThreads), Layout<D>::total, st, tm, p);

@@ -72,6 +72,11 @@ inline bool rows_map_form(const Geo &g, int H, const Strides &s, int &bt)
 // the host launcher's view of the device: SM count (cached)
 int num_sms();
 
+// Allows launches of `kernel` all the dynamic shared memory that it can have on
+// the current device, once.  What is allowed is the process's: were it a call's
+// own size, another thread's smaller call could lower it in front of the launch.
+cudaError_t allow_shared(const void *kernel);
+
 // Launches kernel as a programmatic dependent of the previous kernel on st:
 // it may start before that kernel completes (once that kernel's CTAs have
 // executed griddepcontrol.launch_dependents and resources free up), so it

@@ -564,3 +564,55 @@ def test_a_bounded_row_as_a_server_keeps_it():
             assert len(held[b]) == int(cache.seq_lens[b]) and held[b][:bs] == list(range(bs)) and held[b][-1] == done + n - 1
         assert int((cache.refcount > 0).sum()) == sum(-(-int(x) // bs) for x in cache.seq_lens)
         done += n
+
+
+def at_once(*calls, times=3000):
+    """Each call of the C entries over and over in threads and streams of its own; the states that were not 0."""
+    import threading
+    got = set()
+    start = threading.Barrier(2 * len(calls))
+    streams = [torch.cuda.Stream() for _ in range(2 * len(calls))]
+    torch.cuda.synchronize()
+
+    def run(make, stream):
+        call, args = make(stream)
+        torch.cuda.synchronize()
+        start.wait()
+        for _ in range(times):
+            s = call(*args)
+            if s:
+                got.add(s)
+
+    threads = [threading.Thread(target=run, args=(calls[i // 2], stream)) for i, stream in enumerate(streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return got
+
+
+def test_calls_of_several_threads_with_other_amounts_of_shared_memory():
+    """What a kernel is allowed is the process's: a call that needs little takes nothing from one that needs much."""
+    held = []
+
+    def weigher(rows):
+        def make(stream):
+            cache = filled([20] * rows, 1, 128, 64, 1)
+            q = torch.zeros(rows, 1, 1, 128, device=DEV)
+            lse, weight = torch.zeros(rows, 1, 1, device=DEV), torch.zeros(rows, 1, cache.page_table.shape[1], device=DEV)
+            held.append((cache, q, lse, weight))
+            p = cache.problem(q, 1, None, None, None, False, True)[1]
+            return api.lib().nsa_cache_weigh, (p, cache.ref, 0, None, q.data_ptr(), lse.data_ptr(), 1.0, weight.data_ptr(), None, 0, stream.cuda_stream)
+        return make
+
+    def evicter(cols):
+        def make(stream):
+            cache = filled([20], 1, 32, 16, 1, cols=cols)
+            weight = torch.zeros(1, 1, cols, device=DEV)
+            held.append((cache, weight))
+            return api.lib().nsa_cache_evict, (cache.ref, weight.data_ptr(), 8, 0, 1, None, cache.ws.data_ptr(), cache.ws.numel(), stream.cuda_stream)
+        return make
+
+    assert at_once(weigher(1), weigher(2048)) == set()
+    assert at_once(evicter(11000), evicter(48000)) == set()
