@@ -1358,7 +1358,7 @@ template <typename K> bool smem_ok(K kernel, size_t bytes)
 {
     if (bytes > (size_t)kSmemLimit)
         return false;
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) == cudaSuccess;
+    return allow_shared((const void *)kernel) == cudaSuccess;
 }
 
 size_t union_bytes(const Geo &g) { return union_buf(g).bytes; }

@@ -835,8 +835,11 @@ cudaError_t launch_qtile_unions(const Geo &g, const int *idx, int *utable, cudaS
     if (grid < 1)
         return cudaSuccess;
     const size_t smem = (size_t)8 * up.bytes;
-    if (smem > 48 * 1024)
-        cudaFuncSetAttribute(qtile_union_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = allow_shared((const void *)qtile_union_kernel);
+        if (e != cudaSuccess)
+            return e;
+    }
     return launch_dependent(qtile_union_kernel, dim3(grid), dim3(256), smem, st, g, idx, ntiles, up, utable);
 }
 
@@ -890,7 +893,9 @@ cudaError_t launch_dq_tc(const Geo &g, const void *q, const void *k, const void 
     if (grid < 1)
         return cudaSuccess;
     auto kernel = grouped && utable ? dq_tc_kernel<true> : dq_tc_kernel<false>;
-    cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_shared((const void *)kernel);
+    if (e != cudaSuccess)
+        return e;
     // a programmatic dependent of the kernel before it on the stream (the dK/dV
     // kernel, whose outputs it does not read): its CTAs start as that kernel's
     // CTAs end; everything it reads was written by earlier, completed launches

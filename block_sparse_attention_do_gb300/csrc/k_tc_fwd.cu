@@ -616,7 +616,9 @@ cudaError_t launch_fwd_tc(const Geo &g, const void *q, const void *k, const void
     if (grid < 1)
         return cudaSuccess;
     auto fwd_tc = grouped && utable ? fwd_tc_kernel<true> : fwd_tc_kernel<false>;
-    cudaFuncSetAttribute(fwd_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    const cudaError_t e = allow_shared((const void *)fwd_tc);
+    if (e != cudaSuccess)
+        return e;
     // After the index validation, a programmatic dependent of it (the check
     // only reports errors; this kernel skips invalid entries by itself).
     if (after_kernel)

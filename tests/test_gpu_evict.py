@@ -616,3 +616,28 @@ def test_calls_of_several_threads_with_other_amounts_of_shared_memory():
 
     assert at_once(weigher(1), weigher(2048)) == set()
     assert at_once(evicter(11000), evicter(48000)) == set()
+
+
+@pytest.mark.parametrize("D,bs,dtype,Hq", [(64, 16, F32, 2), (64, 16, BF, 2), (128, 64, BF, 8)])
+def test_training_calls_of_several_threads_with_other_amounts_of_shared_memory(D, bs, dtype, Hq):
+    """The same of the kernels whose shared memory goes by the longest sequence's blocks: forward and backward."""
+    held = []
+
+    def step(T, backward):
+        def make(stream):
+            q, o, dq = (torch.zeros(1, Hq, T, D, dtype=dtype, device=DEV) for _ in range(3))
+            k, dk, dv = (torch.zeros(1, 1, T, D, dtype=dtype, device=DEV) for _ in range(3))
+            idx = torch.zeros(1, 1, T, 1, dtype=torch.int32, device=DEV)
+            lse = torch.zeros(1, Hq, T, device=DEV)
+            p = api.problem_from(q, k, bs, 1)
+            n = api.bwd_workspace_size(p) if backward else api.fwd_workspace_size(p)
+            ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+            held.append((q, o, dq, k, dk, dv, idx, lse, p, ws))
+            at = [x.data_ptr() for x in (q, k, k, o, o, lse, idx, dq, dk, dv)]
+            if backward:
+                return api.lib().nsa_sel_bwd, (p, *at, ws.data_ptr(), n, stream.cuda_stream)
+            return api.lib().nsa_sel_fwd, (p, at[0], at[1], at[2], at[6], at[3], at[5], ws.data_ptr(), n, stream.cuda_stream)
+        return make
+
+    for backward in (False, True):
+        assert at_once(step(64, backward), step(8192, backward), times=400) == set(), backward
