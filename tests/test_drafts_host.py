@@ -114,3 +114,39 @@ def test_tensors_are_checked():
         with pytest.raises(api.NsaError):
             api._weights(c, w)
     api._weights(c, torch.zeros(3, 2, 4))
+
+
+# what a kernel's arguments point to, and the helpers that read it
+_GLOBAL = re.compile(r"\b(lens|cu|table|ref|ks|vs|weight|kept|path|n_new|pos|freq|qw|kw|part|part_\w+|cuts|err|lse|parents|sinks|idx|q|k|qr|kr|r0|r1)\b"
+                     r"|\b\w+(_tokens|_of|_off|_at|_len|_prefix)\(")
+
+
+def _early_reads(source):
+    """{kernel: what it reads in front of its wait} of a file's kernels; shared memory's declarations and places in it are none."""
+    text = re.sub(r"//[^\n]*|L::\w+|[^\n]*__shared__[^\n]*;", "", source)
+    found = {}
+    for part in text.split("__global__")[1:]:
+        name = re.search(r"\b(\w+_kernel)\(", part).group(1)
+        body = part[part.index("\n{"):part.index("\n}")]
+        assert "dependency_wait();" in body, name
+        found[name] = [m.group(0) for m in _GLOBAL.finditer(body[:body.index("dependency_wait();")])]
+    return found
+
+
+def test_no_kernel_reads_in_front_of_its_wait():
+    """The kernels beside the cache's own may start while the launches before them still run.  The check finds a read that is
+    spliced in front of the wait, however it is written."""
+    csrc = os.path.join(os.path.dirname(api.__file__), "csrc")
+    seen = set()
+    for name in ("k_accept.cu", "k_weigh.cu", "k_weigh_tc.cu", "k_tree_tc.cu", "k_evict.cu", "k_norm_rope.cu"):
+        source = open(os.path.join(csrc, name)).read()
+        kernels = _early_reads(source)
+        assert not any(kernels.values()), (name, kernels)
+        seen |= set(kernels)
+        for read in ("int x = a.c.lens[0];", "int x = g.cu[b + 1];", "int x = a.pos[tok];", "int x = c.table[(int64_t)b * c.cols];", "float x = *lse;",
+                     "int x = new_tokens(g, b);", "*err = 0;", "int x = p.parents[t];", "uint4 x = *(const uint4 *)(a.q + 1);", "int x = ws.r0[b];",
+                     "int x = ref[0];", "float x = part[i];"):
+            spliced = source.replace("dependency_wait();", read + "\n    dependency_wait();")
+            planted = _early_reads(spliced)
+            assert set(planted) == set(kernels) and all(planted.values()), (name, read, planted)
+    assert len(seen) == 11, seen
