@@ -1006,9 +1006,9 @@ def _weights(cache, weight):
 
 def cache_weigh(q, lse, cache, weight, decay=1.0, scale=None, cu_seqlens=None, max_seqlen=None, window=None, ws=None, stream=None):
     """What the queries of a cache_fwd call (q, its lse, scale, window and
-    offsets) gave each block of their rows, summed over tokens and a kv
-    head's query heads, is added to weight (float32 [rows, Hkv, max_pages],
-    in place) times decay.  The error word that get_error reads is
+    offsets; no block_idx, and no tree's) gave each block of their rows,
+    summed over tokens and a kv head's query heads, is added to weight
+    (float32 [rows, Hkv, max_pages], in place) times decay.  The error word that get_error reads is
     cache.weigh_ws: ws, the caller's 256 bytes, or the call's own."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):

@@ -13,10 +13,11 @@
 // What bounds it: the bytes, each read or written once.  A warp takes one
 // token's heads, 16 bytes per lane and head, the next loads under way while it
 // computes, over the end of a token too; the token's angles are computed once, a
-// lane each, and shared through shared memory.  Measured: 12,573 packed tokens of
-// 40 heads of 128 in bf16, 257 MB, 47 us, 5.5 TB/s (81% of a plain copy's rate);
-// gradients of 8192 tokens of 34 heads, 214 MB, 43 us, 5.0 TB/s; one token 2 us
-// and the launch.  Loads into registers, two under way within a token: 51 and 52.
+// lane each, and shared through shared memory.  Measured, without the 4 us of a launch
+// from a graph: 12,572 packed tokens of 40 heads of 128 in bf16, 258 MB, 47 us, 5.4 TB/s (80%
+// of a plain copy's rate); gradients of 8192 tokens of 34 heads, 214 MB, 43 us, 5.0 TB/s;
+// the latter's forward and gradients in fp32, 285 MB, 48 us, and 428 MB, 72 us, 5.9 TB/s; one
+// token 2 us.  Loads into registers, two under way within a token: 51 and 52.
 // Rings of 2, 3, 4, 5, 6, 8 vectors: 51, 47, 47, 48, 49, 50 and 47, 43, 43, 43, 43,
 // 44 us; 2 or 4 CTAs an SM instead of 3: 57 and 60, 1 or 3 instead of 2: 56 and 61
 // (registers spill).  A CTA's angles shared by its four tokens' warps behind a
@@ -68,8 +69,9 @@ __device__ __forceinline__ uint64_t turns_of(float f)
 
 // cos and sin of pos * f, f given by turns_of.  A float product would leave a far
 // position's angle no digits (position 10^6: 0.03 radians off); modulo 2^64 the
-// product drops whole turns exactly.  It is off by at most pos f 2^-64 turns, and
-// the 32 bits that are kept by 2^-26 once a float.
+// product drops whole turns exactly.  turns_of is off by its truncation, one 2^-64 turn,
+// and f times the rounding of 2^64 / 2 pi: the product by at most |pos| (1 + f) 2^-64
+// turns, 2^-32 for f up to 1, and the 32 bits that are kept by 2^-26 once a float.
 __device__ __forceinline__ float2 cos_sin(int pos, uint64_t per)
 {
     const int turns = (int)((uint64_t)(int64_t)pos * per >> 32);  // of 2^-32, -1/2 .. 1/2

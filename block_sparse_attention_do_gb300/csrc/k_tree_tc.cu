@@ -12,6 +12,9 @@
 //     joined by a second kernel, in the order of the CTAs;
 //   - a unit of at most 128 rows has its key tiles taken in turn by both row tiles'
 //     pipelines, over the same queries; the two sums are joined in shared memory.
+// Weights go to the products as halves there and here, 11 bits, three more than the
+// outputs have: these are 1.7e-3 from 64 bits, as they are with weights in 32 bits, and
+// 8.5e-4 from those, where a rounding to bf16 falls to the other side.
 #include <math.h>
 
 #include "cache_common.cuh"
@@ -395,7 +398,7 @@ template <int D, int BS> __global__ void __launch_bounds__(kThreads, 1) tree_chu
             const int step = u.two ? 1 : 2;
             for (int i = step == 1 ? 0 : q; i < ntiles && ok; i += step) {
                 const int j = j_first + i;
-                                if (!mbar_wait_warp(&bars[B_SF + q], mine & 1, ctx)) {
+                if (!mbar_wait_warp(&bars[B_SF + q], mine & 1, ctx)) {
                     ok = false;
                     break;
                 }
@@ -992,10 +995,16 @@ template <int D> cudaError_t tree_chunk_t(const Params &p, cudaStream_t st)
 // Where this kernel takes over from k_tree.cu's, whose time goes by 32-row tiles of
 // every key: about 14 us and 0.075 for a thousand keys of a kv head and tile, against
 // 25 and 0.1 for a thousand keys here (D = 128, 8 kv heads of 4 query heads; one
-// sequence of 2048 tokens with 24 and 64 drafts 19 and 23 us there, 28 and 33 here; of
+// sequence of 2048 tokens with 24 and 64 drafts 19 and 24 us there, 28 and 33 here; of
 // 8192 31 and 53 us there, 31 and 37 here; 4 of 8192 with 12 and 24 drafts 51 and 70
 // us there, 49 and 50 here; 8 of 512 with 12 drafts 17 there, 31 here).  The lengths
-// are the device's: the table's width stands for them.
+// are the device's: the table's width stands for them.  Where it is wider than its
+// rows, k_tree.cu's clusters are not to be had either (they go by the width too), and
+// its list is what there is: in a table of 131,072 tokens, one row of 2048 with 12, 24 and
+// 64 drafts 21, 25 and 31 us there, 27, 27 and 31 here; of 8192 27, 35 and 56 there, 31,
+// 31 and 37 here; of 32,768 51, 69 and 140 there, 43, 46 and 58 here; 8 rows of 512 and
+// of 2048 with 24 drafts 38 and 56 there, 31 and 45 here.  So at most 6 us are lost
+// to the width, on few drafts behind short rows.
 bool tree_chunk_supported(const Geo &g, const Cache &c, int dtype, bool sel)
 {
     const int64_t rows = longest_rows(g), heads = (int64_t)g.B * g.Hkv, keys = (int64_t)c.cols * c.bs;

@@ -6,7 +6,8 @@
 //   weight[b, g, j] = decay * weight[b, g, j] + sum exp(scale ks <q, ck_k> - LSE)
 // with the LSE that the attention gave (a block that begins with new tokens had
 // nothing).  The products are k_cache_attn.cu's: codes exact in half, queries
-// scaled per row by a power of two (fp32: two halves), fp32 sums.
+// scaled per row by a power of two (fp32: two halves, 22 bits: a score is then off by
+// 2^-22 of its magnitudes' sum, of the size of its D roundings in fp32), fp32 sums.
 //
 // What bounds it: for single tokens the key codes, each read once.  As there, the
 // call's keys of all rows, in groups of 64, are one list that is cut into equal
@@ -15,8 +16,9 @@
 // nothing is joined.  More query rows than fit shared memory pass through it 64
 // at a time, over the listed groups each time (fp32, and few rows: many in bf16 are
 // k_weigh_tc.cu's).  Measured, D = 128, 8 kv heads of 4 query heads: 32 rows of 128 ..
-// 32768 tokens, 0.52 GB of codes, 90 us, 5.8 TB/s (86% of a plain copy's rate); 4 tokens
-// behind one row of 8192, 7 us and the launch.  Loads into registers, a page at a time: 140.
+// 32768 tokens, 0.52 GB of codes, 91 us and the launch, 5.8 TB/s (85% of a plain copy's rate;
+// fp32 queries 1 to 4% longer); 4 tokens behind one row of 8192, 7 us and the launch.
+// Loads into registers, a page at a time: 140.
 #include <math.h>
 
 #include "cache_common.cuh"

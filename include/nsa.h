@@ -424,7 +424,8 @@ nsa_status nsa_select_topk(const nsa_problem *p, const int32_t *cu_seqlens, cons
  *   z  = y with the pairs (y_a, y_b) of its first `rotary` elements turned:
  *        (y_a c - y_b s, y_b c + y_a s), c = cos(pos f_i), s = sin(pos f_i), pair i < rotary / 2 being elements
  *        (i, i + rotary / 2), or (2 i, 2 i + 1) with `interleaved`
- * Sums and norms are fp32; an angle's whole turns are dropped before it is
+ * Sums and norms are fp32 (so the square of an element, and of u x in the
+ * backward, has to stay in its range: |x| below 10^18); an angle's whole turns are dropped before it is
  * rounded, so that cos and sin are good to 2^-22 at any int32 position
  * (frequencies up to 1).  nsa_norm_rope_fwd writes z, nsa_norm_rope_bwd takes its
  * gradients dqr, dkr and the forward's q and k, and writes dq, dk and the
@@ -635,7 +636,8 @@ nsa_status nsa_cache_accept(const nsa_cache *c, const int32_t *n_new, const int3
  * its sinks); for the query tokens t and heads h of kv head g, and the keys k of
  * block j that they attend,
  *   weight[b, g, j] = decay * weight[b, g, j] + sum exp(scale q_th.k_k - lse_th)
- * for every block below row b's length, 0 <= decay <= 1; decay 0 reads no old
+ * (attention over an index or of a tree has other keys: its LSE is not one to give
+ * here) for every block below row b's length, 0 <= decay <= 1; decay 0 reads no old
  * weight, and a block that begins with new tokens has none.  Rows without query
  * tokens, and blocks behind a row's length, are left as they were.  A query whose
  * LSE is -inf attends nothing.  A page that is none is reported and counts as
