@@ -948,6 +948,8 @@ def _cache_fwd(q, cache, parents, block_idx, scale, cu_seqlens, max_seqlen, wind
     if parents is not None:
         _int32(parents, "cache_tree_fwd: parents", dev, (q.shape[0],) if cu_seqlens is not None else (q.shape[0], q.shape[2]))
     if q.numel() == 0:
+        if ws is None and parents is not None:
+            ws = torch.empty(256, dtype=torch.uint8, device=dev)
         cache.fwd_ws = ws
         if ws is not None:
             ws[:4].zero_()
@@ -955,7 +957,7 @@ def _cache_fwd(q, cache, parents, block_idx, scale, cu_seqlens, max_seqlen, wind
     _, p, n, stats, dense = cache.problem(q, S, scale, cu_seqlens, longest, block_idx is not None, True, parents is not None)
     o = torch.empty_like(q) if dense else torch.empty(q.shape, dtype=q.dtype, device=dev)
     lse = torch.empty(stats, dtype=torch.float32, device=dev)
-    if ws is None and n > 256:
+    if ws is None and (n > 256 or parents is not None):  # (a parent that is none would be taken as -1 and nobody hear of it)
         ws = torch.empty(n, dtype=torch.uint8, device=dev)
     cache.fwd_ws = ws
     at, size = (None, 0) if ws is None else (ws.data_ptr(), ws.numel())
@@ -976,7 +978,9 @@ def cache_tree_fwd(q, cache, parents, block_idx=None, scale=None, cu_seqlens=Non
     """cache_fwd for a tree of drafts: parents (int32 [rows, T], or packed
     [total]) names the draft that each of the new tokens continues, -1: what
     was cached before them.  A draft attends that, its ancestors and itself,
-    at the position that its depth gives it.  At most 256 drafts a row."""
+    at the position that its depth gives it.  At most 256 drafts a row.
+    get_error(cache.fwd_ws) reads what the call found, with or without a ws
+    of the caller's."""
     if _elsewhere(cache, stream):
         with _there(cache, stream):
             return cache_tree_fwd(q, cache, parents, block_idx, scale, cu_seqlens, max_seqlen, window, sinks, ws)

@@ -281,6 +281,37 @@ def test_bad_parents_are_reported_and_taken_as_roots():
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("n,T,cols,form", [(2, 6, None, "cache_tree_cluster"), (2, 6, 2000, "cache_tree_chunk"), (24, 60, None, "cache_tree_cluster"),
+                                           (2, 3, 2000, "cache_tree")])
+def test_trees_report_without_a_workspace_of_the_callers(n, T, cols, form):
+    """Parents that are none, in each form, through the handle; and nothing where all is well."""
+    cache = filled([200] * n, 2, 128, 64, 5, cols=cols)
+    q = torch.randn(n, 16, T, 128, device=DEV).to(BF)
+    par = i32([list(range(-1, T - 1))] * n)
+    api.trace_enable(8)
+    api.trace_reset()
+    want = api.cache_tree_fwd(q, cache, par)
+    names = [x for x, _ in api.trace_records()]
+    api.trace_enable(0)
+    assert names == [form] and api.get_error(cache.fwd_ws) == 0
+    bad = par.clone()
+    bad[1, 0] = 7
+    got = api.cache_tree_fwd(q, cache, bad)
+    assert api.get_error(cache.fwd_ws) == 3
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        api.cache_tree_fwd(q, cache, par)
+    held = cache.fwd_ws
+    for x in (7, -1, 7):
+        par[1, 0] = x
+        graph.replay()
+        torch.cuda.synchronize()
+        assert api.get_error(held) == (3 if x == 7 else 0)
+    api.cache_tree_fwd(q[:, :, :0], cache, par[:, :0].contiguous())
+    assert api.get_error(cache.fwd_ws) == 0 and cache.fwd_ws is not held
+
+
 def test_packed_offsets_that_are_none():
     """Tokens in front of the first offset and behind the last stay as they were; a run that is none is reported."""
     cache = filled([100, 90, 80], 2, 64, 32, 5)
